@@ -77,6 +77,8 @@ typedef enum { PKV_OUT_BF16 = 0, PKV_OUT_FP32 = 1 } pkv_out_dtype;
 #define PKV_DEVFLAG_BAD_BLOCK_ID 0x4u    /* decode: block id outside the pool (read as zeros);
                                             copy: pair skipped */
 #define PKV_DEVFLAG_WAIT_TIMEOUT 0x8u    /* decode: a pipeline wait hit its iteration limit */
+#define PKV_DEVFLAG_BAD_INDPTR 0x10u     /* prefill, gather: an entry of the row offsets is negative,
+                                            decreasing or past the rows (that sequence is skipped) */
 
 /*
  * The caller-owned paged pool.  Nothing is copied; the struct is read during the call.
@@ -340,6 +342,118 @@ pkv_status pkv_paged_kv_checksum(const pkv_cache_desc* cache, const int32_t* blo
  * device, page-locked host nor managed memory (checked with the runtime's pointer query).
  */
 pkv_status pkv_stage_copy(void* dst, const void* src, size_t bytes, pkv_stream_t stream);
+
+/*
+ * The prompt side of the pool: a chunk of new tokens (a prompt, a part of one, or several
+ * speculated tokens) goes in through pkv_qk_norm_rope_append and is attended by
+ * pkv_paged_prefill_attention; pkv_paged_kv_gather reads cached positions back.
+ * (habr.com/ru/articles/1021832, section 1 "Prefill и Decode": the prompt's K, V are computed
+ * for all its tokens at once and kept, decode then appends one per step.)
+ *
+ * A chunk's q, k and v from the projection to the attention and the pool in one launch:
+ *   norm      per head row x of q (with q_weight) and of k (with k_weight):
+ *             y_i = x_i * w_i / sqrt(mean(x^2) + eps); a NULL weight leaves its rows as they are
+ *   rotation  of the first rotary_dim elements of every q and k head by position n: the pair
+ *             p at angle n * inv_freq[p] turns (a, b) into rope_scale * (a cos - b sin,
+ *             b cos + a sin); the pair is (p, p + rotary_dim / 2), or (2p, 2p + 1) when interleaved
+ *   write     q to q_out (bf16); k and v to the pool slots as pkv_paged_kv_append writes them
+ *             (v in a bf16 pool: a bit copy).
+ *   Arithmetic in fp32 (the angle in fp64), rounded once, at the write: to bf16, or for an E4M3
+ *   pool the fp32 value / scale to E4M3, saturated.
+ *   q [num_tokens][num_q_heads][head_dim], k and v [num_tokens][num_kv_heads][head_dim], bf16,
+ *     heads contiguous, tokens `stride` elements apart (a multiple of 8, at least a token's
+ *     elements): slices of one packed projection output qualify.  16-byte aligned.
+ *   positions: [num_tokens] int32; slot_mapping: [num_tokens] int64 as for the append: a
+ *     negative slot writes nothing to the pool (the token's q is still written), one past the
+ *     pool is skipped and sets PKV_DEVFLAG_BAD_SLOT; two tokens with one slot: unspecified which
+ *     lands.
+ *   inv_freq: [rotary_dim / 2] fp64, radians per position (scaling for long contexts is in
+ *     these values and rope_scale).  rotary_dim: a multiple of 16 in [0, head_dim]; 0 rotates
+ *     nothing, and positions and inv_freq may be NULL.
+ *   q_weight, k_weight: [head_dim] bf16, 16-byte aligned, or NULL.
+ *   q_out: may be q itself (same pointer and stride); any other overlap with the inputs is not
+ *     allowed (with q it is refused).
+ *   num_tokens == 0 is a no-op.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride; /* elements */
+  const int32_t* positions;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  int32_t num_q_heads;
+  int32_t rotary_dim;
+  int32_t interleaved; /* 0: half layout, 1: interleaved pairs */
+  float rope_scale;    /* multiplies cos and sin (1 for plain rotation) */
+  const double* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  void* q_out;
+  int64_t q_out_stride; /* elements */
+} pkv_rope_append_desc;
+
+pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_append_desc* desc,
+                                   pkv_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens per sequence over the paged cache, which already holds
+ * the chunk's own K and V (append first).
+ *   q: [total_q][num_q_heads][head_dim] bf16, 16-byte aligned, tokens q_stride elements apart
+ *     (a multiple of 8).  The rows of sequence b are q_indptr[b] .. q_indptr[b + 1] - 1.
+ *   q_indptr: [batch + 1] int32, q_indptr[0] = 0, not decreasing, at most total_q; a sequence may
+ *     have no rows.  Rows from q_indptr[batch] on are neither read into a result nor written.
+ *     A bad range sets PKV_DEVFLAG_BAD_INDPTR and that sequence is skipped.
+ *   block_tables, max_blocks_per_seq, context_lens, max_context_len, softmax_scale: as for the
+ *     decode; context_lens[b] counts the chunk's tokens when causal.
+ *   causal = 1: row i of a sequence with n rows and context c is at position c - n + i and
+ *     attends the keys up to and including its own; rows at negative positions see nothing.
+ *   causal = 0: every row attends all context_lens[b] keys (cross attention to states held in
+ *     pages).
+ *   Row with keys j: out = sum_j softmax_j(softmax_scale q . K_j) V_j (bf16, [total_q][num_q_heads]
+ *     [head_dim] contiguous, 16-byte aligned), lse = ln sum_j exp(softmax_scale q . K_j) (fp32
+ *     [total_q][num_q_heads], or NULL).  A row that sees no key: out 0, lse -inf.
+ *   What the pages hold past a context or at positions a row does not see does not reach that
+ *   row, NaN and infinities included.
+ *   num_q_heads / num_kv_heads in {1, 2, 4, 8}, head_dim 64 or 128, bf16 or E4M3 pools.
+ *   Arithmetic: tensor-core products with fp32 accumulation and fp32 softmax statistics; the
+ *   softmax weights enter the second product rounded to bf16 (bf16 pools) or fp16 (E4M3 pools);
+ *   q enters as it is (E4M3 pools: elements smaller than 2^-10 of their row's largest to within
+ *   2^-18 of it).  Deterministic for given sizes and values; PKV_SPLIT_TOKENS fixes the partition
+ *   length (rounded up to a multiple of 128).
+ *   workspace: pkv_prefill_workspace_size(...) bytes, 256-byte aligned, any contents, NULL when
+ *     0; not to be used by two calls that can run at the same time.
+ *   batch == 0 or total_q == 0 is a no-op.
+ */
+size_t pkv_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t max_context_len);
+
+pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* q, int64_t q_stride,
+                                       const int32_t* q_indptr, int32_t total_q, const int32_t* block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                       int32_t num_q_heads, int32_t max_context_len, int32_t causal,
+                                       float softmax_scale, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, pkv_stream_t stream);
+
+/*
+ * Read ranges of cached positions back into contiguous rows: row kv_indptr[b] + i of k_out and
+ * v_out ([num_rows][num_kv_heads][head_dim], bf16 or fp32, 16-byte aligned) becomes position
+ * starts[b] + i of sequence b, for i = 0 .. kv_indptr[b + 1] - kv_indptr[b] - 1.
+ *   bf16 pools: the elements; E4M3 pools: code * scale (an fp32 product, rounded once more for
+ *   bf16 output).
+ *   kv_indptr: [batch + 1] int32, not decreasing, at most num_rows.  Rows before kv_indptr[0]
+ *     or from kv_indptr[batch] on are left as they were.  A bad range sets PKV_DEVFLAG_BAD_INDPTR.
+ *   starts: [batch] int32, or NULL for 0.
+ *   A position outside [0, max_blocks_per_seq * 16) reads as zeros and sets
+ *   PKV_DEVFLAG_BAD_CONTEXT_LEN; a block id outside the pool reads as zeros and sets
+ *   PKV_DEVFLAG_BAD_BLOCK_ID.
+ *   batch == 0 or num_rows == 0 is a no-op.
+ */
+pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* kv_indptr, const int32_t* starts, int32_t batch, int64_t num_rows,
+                               void* k_out, void* v_out, pkv_out_dtype out_dtype, pkv_stream_t stream);
 
 /*
  * Read and clear the device status word of the current device after the work queued on

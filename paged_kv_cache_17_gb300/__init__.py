@@ -39,13 +39,15 @@ DEVFLAG_BAD_SLOT = 0x1
 DEVFLAG_BAD_CONTEXT_LEN = 0x2
 DEVFLAG_BAD_BLOCK_ID = 0x4
 DEVFLAG_WAIT_TIMEOUT = 0x8
+DEVFLAG_BAD_INDPTR = 0x10
 
 EXPORTED_SYMBOLS = (
     "pkv_paged_kv_append", "pkv_decode_workspace_size",
     "pkv_decode_partition_tokens", "pkv_paged_decode_attention", "pkv_check_device_status",
     "pkv_status_string", "pkv_last_error", "pkv_version", "pkv_paged_decode_attention_noalloc",
     "pkv_copy_blocks", "pkv_cascade_workspace_size", "pkv_cascade_decode_attention", "pkv_paged_kv_checksum",
-    "pkv_paged_append_decode", "pkv_stage_copy",
+    "pkv_paged_append_decode", "pkv_stage_copy", "pkv_qk_norm_rope_append", "pkv_prefill_workspace_size",
+    "pkv_paged_prefill_attention", "pkv_paged_kv_gather",
 )
 
 
@@ -402,3 +404,8 @@ def check_device_status(stream: Optional[torch.cuda.Stream] = None) -> int:
 
 def version() -> int:
     return int(lib.pkv_version())
+
+
+# the prompt side: norm + rotation + append, chunk attention, reading pages back
+from .prompt import (paged_kv_gather, paged_prefill_attention, prefill_workspace_size,  # noqa: E402,F401
+                     qk_norm_rope_append, rope_inv_freq)

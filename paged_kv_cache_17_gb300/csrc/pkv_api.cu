@@ -16,6 +16,7 @@
 #include "../../include/pkv.h"
 #include "cascade.cuh"
 #include "decode_launch.cuh"
+#include "prompt.cuh"
 
 namespace {
 
@@ -907,6 +908,322 @@ pkv_status pkv_check_device_status(pkv_stream_t stream, uint32_t* flags) {
     if (e != cudaSuccess) return cuda_fail(e, "clearing the device status word");
     return fail(PKV_ERR_DEVICE_CHECK, "device-side check failed (flags 0x%x)", host);
   }
+  return PKV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the prompt side
+
+namespace {
+
+// Query rows of a chunk (tokens x the heads of a group) per sequence, and how the chunk
+// attention is laid out over the SMs (one CTA each).
+//   wide: 256-row CTAs when a sequence has more than 128 rows on average.
+//   splits: the context is cut into runs of whole 128-key steps when the tiles alone leave SMs
+//   idle; the count minimises  waves x (steps per CTA x step time + CTA start and end)  plus, when
+//   there is more than one, writing and reading the records.  PKV_SPLIT_TOKENS fixes the run.
+struct PrefillPlan {
+  bool wide;
+  int tile_slots, splits, split_tiles;
+  size_t ml_bytes, ws_bytes;
+};
+
+constexpr double kPrefillStepUs[2] = {0.75, 1.15};  // a narrow / wide step of 128 keys
+constexpr double kPrefillCtaUs = 4.0;               // a CTA's start and end
+constexpr double kPrefillMergeUs = 4.0;             // the merge kernel's launch
+constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
+constexpr long long kPrefillMaxRecords = 1LL << 20;
+
+PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max_context_len, int sm_count) {
+  const int g = hq / hkv;
+  PrefillPlan pp{};
+  pp.wide = static_cast<long long>(total_q) * g > 128LL * batch;
+  const int cta_tok = (pp.wide ? 256 : 128) / g;
+  const long long seqs = std::min(batch, total_q);
+  pp.tile_slots = static_cast<int>((total_q + seqs * (cta_tok - 1)) / cta_tok);
+  const long long tiles = std::max<long long>(seqs, (total_q + cta_tok - 1) / cta_tok);
+  const long long rows = static_cast<long long>(total_q) * hq;
+  const int steps = std::max(1, (max_context_len + 127) / 128);
+  pp.splits = 1;
+  pp.split_tiles = steps;
+  int forced = 0;
+  if (const char* env = std::getenv("PKV_SPLIT_TOKENS")) {
+    const long v = std::strtol(env, nullptr, 10);
+    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, steps));
+  }
+  if (forced > 0) {
+    pp.split_tiles = forced;
+    pp.splits = (steps + forced - 1) / forced;
+  } else {
+    double best = -1;
+    for (int n = 1; n <= std::min(steps, 64); ++n) {
+      const int run = (steps + n - 1) / n;
+      if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
+      if (n > 1 && rows * n > kPrefillMaxRecords) break;
+      const long long waves = (tiles * hkv * n + sm_count - 1) / sm_count;
+      double us = static_cast<double>(waves) * (run * kPrefillStepUs[pp.wide] + kPrefillCtaUs);
+      if (n > 1) us += kPrefillMergeUs + 2.0 * static_cast<double>(rows) * n * (d + 2) * 4 / kPrefillRecordBytesPerUs;
+      if (best < 0 || us < best) {
+        best = us;
+        pp.split_tiles = run;
+        pp.splits = n;
+      }
+    }
+  }
+  if (pp.splits > 1) {
+    pp.ml_bytes = round256(static_cast<size_t>(rows) * pp.splits * 2 * sizeof(float));
+    pp.ws_bytes = pp.ml_bytes + round256(static_cast<size_t>(rows) * pp.splits * d * sizeof(float));
+  }
+  return pp;
+}
+
+// sizes both the call and its workspace query check
+pkv_status check_prefill_sizes(int32_t batch, int32_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t max_len) {
+  if (batch < 0 || batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch must be in [0, 65535]");
+  if (total_q < 0) return fail(PKV_ERR_INVALID_ARG, "total_q must be >= 0");
+  if (hkv <= 0 || hq <= 0 || hq % hkv != 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)", hq, hkv);
+  const int g = hq / hkv;
+  if (g != 1 && g != 2 && g != 4 && g != 8)
+    return fail(PKV_ERR_UNSUPPORTED, "query-group size %d not in {1, 2, 4, 8}", g);
+  if (d != 64 && d != 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
+  if (max_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len must be >= 0");
+  // CTAs of the attention (a slot per tile and kv head) and rows of the merge
+  if ((static_cast<long long>(total_q) + batch) * hkv > 0x7fffffffLL ||
+      static_cast<long long>(total_q) * hq > 8LL * 0x7fffffff)
+    return fail(PKV_ERR_UNSUPPORTED, "too many query tokens (%d) for %d heads", total_q, hq);
+  return PKV_OK;
+}
+
+// q [total_q][hq][D] as boxes of one tile: 64 columns x the G heads of a group x 128 / G tokens
+bool encode_q_map(CUtensorMap* tm, const void* q, int64_t q_stride, int total_q, int hq, int g, int d) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq),
+                              static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g), static_cast<cuuint32_t>(128 / g)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// a row of `heads` heads per token, `stride` elements apart: 16-byte pieces throughout
+pkv_status check_rows(const char* name, const void* x, int64_t stride, int64_t heads, int64_t d) {
+  if (!x) return fail(PKV_ERR_INVALID_ARG, "%s must be non-NULL", name);
+  if (!aligned(x, 16)) return fail(PKV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < heads * d || stride % 8 != 0 || stride > (1LL << 38))
+    return fail(PKV_ERR_INVALID_ARG, "%s's token stride (%lld) must be a multiple of 8 and at least heads * head_dim",
+                name, static_cast<long long>(stride));
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t max_context_len) {
+  t_last_error.clear();
+  if (check_prefill_sizes(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK) return 0;
+  if (batch == 0 || total_q == 0) return 0;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != PKV_OK) return 0;
+  return plan_prefill(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_context_len, dev->sm_count).ws_bytes;
+}
+
+pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* q, int64_t q_stride,
+                                       const int32_t* q_indptr, int32_t total_q, const int32_t* block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                       int32_t num_q_heads, int32_t max_context_len, int32_t causal,
+                                       float softmax_scale, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if ((st = check_prefill_sizes(batch, total_q, num_q_heads, cache->num_kv_heads, cache->head_dim,
+                                max_context_len)) != PKV_OK)
+    return st;
+  if (batch == 0 || total_q == 0) return PKV_OK;
+  if ((st = check_rows("q", q, q_stride, num_q_heads, cache->head_dim)) != PKV_OK) return st;
+  if (!q_indptr || !block_tables || !context_lens || !out)
+    return fail(PKV_ERR_INVALID_ARG, "q_indptr, block_tables, context_lens and out must be non-NULL");
+  if (!aligned(out, 16)) return fail(PKV_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (!aligned(q_indptr, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(lse, 4))
+    return fail(PKV_ERR_INVALID_ARG, "q_indptr, block_tables, context_lens and lse must be 4-byte aligned");
+  if (max_blocks_per_seq <= 0) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * 16)
+    return fail(PKV_ERR_INVALID_ARG, "max_context_len %d exceeds max_blocks_per_seq * 16 = %lld", max_context_len,
+                static_cast<long long>(max_blocks_per_seq) * 16);
+  if (causal != 0 && causal != 1) return fail(PKV_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!std::isfinite(softmax_scale)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite");
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
+  const int d = cache->head_dim, hkv = cache->num_kv_heads, g = num_q_heads / hkv;
+  const PrefillPlan pp = plan_prefill(batch, total_q, num_q_heads, hkv, d, max_context_len, dev->sm_count);
+  if (pp.splits > 65535) return fail(PKV_ERR_UNSUPPORTED, "context too long for the partition grid");
+  if (pp.ws_bytes > 0) {
+    if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes required", pp.ws_bytes);
+    if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (workspace_bytes < pp.ws_bytes)
+      return fail(PKV_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", workspace_bytes, pp.ws_bytes);
+  }
+  // bf16: 64-column boxes for K and V; E4M3: K rows swizzled for the tensor cores, V rows as they
+  // are (its expansion reads them)
+  CUtensorMap tq{}, tk, tv;
+  const int64_t nb = cache->num_blocks;
+  const bool maps_ok = fp8 ? encode_kv_map_e4m3_swz(&tk, cache->k_cache, nb, hkv, d) &&
+                                 encode_kv_map(&tv, cache->v_cache, nb, hkv, d, true)
+                           : encode_q_map(&tq, q, q_stride, total_q, num_q_heads, g, d) &&
+                                 encode_kv_map_sw128(&tk, cache->k_cache, nb, hkv, d) &&
+                                 encode_kv_map_sw128(&tv, cache->v_cache, nb, hkv, d);
+  if (!maps_ok) return fail(PKV_ERR_INVALID_ARG, "cannot describe q or the KV pool as a TMA tensor map");
+
+  pkv::PrefillParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.q_indptr = q_indptr;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.scales = cache->scales;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  if (pp.splits > 1) {
+    p.part_ml = static_cast<float2*>(workspace);
+    p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
+  }
+  p.status = dev->status;
+  p.batch = batch;
+  p.total_q = total_q;
+  p.hq = num_q_heads;
+  p.hkv = hkv;
+  p.group = g;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = static_cast<int>(nb);
+  p.max_context_len = max_context_len;
+  p.causal = causal;
+  p.negate = softmax_scale < 0.f;
+  // a zero scale becomes a factor that leaves every score at 0 while masked ones stay -inf
+  p.score_scale = std::max(std::fabs(softmax_scale) * 1.4426950408889634f, 1e-37f);
+  p.splits = pp.splits;
+  p.split_tiles = pp.split_tiles;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_prefill(d, fp8, pp.wide, tq, tk, tv, p, pp.tile_slots, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+  if (pp.splits > 1) {
+    e = pkv::launch_merge_prefill(d, p, fp8, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "prefill merge launch");
+  }
+  return PKV_OK;
+}
+
+pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_append_desc* a, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (!a) return fail(PKV_ERR_INVALID_ARG, "descriptor is NULL");
+  const int d = cache->head_dim, hkv = cache->num_kv_heads, hq = a->num_q_heads;
+  if (a->num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (hq <= 0) return fail(PKV_ERR_INVALID_ARG, "num_q_heads must be positive");
+  if (hq > 4096 || hkv > 4096) return fail(PKV_ERR_UNSUPPORTED, "more than 4096 heads");
+  if (a->rotary_dim < 0 || a->rotary_dim > d || a->rotary_dim % 16 != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 in [0, head_dim] (got %d)", a->rotary_dim);
+  if (a->interleaved != 0 && a->interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (!std::isfinite(a->rope_scale)) return fail(PKV_ERR_INVALID_ARG, "rope_scale must be finite");
+  if ((a->q_weight || a->k_weight) && !(a->eps >= 0.f && std::isfinite(a->eps)))
+    return fail(PKV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (a->num_tokens == 0) return PKV_OK;
+  if ((st = check_rows("q", a->q, a->q_stride, hq, d)) != PKV_OK) return st;
+  if ((st = check_rows("k", a->k, a->k_stride, hkv, d)) != PKV_OK) return st;
+  if ((st = check_rows("v", a->v, a->v_stride, hkv, d)) != PKV_OK) return st;
+  if ((st = check_rows("q_out", a->q_out, a->q_out_stride, hq, d)) != PKV_OK) return st;
+  if (!a->slot_mapping || !aligned(a->slot_mapping, 8))
+    return fail(PKV_ERR_INVALID_ARG, "slot_mapping must be non-NULL and 8-byte aligned");
+  if (a->rotary_dim > 0 && (!a->positions || !aligned(a->positions, 4) || !a->inv_freq || !aligned(a->inv_freq, 8)))
+    return fail(PKV_ERR_INVALID_ARG, "a rotation needs positions (4-byte aligned) and inv_freq (8-byte aligned)");
+  if (!aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))
+    return fail(PKV_ERR_INVALID_ARG, "q_weight and k_weight must be 16-byte aligned");
+  const uintptr_t qi = reinterpret_cast<uintptr_t>(a->q), qo = reinterpret_cast<uintptr_t>(a->q_out);
+  const uintptr_t ilen = ((a->num_tokens - 1) * a->q_stride + static_cast<int64_t>(hq) * d) * 2;
+  const uintptr_t olen = ((a->num_tokens - 1) * a->q_out_stride + static_cast<int64_t>(hq) * d) * 2;
+  if (!(qi == qo && a->q_stride == a->q_out_stride) && qi < qo + olen && qo < qi + ilen)
+    return fail(PKV_ERR_INVALID_ARG, "q_out overlaps q (it may be q itself, with the same stride)");
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  pkv::RopeAppendParams p{};
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.v = static_cast<const uint16_t*>(a->v);
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.positions = a->positions;
+  p.slots = a->slot_mapping;
+  p.q_weight = static_cast<const uint16_t*>(a->q_weight);
+  p.k_weight = static_cast<const uint16_t*>(a->k_weight);
+  p.inv_freq = a->inv_freq;
+  p.q_out = static_cast<uint16_t*>(a->q_out);
+  p.q_out_stride = a->q_out_stride;
+  p.k_cache = static_cast<uint8_t*>(cache->k_cache);
+  p.v_cache = static_cast<uint8_t*>(cache->v_cache);
+  p.scales = cache->scales;
+  p.status = dev->status;
+  p.num_tokens = a->num_tokens;
+  p.pool_slots = cache->num_blocks * 16;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.rot = a->rotary_dim;
+  p.eps = a->eps;
+  p.rope_scale = a->rope_scale;
+  const cudaError_t e =
+      pkv::launch_qk_rope_append(d, cache->kv_dtype == PKV_KV_FP8_E4M3, a->interleaved != 0, p, dev->sm_count,
+                                 reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm-rope-append launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* kv_indptr, const int32_t* starts, int32_t batch, int64_t num_rows,
+                               void* k_out, void* v_out, pkv_out_dtype out_dtype, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (batch < 0 || batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch must be in [0, 65535]");
+  if (num_rows < 0 || num_rows > 0x7fffffffLL) return fail(PKV_ERR_INVALID_ARG, "num_rows must be in [0, 2^31)");
+  if (out_dtype != PKV_OUT_BF16 && out_dtype != PKV_OUT_FP32)
+    return fail(PKV_ERR_INVALID_ARG, "unknown out_dtype %d", static_cast<int>(out_dtype));
+  if (max_blocks_per_seq <= 0) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
+  if (cache->num_kv_heads > 4096) return fail(PKV_ERR_UNSUPPORTED, "more than 4096 heads");
+  if (batch == 0 || num_rows == 0) return PKV_OK;
+  if (!block_tables || !kv_indptr || !k_out || !v_out)
+    return fail(PKV_ERR_INVALID_ARG, "block_tables, kv_indptr, k_out and v_out must be non-NULL");
+  if (!aligned(block_tables, 4) || !aligned(kv_indptr, 4) || !aligned(starts, 4))
+    return fail(PKV_ERR_INVALID_ARG, "block_tables, kv_indptr and starts must be 4-byte aligned");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(PKV_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  pkv::GatherParams p{};
+  p.k_cache = static_cast<const uint8_t*>(cache->k_cache);
+  p.v_cache = static_cast<const uint8_t*>(cache->v_cache);
+  p.scales = cache->scales;
+  p.block_tables = block_tables;
+  p.kv_indptr = kv_indptr;
+  p.starts = starts;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.status = dev->status;
+  p.num_rows = num_rows;
+  p.num_blocks = cache->num_blocks;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.hkv = cache->num_kv_heads;
+  p.d = cache->head_dim;
+  const cudaError_t e = pkv::launch_kv_gather(cache->kv_dtype == PKV_KV_FP8_E4M3, out_dtype == PKV_OUT_FP32, p,
+                                              dev->sm_count, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gather launch");
   return PKV_OK;
 }
 

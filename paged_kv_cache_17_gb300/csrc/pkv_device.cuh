@@ -14,6 +14,7 @@
 #define PKV_DEVFLAG_BAD_CONTEXT_LEN 0x2u
 #define PKV_DEVFLAG_BAD_BLOCK_ID 0x4u
 #define PKV_DEVFLAG_WAIT_TIMEOUT 0x8u
+#define PKV_DEVFLAG_BAD_INDPTR 0x10u
 
 namespace pkv {
 

@@ -1,0 +1,304 @@
+"""Chunk attention over the paged cache against its definition in 64 bits: both pool types,
+head dims and query groups, lengths from none to long, ragged and odd, causal and not, split
+contexts, rows that see nothing, and pages holding NaN where nothing may be seen."""
+import math
+import os
+
+import pytest
+import torch
+
+from gpu_helpers import split_tokens
+from prompt_helpers import attention_64, attention_bounds, make_pool, offsets
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import paged_kv_cache_17_gb300 as m
+
+    return m
+
+
+def make(lens, ctx, hq, hkv, d, e4m3, seed, junk=float("nan"), extra=0, spread=1.0):
+    k, v, scales, tables = make_pool(ctx, hkv, d, e4m3, seed, junk=junk)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (torch.randn((sum(lens) + extra, hq, d), generator=g) * spread).to(torch.bfloat16).cuda()
+    return q, k, v, scales, tables
+
+
+def indptr(lens):
+    return torch.tensor(offsets(lens), dtype=torch.int32, device="cuda")
+
+
+def check(pkv, lens, ctx, hq, hkv, d, e4m3, causal=True, seed=0, scale=None, extra=0, split=None, spread=1.0, data=None,
+          max_len=None):
+    q, k, v, scales, tables = data or make(lens, ctx, hq, hkv, d, e4m3, seed, extra=extra, spread=spread)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    pkv.check_device_status()
+    with split_tokens(split):
+        pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, scale, out, causal=causal, lse=lse,
+                                    scales=scales, max_context_len=max_len)
+        flags = pkv.check_device_status()
+    assert flags == 0, hex(flags)
+    total = sum(lens)
+    ref, ref_lse, mag, size = attention_64(q[:total], lens, k, v, scales, tables, ctx, scale, causal)
+    bound, lse_bound = attention_bounds(ref, mag, size, q, e4m3, d)
+    got = out[:total].double()
+    if total:
+        both = torch.isnan(ref) & torch.isnan(got) | (torch.isinf(ref) & (got == ref))
+        off = torch.where(both, 0.0, (got - ref).abs() - torch.where(torch.isfinite(ref), bound, 0.0))
+        assert not torch.isnan(off).any(), "NaN where the definition has a value, or the reverse"
+        assert float(off.max()) <= 0, f"off by {float((got - ref).abs().max()):.3e}, {float(off.max()):.3e} past the bound"
+        empty = torch.isinf(ref_lse)
+        assert torch.equal(torch.isinf(lse[:total]) & (lse[:total] < 0), empty)
+        assert torch.equal(got[empty], torch.zeros_like(got[empty]))
+        dl = (lse[:total].double() - ref_lse).abs()[~empty]
+        far = float((dl - ref_lse[~empty].abs() * 2.0 ** -22).max()) if dl.numel() else 0.0
+        assert far <= lse_bound, f"lse off by {far:.3e} of {lse_bound:.3e}"
+    assert bool((out[total:] == 7.0).all()) and bool((lse[total:] == 7.0).all()), "rows behind the last sequence"
+    return out
+
+
+SHAPES = [(8, 8, 64), (8, 4, 128), (8, 2, 64), (16, 2, 128)]  # query groups 1, 2, 4, 8
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("lens,ctx", [
+    ([1], [1]),
+    ([1], [700]),
+    ([5, 0, 1, 17], [5, 33, 129, 400]),
+    ([300], [300]),
+    ([129, 64, 511], [257, 64, 1300]),
+])
+def test_matches_definition(pkv, lens, ctx, hq, hkv, d, e4m3):
+    check(pkv, lens, ctx, hq, hkv, d, e4m3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("lens,ctx", [([3, 40], [127, 1000]), ([200, 7, 333], [1500, 16, 128])])
+def test_not_causal(pkv, lens, ctx, hq, hkv, d, e4m3):
+    check(pkv, lens, ctx, hq, hkv, d, e4m3, causal=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [128, 256, 512])
+@pytest.mark.parametrize("lens,ctx", [([2, 9], [1300, 700]), ([600, 31], [900, 31])])
+def test_split_contexts(pkv, lens, ctx, split, e4m3):
+    check(pkv, lens, ctx, 8, 2, 128, e4m3, split=split)
+    check(pkv, lens, ctx, 8, 2, 64, e4m3, split=split, causal=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_that_see_nothing(pkv, e4m3):
+    # more query rows than context: the first rows are at negative positions
+    check(pkv, [40, 300], [17, 100], 8, 2, 128, e4m3)
+    check(pkv, [40, 300], [17, 100], 8, 2, 128, e4m3, split=128)
+    # contexts of length zero, causal and not
+    check(pkv, [4, 3], [0, 5], 8, 2, 64, e4m3)
+    check(pkv, [4, 300], [0, 0], 8, 2, 64, e4m3, causal=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_behind_the_last_sequence(pkv, e4m3):
+    check(pkv, [33, 20], [50, 20], 8, 2, 128, e4m3, extra=40)
+    check(pkv, [33, 20], [500, 200], 8, 2, 128, e4m3, extra=40, split=128)
+    check(pkv, [0, 0], [50, 20], 8, 2, 128, e4m3, extra=3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1.0])
+def test_scales(pkv, scale, e4m3):
+    check(pkv, [70, 3], [400, 200], 8, 2, 64, e4m3, scale=scale)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_growing_scores_rescale(pkv, e4m3):
+    """Keys whose scores grow along the context: the reference moves step after step."""
+    lens, ctx = [300, 2], [1500, 900]
+    data = list(make(lens, ctx, 8, 2, 128, e4m3, 5))
+    q, k, tables = data[0], data[1], data[4]
+    for b, c in enumerate(ctx):
+        for i in range((c + 15) // 16):
+            f = 0.02 * (1 + i)
+            blk = int(tables[b, i])
+            if e4m3:
+                k.view(torch.uint8)[blk] = (k[blk].float().nan_to_num(0) * f).clamp(-448, 448).to(
+                    torch.float8_e4m3fn).view(torch.uint8)
+            else:
+                k[blk] = k[blk].float().nan_to_num(0) * f
+    check(pkv, lens, ctx, 8, 2, 128, e4m3, data=data, scale=0.05)
+
+
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_values_not_finite_reach_only_rows_that_see_them(pkv, e4m3, split):
+    lens, ctx = [200, 3], [330, 300]
+    data = list(make(lens, ctx, 8, 2, 64, e4m3, 9))
+    v, tables = data[2], data[4]
+    for j, e, x in ((200, 3, math.nan), (317, 5, math.inf), (325, 5, -math.inf), (329, 60, math.nan)):
+        blk = int(tables[0, j // 16])
+        if e4m3:
+            v.view(torch.uint8)[blk, j % 16, 1, e] = 0x7F
+        else:
+            v[blk, j % 16, 1, e] = x
+    if e4m3:  # the only value that is not finite
+        check(pkv, lens, ctx, 8, 2, 64, e4m3, data=data, split=split)
+    else:
+        check(pkv, lens, ctx, 8, 2, 64, e4m3, data=data, split=split)
+
+
+def test_query_not_finite_stays_in_its_row(pkv):
+    for e4m3 in (False, True):
+        lens, ctx = [20], [150]
+        data = list(make(lens, ctx, 8, 2, 64, e4m3, 11))
+        data[0][4, 3, 7] = math.nan
+        q = data[0]
+        out = pkv.paged_prefill_attention(q, indptr(lens), data[1], data[2], data[4],
+                                          torch.tensor(ctx, dtype=torch.int32, device="cuda"), 0.125, scales=data[3])
+        bad = torch.isnan(out).all(-1)
+        want = torch.zeros_like(bad)
+        want[4, 3] = True
+        assert torch.equal(bad, want) and torch.equal(torch.isnan(out).any(-1), want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_small_queries_and_wide_ranges(pkv, e4m3):
+    """Rows of q whose elements differ by many powers of two, and tiny rows."""
+    lens, ctx = [64], [300]
+    data = list(make(lens, ctx, 8, 2, 128, e4m3, 13))
+    g = torch.Generator().manual_seed(3)
+    e = torch.randint(-20, 1, (64, 8, 128), generator=g).cuda()
+    data[0] = (data[0].float() * torch.pow(2.0, e.float())).to(torch.bfloat16)
+    data[0][10] *= 2.0 ** -100
+    data[0][11] = 0
+    check(pkv, lens, ctx, 8, 2, 128, e4m3, data=data)
+
+
+def test_long_context_long_offsets(pkv):
+    """A pool of more than 2^31 elements (bf16): row offsets pass 32 bits."""
+    hkv, d, blocks = 8, 128, (1 << 31) // (16 * 8 * 128) + 64
+    k = torch.zeros((blocks, 16, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.arange(blocks - 40, blocks, dtype=torch.int32, device="cuda")
+    k[-40:] = torch.randn((40, 16, hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    v[-40:] = torch.randn((40, 16, hkv, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    q = torch.randn((9, 32, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    data = (q, k, v, None, ids[None].contiguous())
+    check(pkv, [9], [637], 32, hkv, d, False, data=data)
+    ko = torch.empty((640, hkv, d), dtype=torch.bfloat16, device="cuda")
+    vo = torch.empty_like(ko)
+    pkv.paged_kv_gather(k, v, data[4], indptr([640]), ko, vo)
+    assert torch.equal(ko, k[-40:].flatten(0, 1)) and torch.equal(vo, v[-40:].flatten(0, 1))
+
+
+def test_strided_queries(pkv):
+    lens, ctx = [37, 90], [200, 90]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, False, 17)
+    packed = torch.randn((127, 12, 128), device="cuda").to(torch.bfloat16)
+    packed[:, :8] = q
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    a = pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, 0.1)
+    b = pkv.paged_prefill_attention(packed[:, :8], indptr(lens), k, v, tables, c, 0.1)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("split", [None, 256])
+def test_repeats_bit_for_bit_and_is_independent_of_batch_order(pkv, split):
+    lens, ctx = [100, 3, 260], [700, 513, 260]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, True, 21)
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    with split_tokens(split):
+        a = pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, 0.1, scales=scales)
+        b = pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, 0.1, scales=scales)
+        assert torch.equal(a, b)
+        at = offsets(lens)
+        order = [2, 0, 1]
+        q2 = torch.cat([q[at[i]:at[i + 1]] for i in order])
+        o2 = pkv.paged_prefill_attention(q2, indptr([lens[i] for i in order]), k, v, tables[order].contiguous(),
+                                         c[order].contiguous(), 0.1, scales=scales)
+    assert torch.equal(o2, torch.cat([a[at[i]:at[i + 1]] for i in order]))
+
+
+def test_bad_data_is_flagged_and_not_followed(pkv):
+    lens, ctx = [20, 30, 10], [100, 200, 60]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 64, False, 23, junk=0.0)
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+
+    def run(ip, t, cc):
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        pkv.check_device_status()
+        pkv.paged_prefill_attention(q, ip, k, v, t, cc, 0.125, out)
+        return out, pkv.check_device_status()
+
+    good, flags = run(indptr(lens), tables, c)
+    assert flags == 0
+    t = tables.clone()
+    t[1, 3] = k.shape[0]  # a block past the pool reads as zeros
+    zero = make(lens, ctx, 8, 2, 64, False, 23, junk=0.0)
+    zero[1][tables[1, 3]] = 0
+    zero[2][tables[1, 3]] = 0
+    out, flags = run(indptr(lens), t, c)
+    assert flags == pkv.DEVFLAG_BAD_BLOCK_ID
+    want = pkv.paged_prefill_attention(q, indptr(lens), zero[1], zero[2], tables, c, 0.125)
+    assert torch.equal(out, want)
+    c2 = c.clone()
+    c2[2] = tables.shape[1] * 16 + 5  # clamped to the table
+    _, flags = run(indptr(lens), tables.clone().clamp(min=0), c2)
+    assert flags & pkv.DEVFLAG_BAD_CONTEXT_LEN
+    ip = indptr(lens)
+    ip[3] = 1000  # past the rows: that sequence is skipped
+    out, flags = run(ip, tables, c)
+    assert flags == pkv.DEVFLAG_BAD_INDPTR
+    assert torch.equal(out[:50], good[:50]) and bool((out[50:] == 7).all())
+
+
+def test_captured_graphs_share_no_workspace(pkv):
+    """Two captured calls with split contexts, replayed beside each other on two streams."""
+    jobs = []
+    with split_tokens(128):
+        for seed in (31, 32):
+            lens, ctx = [3, 2], [1500, 1100]
+            q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, False, seed)
+            c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+            ip = indptr(lens)
+            want = pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out = pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1)
+            jobs.append((graph, out, want, torch.cuda.Stream(), (q, k, v, tables, c, ip)))
+    for _ in range(20):
+        for graph, _, _, s, _ in jobs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in jobs:
+        assert torch.equal(out, want)
+
+
+def test_other_stream(pkv):
+    lens, ctx = [3, 2], [1500, 1100]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, True, 41)
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    want = pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, 0.1, scales=scales)
+    ip = indptr(lens)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with split_tokens(256):
+        got = [pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1, scales=scales, stream=s) for _ in range(4)]
+    s.synchronize()
+    for o in got[1:]:
+        assert torch.equal(o, got[0])
+    assert float((got[0].float() - want.float()).abs().max()) < 0.05
