@@ -64,18 +64,40 @@ struct PrefillCfg {
   static constexpr int kOffRing = kOffQ + 2 * kQTile;
   static constexpr int kOffExp = kOffRing + kSlots * kSlot;
   static constexpr int kOffBar = kOffExp + kExp * kTile16;
-  static constexpr int kBarBytes = 320;
-  static constexpr int kOffPoison = kOffBar + kBarBytes;  // int[3][D]
-  static constexpr int kBytes = 1024 + kOffPoison + 3 * D * 4;
+  static constexpr int kBarBytes = 512;
+  static constexpr int kOffPoison = kOffBar + kBarBytes;  // int[kinds][D]
+  static constexpr int kKinds = FP8 ? 1 : 3;               // NaN, +inf, -inf (E4M3 has no infinity)
+  // 1008: alignment slack (the start of dynamic shared memory is 16-byte aligned)
+  static constexpr int kBytes = 1008 + kOffPoison + kKinds * D * 4;
   static constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
   static constexpr int kThreads = 384;
   static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kFixWarp0 = 10;
   static constexpr float kLazy = 8.f;
   static constexpr float kBias = FP8 ? kPrefillWeightBias : 0.f;
   static_assert(kBytes <= 227 * 1024, "shared memory");
-  static_assert(kSlots * kSlot + kExp * kTile16 >= 128 * D * 4, "room for the join of two groups");
-  static_assert((2 * kSlots + 18) * 8 + 12 <= kBarBytes, "barriers");
 };
+
+// barriers and small shared state, at kOffBar
+struct PrefillShared {
+  uint64_t full[8], empty[8];  // ring: tile landed, tile consumed
+  uint64_t s_full[2];          // scores of a step done (and every product issued before)
+  uint64_t p_full[2];          // weights of a step written (one arrival per warp)
+  uint64_t o_full[2];          // every product of the group's work done
+  uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
+  uint64_t exp_free[2];        // E4M3: expanded V tile consumed
+  uint64_t v_sent[8];          // load of a V tile that warps 10, 11 work on issued
+  uint64_t q_full, q_empty;
+  uint64_t work_full[2], work_empty[2];
+  uint64_t clc;                // answer of the work query landed
+  uint64_t drain;              // every MMA issued so far done
+  alignas(16) uint4 clc_answer;
+  int4 work[2][2];
+  uint32_t tmem;
+  int abort;
+  int poisoned;  // 1 + number of the work whose V held values that are not finite
+  int epilogues;  // softmax warps through the epilogue of a work with steps, all works counted
+};
+static_assert(sizeof(PrefillShared) <= 512, "shared state");
 
 namespace {
 
@@ -132,13 +154,75 @@ __device__ __forceinline__ uint32_t e4m3x4_rest(float (&x)[4]) {
   return w;
 }
 
-// what a CTA works on
+// Ask for the next CTA of the grid that has not started, to do its work here; the 16-byte
+// answer lands in shared memory and completes on the barrier.
+__device__ __forceinline__ void clc_ask(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The answer: false when no CTA is left, else that CTA's grid index.
+__device__ __forceinline__ bool clc_read(const uint4* answer, uint32_t& x, uint32_t& y) {
+  uint32_t ok;
+  [[maybe_unused]] uint32_t z;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %3, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, a;\n\t}"
+      : "=r"(x), "=r"(y), "=r"(z), "=r"(ok)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok != 0;
+}
+
+// 2^x by the hardware approximation, subnormal results flushed to zero
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One CTA's worth of work, and what every role derives from it
 struct Work {
-  int tok0;    // first query token (row of q) of the CTA
-  int ntok;    // its tokens
-  int seq;     // sequence
-  int ctx;     // cached tokens
-  int shift;   // causal: the CTA's token i sees keys < shift + i + 1
+  int tok0;   // first query token (row of q)
+  int ntok;   // its tokens
+  int seq;    // sequence
+  int ctx;    // cached tokens
+  int shift;  // causal: the work's token i sees keys < shift + i + 1
+  int h, split;
+};
+
+template <bool WIDE>
+struct Steps {
+  int k0, nstep, n_of[2];  // first 128-key step, steps, local steps of the groups
+  int lim_min;             // keys that every row sees
+  int first_cut;           // first step whose V needs care: some row does not see all of its keys
+  __device__ __forceinline__ static int lim(const Work& w, const PrefillParams& p, int i) {
+    return p.causal ? max(0, min(w.ctx, w.shift + i + 1)) : w.ctx;
+  }
+  __device__ __forceinline__ Steps(const Work& w, const PrefillParams& p, int tile_tok) {
+    k0 = w.split * p.split_tiles;
+    auto to = [&](int l) { return max(0, min((l + 127) / 128, k0 + p.split_tiles) - k0); };
+    nstep = to(lim(w, p, w.ntok - 1));
+    if constexpr (WIDE) {
+      n_of[0] = to(lim(w, p, min(w.ntok, tile_tok) - 1));
+      n_of[1] = w.ntok > tile_tok ? nstep : 0;
+    } else {
+      n_of[0] = (nstep + 1) / 2;
+      n_of[1] = nstep / 2;
+    }
+    lim_min = lim(w, p, 0);
+    first_cut = max(0, min(nstep, lim_min / 128 - k0));
+  }
+  // position of K and V of step j in the ring's order K0 K1 V0 K2 V1 ..
+  __device__ __forceinline__ static int k_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
+  __device__ __forceinline__ int v_item(int j) const { return min(2 * j + 2, 2 * nstep - 1); }
 };
 
 }  // namespace
@@ -148,153 +232,55 @@ __global__ void __launch_bounds__(384, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
   using C = PrefillCfg<D, FP8>;
-  constexpr int NS = C::kSlots;
+  constexpr unsigned NS = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [NS] tile landed
-  uint64_t* empty = full + NS;     // [NS] tile consumed
-  uint64_t* s_full = empty + NS;   // [2] scores of a step done (and the products issued before)
-  uint64_t* p_full = s_full + 2;   // [2] weights of a step written (one arrival per warp)
-  uint64_t* o_full = p_full + 2;   // [2] every product of the group done
-  uint64_t* fixed = o_full + 2;    // bf16: [4] V tile of a cut step fixed; E4M3: [2] V tile expanded
-  uint64_t* exp_free = fixed + 4;  // E4M3: [2] expanded V tile consumed
-  uint64_t* q_full = exp_free + 2;
-  uint64_t* drain = q_full + 1;    // every MMA issued so far done (abort path)
-  uint64_t* v_sent = drain + 1;    // [4] load of V of a step that warps 10, 11 work on issued
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_sent + 4);
-  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* poisoned = abort + 1;
-  int* poison = reinterpret_cast<int*>(smem + C::kOffPoison);  // [3][D] first key with NaN, +inf, -inf
+  PrefillShared& sh = *reinterpret_cast<PrefillShared*>(smem + C::kOffBar);
+  volatile int* abort = &sh.abort;
+  volatile int* poisoned = &sh.poisoned;
+  int* poison = reinterpret_cast<int*>(smem + C::kOffPoison);  // [kinds][D] first key with such a value
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % p.hkv;
-  const int slot = blockIdx.x / p.hkv;
-  const int split = blockIdx.y;
   const int G = p.group;
   const int tile_tok = C::kRows / G;                   // tokens of a 128-row tile
-  const int cta_tok = WIDE ? 2 * tile_tok : tile_tok;  // tokens of a CTA
-  pdl_wait();
-  pdl_launch_dependents();
-
-  // ---- the CTA's tokens: tile slots count the sequences' tiles in order, each sequence's
-  // longest (last) tile first; every warp finds them by itself
-  Work w{0, 0, -1, 0, 0};
-  {
-    int before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      int first = 0, n = 0;
-      if (b < p.batch) {
-        first = p.q_indptr[b];
-        const int last = p.q_indptr[b + 1];
-        n = last - first;
-        if (first < 0 || last < first || last > p.total_q) {
-          if (warp == 0 && blockIdx.x == 0 && split == 0) set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
-          n = 0;
-        }
-      }
-      const int tiles = (n + cta_tok - 1) / cta_tok;
-      int upto = tiles;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int v = __shfl_up_sync(kFull, upto, m);
-        if (lane >= m) upto += v;
-      }
-      const unsigned hit = __ballot_sync(kFull, slot < before + upto);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const int tile = __shfl_sync(kFull, before + upto - 1 - slot, src);  // tiles after this one: reversed order
-        first = __shfl_sync(kFull, first, src);
-        n = __shfl_sync(kFull, n, src);
-        w.seq = b0 + src;
-        int ctx = p.context_lens[w.seq];
-        const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
-        if (ctx < 0 || ctx > cap) {
-          if (threadIdx.x == 0) set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
-          ctx = max(0, min(ctx, cap));
-        }
-        w.ctx = ctx;
-        w.tok0 = first + tile * cta_tok;
-        w.ntok = min(cta_tok, n - tile * cta_tok);
-        w.shift = ctx - n + tile * cta_tok;
-        break;
-      }
-      before += __shfl_sync(kFull, upto, 31);
-    }
-  }
-  if (w.seq < 0) return;  // a slot past the last tile
-  auto lim_of = [&](int i) { return p.causal ? max(0, min(w.ctx, w.shift + i + 1)) : w.ctx; };
-
-  // ---- the steps (128-key tiles) of the split that each group takes part in
-  const int k0 = split * p.split_tiles;
-  auto steps_to = [&](int lim) { return max(0, min((lim + C::kKeys - 1) / C::kKeys, k0 + p.split_tiles) - k0); };
-  const int nstep = steps_to(lim_of(w.ntok - 1));
-  int n_of[2];  // local steps of the groups
-  if constexpr (WIDE) {
-    n_of[0] = steps_to(lim_of(min(w.ntok, tile_tok) - 1));
-    n_of[1] = w.ntok > tile_tok ? nstep : 0;
-  } else {
-    n_of[0] = (nstep + 1) / 2;
-    n_of[1] = nstep / 2;
-  }
-  const int lim_min = lim_of(0);
-  // the first step whose V needs care: some row of the CTA does not see all of its keys
-  const int first_cut = max(0, min(nstep, lim_min / C::kKeys - k0));
-
-  const bool soft = warp < 8;
-  const int group = WIDE ? (warp >> 2) & 1 : 0;  // which tile's rows a softmax thread owns
-  const int r = threadIdx.x & 127;               // row of the tile, TMEM lane
-  const int my_i = group * tile_tok + r / G;     // token within the CTA
-  const bool rv = soft && my_i < w.ntok;
-  const int hq = h * G + r % G;
-  const int64_t orow = static_cast<int64_t>(w.tok0 + my_i) * p.hq + hq;
-  const int64_t rec = static_cast<int64_t>(split) * p.total_q * p.hq + orow;
-
-  if (nstep == 0) {  // nothing to see here: empty rows, or an empty record
-    if (rv && (WIDE || warp < 4)) {
-      if (p.splits > 1) {
-        p.part_ml[rec] = make_float2(-INFINITY, 0.f);
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse != nullptr) p.lse[orow] = -INFINITY;
-      }
-    }
-    return;
-  }
+  const int cta_tok = WIDE ? 2 * tile_tok : tile_tok;  // tokens of a work
 
   if (warp == 0) {
     __syncwarp();
-    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
     tmem_relinquish();
   }
   if (threadIdx.x == C::kIssuerWarp * 32) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.fixed[i], 1);
+      mbar_init(&sh.v_sent[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&exp_free[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.exp_free[i], 1);
+      mbar_init(&sh.work_full[i], 1);
+      mbar_init(&sh.work_empty[i], 11);  // the issuer, warps 10 and 11, 8 softmax warps
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&fixed[i], 1);
-      mbar_init(&v_sent[i], 1);
-    }
-    mbar_init(q_full, FP8 ? (WIDE ? 8 : 4) : 1);
-    mbar_init(drain, 1);
-    *abort = 0;
-    *poisoned = 0;
+    mbar_init(&sh.q_full, FP8 ? (WIDE ? 8 : 4) : 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.clc, 1);
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    sh.poisoned = 0;
+    sh.epilogues = 0;
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < 3 * D; i += C::kThreads) poison[i] = 0x7fffffff;
+  for (int i = threadIdx.x; i < C::kKinds * D; i += C::kThreads) poison[i] = 0x7fffffff;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+  pdl_wait();  // nothing above touches global memory
+  pdl_launch_dependents();
 
   const uint32_t q_base = smem_u32(smem + C::kOffQ);
   const uint32_t ring = smem_u32(smem + C::kOffRing);
@@ -302,10 +288,23 @@ __global__ void __launch_bounds__(384, 1)
     set_flag(p.status, PKV_DEVFLAG_WAIT_TIMEOUT);
     *abort = 1;
   };
-  // position of K and V of step j in the ring's order K0 K1 V0 K2 V1 ..
-  auto k_item = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-  auto v_item = [&](int j) { return min(2 * j + 2, 2 * nstep - 1); };
+  // the work number n (all roles see the same sequence); false: there is none left, or abort
+  auto next_work = [&](unsigned n, Work& w, unsigned lanes = kFull) -> bool {
+    const bool ok = wait_or_abort(&sh.work_full[n & 1], (n >> 1) & 1, abort);
+    if (!__all_sync(lanes, ok)) {
+      if (!*abort) fail();
+      return false;
+    }
+    const int4 a = sh.work[n & 1][0], b = sh.work[n & 1][1];
+    w = Work{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    __syncwarp(lanes);
+    if (lane == 0) mbar_arrive(&sh.work_empty[n & 1]);
+    return w.seq >= 0;
+  };
 
+  // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == C::kIssuerWarp) {
     // ======================================================================== MMA issuer
     if (lane == 0) {
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t id_s = (FP8 ? idesc_f16(C::kRows, C::kKeys, false, false)
                                  : idesc_f16(C::kRows, C::kKeys, true, false)) |
                             (p.negate ? 1u << 13 : 0u);
-      auto issue_s = [&](int g, int item) {
+      auto issue_s = [&](int g, unsigned item) {
         const uint32_t kt = ring + (item % NS) * C::kSlot;
         const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
         const uint32_t d = tmem + C::kColS + 128 * g;
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(384, 1)
             mma_f16_ss(d, sdesc_sw128(qt + at, 16, 1024), sdesc_sw128(kt + at, 16, 1024), id_s, kk > 0 ? 1u : 0u);
           }
         }
-        tc_commit(&s_full[g]);
+        tc_commit(&sh.s_full[g]);
       };
       auto issue_o = [&](int g, int t, uint32_t vt) {
         const uint32_t pt = tmem + C::kColS + 128 * g;
@@ -342,470 +341,672 @@ __global__ void __launch_bounds__(384, 1)
           mma_f16_ts(tmem + C::kColO + D * g, pt + 8 * kk, sdesc_sw128(vt + kk * 2048, C::kHalf16, 1024), kIdO,
                      (t > 0 || kk > 0) ? 1u : 0u);
       };
-      auto wait_full = [&](int item) { return wait_or_abort(&full[item % NS], (item / NS) & 1, abort); };
-      // V of step j is ready for the tensor cores
-      auto wait_v = [&](int j) {
-        if constexpr (FP8) return wait_or_abort(&fixed[j & 1], (j >> 1) & 1, abort);
-        if (j >= first_cut) return wait_or_abort(&fixed[j - first_cut], 0, abort);
-        return wait_full(v_item(j));
-      };
-      auto v_tile = [&](int j) {
-        return FP8 ? smem_u32(smem + C::kOffExp + (j & 1) * C::kTile16) : ring + (v_item(j) % NS) * C::kSlot;
-      };
-      auto free_v = [&](int j) { tc_commit(FP8 ? &exp_free[j & 1] : &empty[v_item(j) % NS]); };
+      auto wait_full = [&](unsigned item) { return wait_or_abort(&sh.full[item % NS], (item / NS) & 1, abort); };
 
-      bool ok = wait_or_abort(q_full, 0, abort);
-      tc_fence_after();
-      if constexpr (WIDE) {
-        // step j of both tiles: S of step j + 1 follows P V of step j in the same columns, in
-        // issue order
-        if (ok) ok = wait_full(0);
-        if (ok) {
-          tc_fence_after();
-          if (n_of[0] > 0) issue_s(0, 0);
-          if (n_of[1] > 0) issue_s(1, 0);
-          tc_commit(&empty[0]);
-        }
-        for (int j = 0; j < nstep && ok; ++j) {
-          bool k_ready = false;
+      unsigned base = 0, steps_done = 0, cuts = 0, q_count = 0;
+      unsigned c_p[2] = {0, 0};  // steps of the groups so far
+      bool ok = true;
+      Work w;
+      for (unsigned n = 0; ok && next_work(n, w, 1u); ++n) {
+        const Steps<WIDE> st(w, p, tile_tok);
+        const int nstep = st.nstep;
+        if (nstep == 0) continue;
+        // V of step j is ready for the tensor cores
+        auto wait_v = [&](int j) {
+          if constexpr (FP8) {
+            const unsigned v = steps_done + j;
+            return wait_or_abort(&sh.fixed[v & 1], (v >> 1) & 1, abort);
+          }
+          if (j >= st.first_cut) {
+            const unsigned c = cuts + j - st.first_cut;
+            return wait_or_abort(&sh.fixed[c & 7], (c >> 3) & 1, abort);
+          }
+          return wait_full(base + st.v_item(j));
+        };
+        auto v_tile = [&](int j) {
+          return FP8 ? smem_u32(smem + C::kOffExp + ((steps_done + j) & 1) * C::kTile16)
+                     : ring + ((base + st.v_item(j)) % NS) * C::kSlot;
+        };
+        auto free_v = [&](int j) {
+          tc_commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[(base + st.v_item(j)) % NS]);
+        };
+        auto k_item = [&](int j) { return base + st.k_item(j); };
+        ok = wait_or_abort(&sh.q_full, q_count & 1, abort);
+        ++q_count;
+        if constexpr (WIDE) {
+          // step j of both tiles: S of step j + 1 follows P V of step j in the same columns, in
+          // issue order
+          if (ok) ok = wait_full(k_item(0));
+          if (ok) {
+            tc_fence_after();
+            if (st.n_of[0] > 0) issue_s(0, k_item(0));
+            if (st.n_of[1] > 0) issue_s(1, k_item(0));
+            tc_commit(&sh.empty[k_item(0) % NS]);
+            if (nstep == 1) tc_commit(&sh.q_empty);
+          }
+          for (int j = 0; j < nstep && ok; ++j) {
+            bool k_ready = false;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (ok && j < n_of[g]) {
-              ok = wait_or_abort(&p_full[g], j & 1, abort) && wait_v(j);
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(g, j, v_tile(j));
-              if (j + 1 == n_of[g]) tc_commit(&o_full[g]);
+            for (int g = 0; g < 2; ++g) {
+              if (ok && j < st.n_of[g]) {
+                ok = wait_or_abort(&sh.p_full[g], (c_p[g] + j) & 1, abort) && wait_v(j);
+                if (!ok) break;
+                tc_fence_after();
+                issue_o(g, j, v_tile(j));
+                if (j + 1 == st.n_of[g]) tc_commit(&sh.o_full[g]);
+              }
+              if (g == 1) free_v(j);
+              if (ok && j + 1 < st.n_of[g]) {
+                if (!k_ready) ok = wait_full(k_item(j + 1));
+                if (!ok) break;
+                k_ready = true;
+                tc_fence_after();
+                issue_s(g, k_item(j + 1));
+              }
             }
-            if (g == 1) free_v(j);
-            if (ok && j + 1 < n_of[g]) {
-              if (!k_ready) ok = wait_full(k_item(j + 1));
-              if (!ok) break;
-              k_ready = true;
-              tc_fence_after();
-              issue_s(g, k_item(j + 1));
+            if (ok && j + 1 < nstep) {
+              tc_commit(&sh.empty[k_item(j + 1) % NS]);
+              if (j + 2 == nstep) tc_commit(&sh.q_empty);
             }
           }
-          if (ok && j + 1 < nstep) tc_commit(&empty[k_item(j + 1) % NS]);
-        }
-      } else {
-        for (int j = 0; j < min(2, nstep) && ok; ++j) {
-          ok = wait_full(k_item(j));
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(j, k_item(j));
-          tc_commit(&empty[k_item(j) % NS]);
-        }
-        for (int j = 0; j < nstep && ok; ++j) {
-          const int g = j & 1, t = j >> 1;
-          ok = wait_or_abort(&p_full[g], t & 1, abort) && wait_v(j);
-          if (!ok) break;
-          tc_fence_after();
-          issue_o(g, t, v_tile(j));
-          free_v(j);
-          if (j + 2 >= nstep) tc_commit(&o_full[g]);
-          if (j + 2 < nstep) {
-            ok = wait_full(k_item(j + 2));
+        } else {
+          for (int j = 0; j < min(2, nstep) && ok; ++j) {
+            ok = wait_full(k_item(j));
             if (!ok) break;
             tc_fence_after();
-            issue_s(g, k_item(j + 2));
-            tc_commit(&empty[k_item(j + 2) % NS]);
+            issue_s(j, k_item(j));
+            tc_commit(&sh.empty[k_item(j) % NS]);
+            if (j + 1 == nstep) tc_commit(&sh.q_empty);
+          }
+          for (int j = 0; j < nstep && ok; ++j) {
+            const int g = j & 1, t = j >> 1;
+            ok = wait_or_abort(&sh.p_full[g], (c_p[g] + t) & 1, abort) && wait_v(j);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(g, t, v_tile(j));
+            free_v(j);
+            if (j + 2 >= nstep) tc_commit(&sh.o_full[g]);
+            if (j + 2 < nstep) {
+              ok = wait_full(k_item(j + 2));
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(g, k_item(j + 2));
+              tc_commit(&sh.empty[k_item(j + 2) % NS]);
+              if (j + 3 == nstep) tc_commit(&sh.q_empty);
+            }
           }
         }
+        base += 2 * nstep;
+        steps_done += nstep;
+        cuts += nstep - st.first_cut;
+        c_p[0] += st.n_of[0];
+        c_p[1] += st.n_of[1];
       }
       if (!ok && !*abort) fail();
       // nothing may run on the tensor cores when the CTA frees its tensor memory
-      tc_commit(drain);
-      mbar_wait(drain, 0);
+      tc_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
   } else if (warp == C::kProducerWarp) {
-    // ======================================================================== TMA producer
-    const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
-    const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
+    // ======================================================================== work and TMA producer
     // bf16 at D = 128: lane 2 b + half takes half of block b; else lane b takes block b
     constexpr int kPer = FP8 ? 1 : C::kHalves;
     const bool loads = lane < C::kStepBlocks * kPer;
     const int blk = lane / kPer, hf = lane % kPer;
-    // pool row of this lane's block in step j; a block past the context, or with an id outside
-    // the pool, becomes a box entirely outside the tensor, which reads zeros
-    auto row_of = [&](int j) {
-      int row = -kBlockSize;
-      const int at = (k0 + j) * C::kStepBlocks + blk;
-      if (loads && j < nstep && at < nblk) {
-        const int id = table[at];
-        if (id >= 0 && id < p.num_blocks) row = id * kBlockSize;
-        else set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
-      }
-      return row;
-    };
-    auto load = [&](const CUtensorMap* tm, int item, int row) {
-      const int st = item % NS;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kSlot);
+    auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row) {
+      const unsigned st = item % NS;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
       __syncwarp();
       if (loads) {
         uint8_t* dst = smem + C::kOffRing + st * C::kSlot;
-        if constexpr (FP8) tma_load_3d(dst + blk * kBlockSize * D, tm, 0, h, row, &full[st]);
-        else tma_load_3d(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, h, row, &full[st]);
+        if constexpr (FP8) tma_load_3d(dst + blk * kBlockSize * D, tm, 0, head, row, &sh.full[st]);
+        else tma_load_3d(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, row, &sh.full[st]);
       }
     };
-    auto slot_free = [&](int item) {
-      const bool ok = item < NS || wait_or_abort(&empty[item % NS], ((item / NS) - 1) & 1, abort);
+    auto slot_free = [&](unsigned item) {
+      const bool ok = item < NS || wait_or_abort(&sh.empty[item % NS], ((item / NS) - 1) & 1, abort);
       return __all_sync(kFull, ok);
     };
-    int cur = row_of(0), nxt = row_of(1), ahead = row_of(2);
-    if constexpr (!FP8) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, (WIDE ? 2 : 1) * C::kQTile);
+    // the tokens of the work at (x, y) of the grid: tile slots count the sequences' tiles in
+    // order, each sequence's longest (last) tile first.  seq < 0: a slot past the last tile
+    auto find = [&](unsigned x, unsigned y) {
+      Work w{0, 0, -1, 0, 0, static_cast<int>(x % p.hkv), static_cast<int>(y)};
+      const int slot = x / p.hkv;
+      int before = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int first = 0, n = 0;
+        if (b < p.batch) {
+          first = p.q_indptr[b];
+          const int last = p.q_indptr[b + 1];
+          n = last - first;
+          if (first < 0 || last < first || last > p.total_q) {
+            set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
+            n = 0;
+          }
+        }
+        const int tiles = (n + cta_tok - 1) / cta_tok;
+        int upto = tiles;
 #pragma unroll
-        for (int t = 0; t < (WIDE ? 2 : 1); ++t)
-#pragma unroll
-          for (int c = 0; c < C::kHalves; ++c)
-            tma_load_3d(smem + C::kOffQ + t * C::kQTile + c * C::kHalf16, &tm_q, c * 64, h * G, w.tok0 + t * tile_tok,
-                        q_full);
+        for (int m = 1; m < 32; m <<= 1) {
+          const int v = __shfl_up_sync(kFull, upto, m);
+          if (lane >= m) upto += v;
+        }
+        const unsigned hit = __ballot_sync(kFull, slot < before + upto);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          const int tile = __shfl_sync(kFull, before + upto - 1 - slot, src);  // tiles after this one
+          first = __shfl_sync(kFull, first, src);
+          n = __shfl_sync(kFull, n, src);
+          w.seq = b0 + src;
+          int ctx = p.context_lens[w.seq];
+          const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
+          if (ctx < 0 || ctx > cap) {
+            set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
+            ctx = max(0, min(ctx, cap));
+          }
+          w.ctx = ctx;
+          w.tok0 = first + tile * cta_tok;
+          w.ntok = min(cta_tok, n - tile * cta_tok);
+          w.shift = ctx - n + tile * cta_tok;
+          break;
+        }
+        before += __shfl_sync(kFull, upto, 31);
       }
+      return w;
+    };
+
+    unsigned n = 0, base = 0, steps_done = 0, cuts = 0, q_count = 0, asked = 0;
+    uint32_t gx = blockIdx.x, gy = blockIdx.y;
+    bool more = true, ok = true;
+    while (more && ok) {
+      const Work w = find(gx, gy);
+      if (lane == 0) clc_ask(&sh.clc_answer, &sh.clc);
+      if (w.seq >= 0) {
+        const Steps<WIDE> st(w, p, tile_tok);
+        const int nstep = st.nstep;
+        ok = n < 2 || wait_or_abort(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+        ok = __all_sync(kFull, ok);
+        if (ok) {
+          if (lane == 0) {
+            sh.work[n & 1][0] = make_int4(w.tok0, w.ntok, w.seq, w.ctx);
+            sh.work[n & 1][1] = make_int4(w.shift, w.h, w.split, 0);
+            mbar_arrive(&sh.work_full[n & 1]);
+          }
+          ++n;
+        }
+        if (ok && nstep > 0) {
+          const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
+          const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
+          // pool row of this lane's block in step j; a block past the context, or with an id
+          // outside the pool, becomes a box entirely outside the tensor, which reads zeros
+          auto row_of = [&](int j) {
+            int row = -kBlockSize;
+            const int at = (st.k0 + j) * C::kStepBlocks + blk;
+            if (loads && j < nstep && at < nblk) {
+              const int id = table[at];
+              if (id >= 0 && id < p.num_blocks) row = id * kBlockSize;
+              else set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
+            }
+            return row;
+          };
+          int cur = row_of(0), nxt = row_of(1), ahead = row_of(2);
+          if constexpr (!FP8) {
+            // Q's tiles are free once the last scores of the work before are done
+            if (q_count > 0) ok = wait_or_abort(&sh.q_empty, (q_count - 1) & 1, abort);
+            ok = __all_sync(kFull, ok);
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
+#pragma unroll
+              for (int t = 0; t < (WIDE ? 2 : 1); ++t)
+#pragma unroll
+                for (int c = 0; c < C::kHalves; ++c)
+                  tma_load_3d(smem + C::kOffQ + t * C::kQTile + c * C::kHalf16, &tm_q, c * 64, w.h * G,
+                              w.tok0 + t * tile_tok, &sh.q_full);
+            }
+          }
+          if (ok) ++q_count;
+          ok = ok && slot_free(base);
+          if (ok) load(&tm_k, base, w.h, cur);
+          unsigned issued = base + (ok ? 1 : 0);
+          for (int j = 0; j < nstep && ok; ++j) {
+            if (j + 1 < nstep) {
+              if (!(ok = slot_free(base + st.k_item(j + 1)))) break;
+              load(&tm_k, base + st.k_item(j + 1), w.h, nxt);
+              issued = base + st.k_item(j + 1) + 1;
+            }
+            if (!(ok = slot_free(base + st.v_item(j)))) break;
+            load(&tm_v, base + st.v_item(j), w.h, cur);
+            issued = base + st.v_item(j) + 1;
+            if (lane == 0 && (FP8 || j >= st.first_cut))
+              mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
+            cur = nxt;
+            nxt = ahead;
+            ahead = row_of(j + 3);
+          }
+          base = ok ? base + 2 * nstep : issued;
+          steps_done += nstep;
+          cuts += nstep - st.first_cut;
+        }
+      }
+      // the next work: the answer is always taken, so that none is in flight at the end
+      const bool told = mbar_wait(&sh.clc, asked & 1);
+      ++asked;
+      ok = __all_sync(kFull, told) && ok;
+      more = told && clc_read(&sh.clc_answer, gx, gy);
+      fence_proxy_async_smem();  // read before the next answer is written
+      __syncwarp();
     }
-    load(&tm_k, 0, cur);
-    int issued = 1;
-    bool ok = true;
-    for (int j = 0; j < nstep; ++j) {
-      if (j + 1 < nstep) {
-        if (!(ok = slot_free(k_item(j + 1)))) break;
-        load(&tm_k, k_item(j + 1), nxt);
-        issued = k_item(j + 1) + 1;
+    // no work left: tell the other roles
+    if (ok) {
+      ok = n < 2 || wait_or_abort(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+      if (ok && lane == 0) {
+        sh.work[n & 1][0] = make_int4(0, 0, -1, 0);
+        sh.work[n & 1][1] = make_int4(0, 0, 0, 0);
+        mbar_arrive(&sh.work_full[n & 1]);
       }
-      if (!(ok = slot_free(v_item(j)))) break;
-      load(&tm_v, v_item(j), cur);
-      issued = v_item(j) + 1;
-      if (lane == 0 && (FP8 || j >= first_cut)) mbar_arrive(&v_sent[(FP8 ? j : j - first_cut) & 3]);
-      cur = nxt;
-      nxt = ahead;
-      ahead = row_of(j + 3);
     }
     if (lane == 0) {
       if (!ok && !*abort) fail();
       // nothing may be in flight when the CTA exits: the last tiles issued have landed
-      for (int i = max(0, issued - NS); i < issued; ++i)
-        if (!mbar_wait(&full[i % NS], (i / NS) & 1)) break;
-      if (!FP8) mbar_wait(q_full, 0);
+      for (unsigned i = base > NS ? base - NS : 0; i < base; ++i)
+        if (!mbar_wait(&sh.full[i % NS], (i / NS) & 1)) break;
+      if (!FP8 && q_count > 0) mbar_wait(&sh.q_full, (q_count - 1) & 1);
     }
     __syncwarp();
-  } else if (!soft) {
+  } else {
     // ======================================================================== V: cut tiles, expansion
     const int ft = threadIdx.x - C::kFixWarp0 * 32;  // 0 .. 63
+    unsigned number = 0;
     auto note = [&](int kind, int dim, int key) {
       atomicMin(&poison[kind * D + dim], key);
-      *poisoned = 1;
+      *poisoned = static_cast<int>(number) + 1;
     };
-    const int j_first = FP8 ? 0 : first_cut;
-    for (int j = j_first; j < nstep; ++j) {
-      const int item = v_item(j);
-      // the parity of `full` means this load only once it is issued (the slot's loads before it
-      // are not waited for here); v_sent itself is at most one phase ahead: step j + 4 goes out
-      // after V of step j, or of a later one, was consumed (bf16: at most 3 cut steps)
-      const int sent = FP8 ? j : j - first_cut;
-      bool ok = wait_or_abort(&v_sent[sent & 3], (sent >> 2) & 1, abort);
-      if (ok) ok = wait_or_abort(&full[item % NS], (item / NS) & 1, abort);
-      if constexpr (FP8)
-        if (ok && j >= 2) ok = wait_or_abort(&exp_free[j & 1], ((j >> 1) - 1) & 1, abort);
-      if (!ok && !*abort) fail();
-      const int key0 = (k0 + j) * C::kKeys;
-      const int seen = lim_min - key0, end = w.ctx - key0;  // rows below seen: every row's; from end on: no row's
-      uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
-      if (ok) {
-        if constexpr (FP8) {
-          constexpr int kChunks = D / 8;  // 8-code pieces of a row
-          constexpr int kStep = 64 / kChunks;
-          const int c = ft % kChunks, r0 = ft / kChunks;
-          const uint32_t ex = smem_u32(smem + C::kOffExp + (j & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
+    constexpr int kChunks = D / 8;  // 8-element pieces of a row
+    constexpr int kStep = 64 / kChunks;
+    const int c = ft % kChunks, r0 = ft / kChunks;
+    unsigned base = 0, steps_done = 0, cuts = 0, with_steps = 0;
+    bool ok = true;
+    Work w;
+    for (unsigned n = 0; ok; ++n) {
+      // both warps leave together
+      if (named_sync_or(1, 64, !next_work(n, w))) break;
+      number = n;
+      const Steps<WIDE> st(w, p, tile_tok);
+      const int nstep = st.nstep;
+      if (nstep == 0) continue;
+      // before this work's cut steps: the works before are through their epilogues, and what they
+      // left in the list of values that are not finite is cleared
+      bool cleared = false;
+      auto clear = [&]() {
+        cleared = true;
+        const volatile int* through = &sh.epilogues;
+        const long long start = clock64();
+        while (ok && *through < static_cast<int>(8 * with_steps)) {
+          if (*abort) ok = false;
+          if (clock64() - start > kWaitLimitCycles) {
+            ok = false;
+            fail();
+          }
+        }
+        const bool any = *poisoned != 0;
+        named_sync(3, 64);
+        if (any) {
+          for (int i = ft; i < C::kKinds * D; i += 64) poison[i] = 0x7fffffff;
+          *poisoned = 0;
+          named_sync(3, 64);
+        }
+      };
+      for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
+        const bool cut = j >= st.first_cut;
+        if (cut && !cleared) clear();
+        const unsigned item = base + st.v_item(j);
+        // the parity of `full` means this load only once it is issued (the slot's loads before it
+        // are not waited for here); v_sent itself is never a phase ahead: eight V tiles on, the
+        // ring has come round
+        const unsigned sent = FP8 ? steps_done + j : cuts + j - st.first_cut;
+        if (ok) ok = wait_or_abort(&sh.v_sent[sent & 7], (sent >> 3) & 1, abort);
+        if (ok) ok = wait_or_abort(&sh.full[item % NS], (item / NS) & 1, abort);
+        if constexpr (FP8)
+          if (ok && sent >= 2) ok = wait_or_abort(&sh.exp_free[sent & 1], ((sent >> 1) - 1) & 1, abort);
+        if (!ok && !*abort) fail();
+        const int key0 = (st.k0 + j) * C::kKeys;
+        // rows below seen: every row's; from end on: no row's
+        const int seen = st.lim_min - key0, end = w.ctx - key0;
+        uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
+        if (ok) {
+          if constexpr (FP8) {
+            const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
 #pragma unroll 4
-          for (int row = r0; row < C::kKeys; row += kStep) {
-            uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
-            if (j >= first_cut && row >= seen) {
-              if (row >= end) {
-                v = make_uint2(0u, 0u);
-              } else {
-                uint8_t* b = reinterpret_cast<uint8_t*>(&v);
+            for (int row = r0; row < C::kKeys; row += kStep) {
+              uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
+              if (cut && row >= seen) {
+                if (row >= end) {
+                  v = make_uint2(0u, 0u);
+                } else {
+                  uint8_t* b = reinterpret_cast<uint8_t*>(&v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if ((b[e] & 0x7f) == 0x7f) {  // NaN, the only E4M3 code that is not finite
-                    note(0, c * 8 + e, key0 + row);
-                    b[e] = 0;
-                  }
-              }
-            }
-            st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
-                         e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
-          }
-        } else {
-          constexpr int kChunks = D / 8;
-          constexpr int kStep = 64 / kChunks;
-          const int c = ft % kChunks;
-#pragma unroll 2
-          for (int row = max(0, seen) + ft / kChunks; row < C::kKeys; row += kStep) {
-            uint4* at = reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-            if (row >= end) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint4 v = *at;
-              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-              uint32_t odd = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-              if (odd) {  // exponent all ones somewhere
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t x = (e[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-                  if ((x & 0x7f80u) == 0x7f80u) {
-                    note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + k, key0 + row);
-                    e[k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
-                  }
+                  for (int e = 0; e < 8; ++e)
+                    if ((b[e] & 0x7f) == 0x7f) {  // NaN, the only E4M3 code that is not finite
+                      note(0, c * 8 + e, key0 + row);
+                      b[e] = 0;
+                    }
                 }
-                *at = v;
+              }
+              st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
+                           e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
+            }
+          } else {
+#pragma unroll 2
+            for (int row = max(0, seen) + r0; row < C::kKeys; row += kStep) {
+              uint4* at =
+                  reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+              if (row >= end) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint4 v = *at;
+                uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+                uint32_t odd = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                if (odd) {  // exponent all ones somewhere
+                  for (int k = 0; k < 8; ++k) {
+                    const uint32_t x = (e[k >> 1] >> (16 * (k & 1))) & 0xffffu;
+                    if ((x & 0x7f80u) == 0x7f80u) {
+                      note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + k, key0 + row);
+                      e[k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
+                    }
+                  }
+                  *at = v;
+                }
               }
             }
           }
         }
-      }
-      fence_proxy_async_smem();  // the tile is read by the tensor cores
-      if (named_sync_or(1, 64, *abort != 0)) break;
-      if (ft == 0) {
-        if constexpr (FP8) {
-          mbar_arrive(&empty[item % NS]);
-          mbar_arrive(&fixed[j & 1]);
-        } else {
-          mbar_arrive(&fixed[j - first_cut]);
+        fence_proxy_async_smem();  // the tile is read by the tensor cores
+        if (named_sync_or(1, 64, *abort != 0)) {
+          ok = false;
+          break;
+        }
+        if (ft == 0) {
+          if constexpr (FP8) {
+            mbar_arrive(&sh.empty[item % NS]);
+            mbar_arrive(&sh.fixed[sent & 1]);
+          } else {
+            mbar_arrive(&sh.fixed[sent & 7]);
+          }
         }
       }
+      ++with_steps;
+      base += 2 * nstep;
+      steps_done += nstep;
+      cuts += nstep - st.first_cut;
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ======================================================================== softmax
-    const int g = warp >> 2;  // accumulators: the tile (wide) or the parity of the steps (narrow)
-    const int nloc = n_of[g];
+    const int g = warp >> 2;               // accumulators: the tile (wide) or the parity of the steps (narrow)
+    const int r = threadIdx.x & 127;       // row of the tile, TMEM lane
+    const int my_i = (WIDE ? g * tile_tok : 0) + r / G;  // token within the work
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_base + C::kColS + 128 * g;
-    const uint32_t ocol = tmem + lane_base + C::kColO + D * g;
-    float sscale = p.score_scale;
-
-    if constexpr (FP8) {
-      // this row of Q as hi and lo codes, times 2^e that takes its largest into [128, 256)
-      if (WIDE || g == 0) {
-        const uint4* qr = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(w.tok0 + my_i) * p.q_stride + hq * D);
-        uint4 v[D / 8];
-        float top = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          v[c] = rv ? qr[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(e[k])), fabsf(bf16_hi(e[k]))));
-            odd |= ((((e[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u);
-          }
-        }
-        int ex = 0;
-        if (top > 0.f && !odd) ex = 7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-        ex = min(ex, 126);  // rows below 2^-119: their codes lose what lies under 2^-135
-        const float up = __uint_as_float(static_cast<uint32_t>(max(ex, -126) + 127) << 23);
-        const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {  // 16 codes: one 16-byte piece of the row
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = u4_word(v[2 * c + k / 2], 2 * (k & 1)), b = u4_word(v[2 * c + k / 2], 2 * (k & 1) + 1);
-            float x[4] = {bf16_lo(a) * up, bf16_hi(a) * up, bf16_lo(b) * up, bf16_hi(b) * up};
-            hi[k] = e4m3x4_rest(x);
-            lo[k] = e4m3x4_rest(x);
-          }
-          const uint32_t at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-          st_shared_v4(qt + at, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(qt + C::kCodes + at, lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
-        sscale = odd ? __int_as_float(0x7fffffff) : sscale * p.scales[h] / up;
-      }
-      if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
-        float* shared_scale = reinterpret_cast<float*>(smem + C::kOffQ + C::kQTile);  // no second Q tile here
-        if (g == 0) shared_scale[r] = sscale;
-        named_sync(2, 256);
-        if (g == 1) sscale = shared_scale[r];
-        named_sync(2, 256);
-      }
-    }
-
-    const int my_lim = lim_of(my_i);
-    // keys below every lim of the warp's rows need no mask (rows that do not exist do not count)
-    const int warp_lim = __reduce_min_sync(kFull, rv ? my_lim : 0x7fffffff);
-    const bool idle = !__any_sync(kFull, rv);  // no row of the warp exists: its products go nowhere
-    float m_used = -INFINITY, l = 0.f;
+    const uint32_t ocol = tmem + lane_base + C::kColO;
+    // narrow: (m, l) of both groups' rows and the rows' factors, where wide has its second Q tile
+    float2* join_ml = reinterpret_cast<float2*>(smem + C::kOffQ + C::kQTile);
+    float* join_scale = reinterpret_cast<float*>(join_ml + 256);
+    unsigned c_s = 0, c_o = 0;  // steps and works of the group so far
     bool dead = false;
-    for (int t = 0; t < nloc; ++t) {
-      const int key0 = (k0 + (WIDE ? t : 2 * t + g)) * C::kKeys;
-      bool ok = wait_or_abort(&s_full[g], t & 1, abort);
-      if (!__all_sync(kFull, ok)) {  // tensor-memory loads are warp-collective: leave as a warp
-        if (!*abort) fail();
+    Work w;
+    for (unsigned n = 0; !dead; ++n) {
+      if (!next_work(n, w)) {
         dead = true;
         break;
       }
-      tc_fence_after();
-      if (!idle) {
-        float s[2][64];
-        tmem_ld64(scol, s[0]);
-        tmem_ld64(scol + 64, s[1]);
-        if (key0 + C::kKeys > warp_lim) {
-          const int left = my_lim - key0;
+      const Steps<WIDE> st(w, p, tile_tok);
+      const int nloc = st.n_of[g];
+      const bool rv = my_i < w.ntok;
+      const int hq = w.h * G + r % G;
+      const int64_t orow = static_cast<int64_t>(w.tok0 + my_i) * p.hq + hq;
+      const int64_t rec = static_cast<int64_t>(w.split) * p.total_q * p.hq + orow;
+      const bool split_out = p.splits > 1;
+      if (WIDE ? nloc == 0 : st.nstep == 0) {  // rows that see nothing (of this split)
+        if (rv && (WIDE || g == 0)) {
+          if (split_out) {
+            p.part_ml[rec] = make_float2(-INFINITY, 0.f);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= left) s[i >> 6][i & 63] = -INFINITY;
-        }
-        float mx0 = s[0][0], mx1 = s[0][1];
-#pragma unroll
-        for (int i = 2; i < 128; i += 2) {
-          mx0 = fmaxf(mx0, s[i >> 6][i & 63]);
-          mx1 = fmaxf(mx1, s[i >> 6][(i & 63) + 1]);
-        }
-        const float mx = fmaxf(mx0, mx1) * sscale;
-        const bool grow = mx > m_used + C::kLazy;
-        float alpha = 1.f;
-        if (grow) {
-          alpha = fast_exp2(m_used - mx);  // 0 while the row has seen nothing
-          l *= alpha;
-          m_used = mx;
-        }
-        // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
-        const float negm = (m_used == -INFINITY ? 0.f : -m_used) + C::kBias;
-        const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pw[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 x = ffma2(make_float2(s[hf][2 * i], s[hf][2 * i + 1]), sc2, nm2);
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            sum = fadd2(sum, x);
-            pw[i] = pack16<FP8>(x.x, x.y);
-          }
-          tmem_st32u(scol + 32 * hf, pw);
-        }
-        l += sum.x + sum.y;
-        // P V of the previous step was issued before these scores: it is done
-        if (t > 0 && __any_sync(kFull, grow)) {
-#pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
-            float o[32];
-            tmem_ld32(ocol + 32 * ch, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(ocol + 32 * ch, o);
+            for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse != nullptr) p.lse[orow] = -INFINITY;
           }
         }
-        tmem_wait_st();
+        if (FP8 && st.nstep > 0) {  // the other tile's scores wait for both
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full);
+        }
+        if (st.nstep > 0 && lane == 0) atomicAdd(&sh.epilogues, 1);
+        continue;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[g]);
-    }
+      float sscale = p.score_scale;
 
-    // ---- epilogue: the output row, or its record
-    if (!dead && nloc > 0) {
-      const bool ok = wait_or_abort(&o_full[g], 0, abort);
-      if (!__all_sync(kFull, ok)) {
-        if (!*abort) fail();
-        dead = true;
-      }
-      tc_fence_after();
-    }
-    float* join = reinterpret_cast<float*>(smem + C::kOffRing);  // narrow: [D][128] of group 1
-    float2* join_ml = reinterpret_cast<float2*>(smem + C::kOffQ + C::kQTile);  // narrow: [128]
-    float a0 = 1.f, a1 = 0.f;
-    if constexpr (!WIDE) {
-      // every step of both groups is done before the ring is written over: group 1 finished
-      // its own, and group 0's last products were waited for above
-      dead = named_sync_or(2, 256, dead);
-      if (g == 1 && !dead && nloc > 0) {
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          float o[32];
-          tmem_ld32(ocol + 32 * ch, o);
+      if constexpr (FP8) {
+        // this row of Q as hi and lo codes, times 2^e that takes its largest into [128, 256); the
+        // tile is free: the group's last scores of the work before are done
+        if (WIDE || g == 0) {
+          const uint4* qr =
+              reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(w.tok0 + my_i) * p.q_stride + hq * D);
+          uint4 v[D / 8];
+          float top = 0.f;
+          bool odd = false;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) join[(32 * ch + i) * 128 + r] = o[i];
+          for (int c = 0; c < D / 8; ++c) {
+            v[c] = rv ? qr[c] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(e[k])), fabsf(bf16_hi(e[k]))));
+              odd |= ((((e[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u);
+            }
+          }
+          int ex = 0;
+          if (top > 0.f && !odd) ex = 7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+          ex = min(ex, 126);  // rows below 2^-119: their codes lose what lies under 2^-135
+          const float up = __uint_as_float(static_cast<uint32_t>(max(ex, -126) + 127) << 23);
+          const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {  // 16 codes: one 16-byte piece of the row
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a = u4_word(v[2 * c + k / 2], 2 * (k & 1)), b = u4_word(v[2 * c + k / 2], 2 * (k & 1) + 1);
+              float x[4] = {bf16_lo(a) * up, bf16_hi(a) * up, bf16_lo(b) * up, bf16_hi(b) * up};
+              hi[k] = e4m3x4_rest(x);
+              lo[k] = e4m3x4_rest(x);
+            }
+            const uint32_t at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+            st_shared_v4(qt + at, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(qt + C::kCodes + at, lo[0], lo[1], lo[2], lo[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full);
+          // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
+          sscale = odd ? __int_as_float(0x7fffffff) : sscale * p.scales[w.h] / up;
         }
-        join_ml[r] = make_float2(m_used, l);
+        if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
+          if (g == 0) join_scale[r] = sscale;
+          named_sync(2, 256);
+          if (g == 1) sscale = join_scale[r];
+        }
       }
-      named_sync(2, 256);
-      if (g == 0 && !dead && n_of[1] > 0) {
-        const float2 o = join_ml[r];
-        const float top = fmaxf(m_used, o.x);
-        a0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - top);
-        a1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - top);
-        l = l * a0 + o.y * a1;
+
+      const int my_lim = Steps<WIDE>::lim(w, p, my_i);
+      // keys below every lim of the warp's rows need no mask (rows that do not exist do not count)
+      const int warp_lim = __reduce_min_sync(kFull, rv ? my_lim : 0x7fffffff);
+      const bool idle = !__any_sync(kFull, rv);  // no row of the warp exists: its products go nowhere
+      float m_used = -INFINITY, l = 0.f;
+      for (int t = 0; t < nloc; ++t) {
+        const int key0 = (st.k0 + (WIDE ? t : 2 * t + g)) * C::kKeys;
+        const bool ok = wait_or_abort(&sh.s_full[g], (c_s + t) & 1, abort);
+        if (!__all_sync(kFull, ok)) {  // tensor-memory loads are warp-collective: leave as a warp
+          if (!*abort) fail();
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+        if (!idle) {
+          float s[2][64];
+          tmem_ld64(scol, s[0]);
+          tmem_ld64(scol + 64, s[1]);
+          if (key0 + C::kKeys > warp_lim) {
+            const int left = my_lim - key0;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= left) s[i >> 6][i & 63] = -INFINITY;
+          }
+          float mx0 = s[0][0], mx1 = s[0][1];
+#pragma unroll
+          for (int i = 2; i < 128; i += 2) {
+            mx0 = fmaxf(mx0, s[i >> 6][i & 63]);
+            mx1 = fmaxf(mx1, s[i >> 6][(i & 63) + 1]);
+          }
+          const float mx = fmaxf(mx0, mx1) * sscale;
+          const bool grow = mx > m_used + C::kLazy;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = fast_exp2(m_used - mx);  // 0 while the row has seen nothing
+            l *= alpha;
+            m_used = mx;
+          }
+          // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
+          const float negm = (m_used == -INFINITY ? 0.f : -m_used) + C::kBias;
+          const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pw[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float2 x = ffma2(make_float2(s[hf][2 * i], s[hf][2 * i + 1]), sc2, nm2);
+              x.x = exp2_ftz(x.x);
+              x.y = exp2_ftz(x.y);
+              sum = fadd2(sum, x);
+              pw[i] = pack16<FP8>(x.x, x.y);
+            }
+            tmem_st32u(scol + 32 * hf, pw);
+          }
+          l += sum.x + sum.y;
+          // P V of the previous step was issued before these scores: it is done
+          if (t > 0 && __any_sync(kFull, grow)) {
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float o[32];
+              tmem_ld32(ocol + D * g + 32 * ch, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(ocol + D * g + 32 * ch, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[g]);
+      }
+      c_s += nloc;
+
+      // ---- epilogue: the output row, or its record
+      if (!dead && nloc > 0) {
+        const bool ok = wait_or_abort(&sh.o_full[g], c_o & 1, abort);
+        if (!__all_sync(kFull, ok)) {
+          if (!*abort) fail();
+          dead = true;
+        }
+        ++c_o;
+        tc_fence_after();
+      }
+      // narrow: both groups' outputs are done and their statistics shared; each joins half of the
+      // columns (the other group's output is in the same TMEM lanes)
+      float a0 = 1.f, a1 = 0.f;
+      if constexpr (!WIDE) {
+        join_ml[g * 128 + r] = make_float2(m_used, l);
+        tc_fence_before();
+        dead = named_sync_or(2, 256, dead);
+        tc_fence_after();
+        const float2 x0 = join_ml[r], x1 = join_ml[128 + r];
+        const float top = fmaxf(x0.x, x1.x);
+        a0 = x0.x == -INFINITY ? 0.f : fast_exp2(x0.x - top);
+        a1 = x1.x == -INFINITY ? 0.f : fast_exp2(x1.x - top);
+        if (x0.y != x0.y || x1.y != x1.y) a0 = a1 = __int_as_float(0x7fffffff);
+        l = x0.y * a0 + x1.y * a1;
         m_used = top;
       }
-    }
-    if (!dead && nloc == 0 && WIDE) {  // a tile whose rows see nothing of this split
-      if (rv) {
-        if (p.splits > 1) {
-          p.part_ml[rec] = make_float2(-INFINITY, 0.f);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr) p.lse[orow] = -INFINITY;
+      if (!dead && !idle) {
+        const bool bad = *poisoned == static_cast<int>(n) + 1;
+        float inv = 1.f;
+        if (!split_out) {
+          inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          if constexpr (FP8) inv *= p.scales[p.hkv + w.h];
         }
-      }
-    } else if (!dead && (WIDE || g == 0) && !idle) {
-      const bool split_out = p.splits > 1;
-      const bool bad = *poisoned != 0;
-      float inv = 1.f;
-      if (!split_out) {
-        inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        if constexpr (FP8) inv *= p.scales[p.hkv + h];
-        if (rv && p.lse != nullptr)
-          p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
-      } else if (rv) {
-        p.part_ml[rec] = make_float2(m_used, l);
-      }
+        if (rv && (WIDE || g == 0)) {
+          if (split_out) p.part_ml[rec] = make_float2(m_used, l);
+          else if (p.lse != nullptr)
+            p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
+        }
+        constexpr int kMine = WIDE ? D : D / 2;  // columns of this group
+        const int col0 = WIDE ? 0 : g * kMine;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        float o[32];
-        tmem_ld32(ocol + 32 * ch, o);
-        if constexpr (!WIDE) {
-          if (n_of[1] > 0) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = o[i] * a0 + join[(32 * ch + i) * 128 + r] * a1;
-          }
-        }
-        if (bad) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int dim = 32 * ch + i;
-            if (poison[dim] < my_lim) o[i] = __int_as_float(0x7fffffff);
-            if (poison[D + dim] < my_lim) o[i] += INFINITY;
-            if (poison[2 * D + dim] < my_lim) o[i] -= INFINITY;
-          }
-        }
-        if (rv) {
-          if (split_out) {
-            float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * D + 32 * ch);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int ch = 0; ch < kMine / 32; ++ch) {
+          const int col = col0 + 32 * ch;
+          float o[32];
+          if constexpr (WIDE) {
+            tmem_ld32(ocol + D * g + col, o);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * ch);
+            tmem_ld32(ocol + col, o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            for (int i = 0; i < 32; ++i) o[i] *= a0;
+            if (st.n_of[1] > 0) {
+              float o1[32];
+              tmem_ld32(ocol + D + col, o1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], a1, o[i]);
+            }
+          }
+          if (bad) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int dim = col + i;
+              if (poison[dim] < my_lim) o[i] = __int_as_float(0x7fffffff);
+              if constexpr (!FP8) {
+                if (poison[D + dim] < my_lim) o[i] += INFINITY;
+                if (poison[2 * D + dim] < my_lim) o[i] -= INFINITY;
+              }
+            }
+          }
+          if (rv) {
+            if (split_out) {
+              float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * D + col);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            }
           }
         }
       }
+      tc_fence_before();
+      if constexpr (!WIDE) dead = named_sync_or(2, 256, dead);  // both are through with both outputs
+      __syncwarp();
+      __threadfence_block();
+      if (lane == 0) atomicAdd(&sh.epilogues, 1);
     }
   }
 
