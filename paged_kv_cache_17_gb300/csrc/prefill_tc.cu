@@ -81,7 +81,8 @@ struct PrefillCfg {
 struct PrefillShared {
   uint64_t full[8], empty[8];  // ring: tile landed, tile consumed
   uint64_t s_full[2];          // scores of a step done (and every product issued before)
-  uint64_t p_full[2];          // weights of a step written (one arrival per warp)
+  uint64_t p_half[2];          // weights of a step's first 64 keys written, output rescaled (one arrival per warp)
+  uint64_t p_full[2];          // all weights of a step written
   uint64_t o_full[2];          // every product of the group's work done
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
@@ -101,21 +102,104 @@ static_assert(sizeof(PrefillShared) <= 512, "shared state");
 
 namespace {
 
-// descriptor of an operand in shared memory with 128-byte (sw = 2) or 64-byte (sw = 4) swizzle
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint64_t sw) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (sw << 61);
+// Shared-memory descriptors as two words (see tc_ops.cuh for the fields).  The high word is a
+// constant of the operand; the low word is the address >> 4 plus the leading offset, so the
+// K slices of an operand differ by an added constant.  The issuing warp computes them as a warp, so
+// that they stay in uniform registers, and only the MMA itself is left to the elected lane: issued
+// from a branch of one lane, each MMA took 70 cycles of moves between register files, more than it
+// executes (64), and the step 4170 cycles for 2050 of products.
+constexpr uint32_t kDescK128 = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, 128-byte swizzle
+constexpr uint32_t kDescK64 = (512u >> 4) | (1u << 14) | (4u << 29);    // stride 512, 64-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
 }
 
-// D[tmem] = A[smem] B[smem] (+ D) for 8-bit operands (E4M3: formats 0 in the descriptor)
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// D[tmem] (+)= A[smem] B[smem]: 16-bit operands, or 8-bit ones (E4M3: formats 0 in the
+// descriptor); D[tmem] (+)= A[tmem] B[smem], 16-bit operands.  Called by the whole warp; the lane
+// with leader != 0 issues.
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       bool accumulate, uint32_t leader) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       bool accumulate, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
       : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// One arrival on bar once every tcgen05 operation the leader issued before has completed.
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
+// 128 consecutive columns of this thread's lane in one load; the wait is inside.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 consecutive columns of this thread's lane; the waits are inside.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -259,6 +343,7 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 4);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.exp_free[i], 1);
@@ -307,47 +392,53 @@ __global__ void __launch_bounds__(384, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == C::kIssuerWarp) {
     // ======================================================================== MMA issuer
-    if (lane == 0) {
+    const uint32_t leader = elect_one();
+    {
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_or_abort(bar, parity, abort)); };
+      auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
       constexpr uint32_t kIdO = idesc_f16(C::kRows, D, !FP8, true);
       // scores: A = Q with its sign turned (bit 13) for a negative scale; E4M3 formats are 0
       const uint32_t id_s = (FP8 ? idesc_f16(C::kRows, C::kKeys, false, false)
                                  : idesc_f16(C::kRows, C::kKeys, true, false)) |
                             (p.negate ? 1u << 13 : 0u);
+      const uint32_t tm = same(tmem);
       auto issue_s = [&](int g, unsigned item) {
-        const uint32_t kt = ring + (item % NS) * C::kSlot;
-        const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
-        const uint32_t d = tmem + C::kColS + 128 * g;
+        const uint32_t k_lo = same(desc_lo(ring + (item % NS) * C::kSlot, 16));
+        const uint32_t q_lo = same(desc_lo(q_base + (WIDE ? g : 0) * C::kQTile, 16));
+        const uint32_t d = tm + C::kColS + 128 * g;
         if constexpr (FP8) {
-          constexpr uint64_t sw = D == 128 ? 2 : 4;
+          constexpr uint32_t hi = D == 128 ? kDescK128 : kDescK64;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-              mma_f8_ss(d, sdesc(qt + part * C::kCodes + kk * 32, 16, 8 * D, sw), sdesc(kt + kk * 32, 16, 8 * D, sw),
-                        id_s, (part > 0 || kk > 0) ? 1u : 0u);
+              mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, hi, id_s, part > 0 || kk > 0,
+                           leader);
         } else {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = (kk >> 2) * C::kHalf16 + (kk & 3) * 32;
-            mma_f16_ss(d, sdesc_sw128(qt + at, 16, 1024), sdesc_sw128(kt + at, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+            const uint32_t at = ((kk >> 2) * C::kHalf16 + (kk & 3) * 32) / 16;
+            mma_ss<false>(d, q_lo + at, k_lo + at, kDescK128, id_s, kk > 0, leader);
           }
         }
-        tc_commit(&sh.s_full[g]);
+        commit(&sh.s_full[g], leader);
       };
-      auto issue_o = [&](int g, int t, uint32_t vt) {
-        const uint32_t pt = tmem + C::kColS + 128 * g;
+      // keys 64 part .. of a step
+      auto issue_o = [&](int g, int t, uint32_t vt, int part) {
+        const uint32_t pt = tm + C::kColS + 128 * g + 32 * part;
+        const uint32_t v_lo = same(desc_lo(vt + part * 8192, C::kHalf16));
 #pragma unroll
-        for (int kk = 0; kk < C::kKeys / 16; ++kk)
-          mma_f16_ts(tmem + C::kColO + D * g, pt + 8 * kk, sdesc_sw128(vt + kk * 2048, C::kHalf16, 1024), kIdO,
-                     (t > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < C::kKeys / 32; ++kk)
+          mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, t > 0 || part > 0 || kk > 0,
+                 leader);
       };
-      auto wait_full = [&](unsigned item) { return wait_or_abort(&sh.full[item % NS], (item / NS) & 1, abort); };
+      auto wait_full = [&](unsigned item) { return wait(&sh.full[item % NS], (item / NS) & 1); };
 
       unsigned base = 0, steps_done = 0, cuts = 0, q_count = 0;
       unsigned c_p[2] = {0, 0};  // steps of the groups so far
       bool ok = true;
       Work w;
-      for (unsigned n = 0; ok && next_work(n, w, 1u); ++n) {
+      for (unsigned n = 0; ok && next_work(n, w); ++n) {
         const Steps<WIDE> st(w, p, tile_tok);
         const int nstep = st.nstep;
         if (nstep == 0) continue;
@@ -355,11 +446,11 @@ __global__ void __launch_bounds__(384, 1)
         auto wait_v = [&](int j) {
           if constexpr (FP8) {
             const unsigned v = steps_done + j;
-            return wait_or_abort(&sh.fixed[v & 1], (v >> 1) & 1, abort);
+            return wait(&sh.fixed[v & 1], (v >> 1) & 1);
           }
           if (j >= st.first_cut) {
             const unsigned c = cuts + j - st.first_cut;
-            return wait_or_abort(&sh.fixed[c & 7], (c >> 3) & 1, abort);
+            return wait(&sh.fixed[c & 7], (c >> 3) & 1);
           }
           return wait_full(base + st.v_item(j));
         };
@@ -368,10 +459,10 @@ __global__ void __launch_bounds__(384, 1)
                      : ring + ((base + st.v_item(j)) % NS) * C::kSlot;
         };
         auto free_v = [&](int j) {
-          tc_commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[(base + st.v_item(j)) % NS]);
+          commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[(base + st.v_item(j)) % NS], leader);
         };
         auto k_item = [&](int j) { return base + st.k_item(j); };
-        ok = wait_or_abort(&sh.q_full, q_count & 1, abort);
+        ok = wait(&sh.q_full, q_count & 1);
         ++q_count;
         if constexpr (WIDE) {
           // step j of both tiles: S of step j + 1 follows P V of step j in the same columns, in
@@ -381,19 +472,23 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             if (st.n_of[0] > 0) issue_s(0, k_item(0));
             if (st.n_of[1] > 0) issue_s(1, k_item(0));
-            tc_commit(&sh.empty[k_item(0) % NS]);
-            if (nstep == 1) tc_commit(&sh.q_empty);
+            commit(&sh.empty[k_item(0) % NS], leader);
+            if (nstep == 1) commit(&sh.q_empty, leader);
           }
           for (int j = 0; j < nstep && ok; ++j) {
             bool k_ready = false;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (ok && j < st.n_of[g]) {
-                ok = wait_or_abort(&sh.p_full[g], (c_p[g] + j) & 1, abort) && wait_v(j);
+                ok = wait(&sh.p_half[g], (c_p[g] + j) & 1) && wait_v(j);
                 if (!ok) break;
                 tc_fence_after();
-                issue_o(g, j, v_tile(j));
-                if (j + 1 == st.n_of[g]) tc_commit(&sh.o_full[g]);
+                issue_o(g, j, v_tile(j), 0);
+                ok = wait(&sh.p_full[g], (c_p[g] + j) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_o(g, j, v_tile(j), 1);
+                if (j + 1 == st.n_of[g]) commit(&sh.o_full[g], leader);
               }
               if (g == 1) free_v(j);
               if (ok && j + 1 < st.n_of[g]) {
@@ -405,8 +500,8 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
             if (ok && j + 1 < nstep) {
-              tc_commit(&sh.empty[k_item(j + 1) % NS]);
-              if (j + 2 == nstep) tc_commit(&sh.q_empty);
+              commit(&sh.empty[k_item(j + 1) % NS], leader);
+              if (j + 2 == nstep) commit(&sh.q_empty, leader);
             }
           }
         } else {
@@ -415,24 +510,28 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             tc_fence_after();
             issue_s(j, k_item(j));
-            tc_commit(&sh.empty[k_item(j) % NS]);
-            if (j + 1 == nstep) tc_commit(&sh.q_empty);
+            commit(&sh.empty[k_item(j) % NS], leader);
+            if (j + 1 == nstep) commit(&sh.q_empty, leader);
           }
           for (int j = 0; j < nstep && ok; ++j) {
             const int g = j & 1, t = j >> 1;
-            ok = wait_or_abort(&sh.p_full[g], (c_p[g] + t) & 1, abort) && wait_v(j);
+            ok = wait(&sh.p_half[g], (c_p[g] + t) & 1) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_o(g, t, v_tile(j));
+            issue_o(g, t, v_tile(j), 0);
+            ok = wait(&sh.p_full[g], (c_p[g] + t) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(g, t, v_tile(j), 1);
             free_v(j);
-            if (j + 2 >= nstep) tc_commit(&sh.o_full[g]);
+            if (j + 2 >= nstep) commit(&sh.o_full[g], leader);
             if (j + 2 < nstep) {
               ok = wait_full(k_item(j + 2));
               if (!ok) break;
               tc_fence_after();
               issue_s(g, k_item(j + 2));
-              tc_commit(&sh.empty[k_item(j + 2) % NS]);
-              if (j + 3 == nstep) tc_commit(&sh.q_empty);
+              commit(&sh.empty[k_item(j + 2) % NS], leader);
+              if (j + 3 == nstep) commit(&sh.q_empty, leader);
             }
           }
         }
@@ -442,9 +541,9 @@ __global__ void __launch_bounds__(384, 1)
         c_p[0] += st.n_of[0];
         c_p[1] += st.n_of[1];
       }
-      if (!ok && !*abort) fail();
+      if (!ok && !*abort && lane == 0) fail();
       // nothing may run on the tensor cores when the CTA frees its tensor memory
-      tc_commit(&sh.drain);
+      commit(&sh.drain, leader);
       mbar_wait(&sh.drain, 0);
     }
     __syncwarp();
@@ -857,59 +956,67 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc_fence_after();
         if (!idle) {
-          float s[2][64];
-          tmem_ld64(scol, s[0]);
-          tmem_ld64(scol + 64, s[1]);
+          float s[128];
+          tmem_ld128(scol, s);
           if (key0 + C::kKeys > warp_lim) {
             const int left = my_lim - key0;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
-              if (i >= left) s[i >> 6][i & 63] = -INFINITY;
+              if (i >= left) s[i] = -INFINITY;
           }
-          float mx0 = s[0][0], mx1 = s[0][1];
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 2; i < 128; i += 2) {
-            mx0 = fmaxf(mx0, s[i >> 6][i & 63]);
-            mx1 = fmaxf(mx1, s[i >> 6][(i & 63) + 1]);
+          for (int i = 4; i < 124; i += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
           }
-          const float mx = fmaxf(mx0, mx1) * sscale;
-          const bool grow = mx > m_used + C::kLazy;
+          const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(fmaxf(s[124], s[125]), s[126], s[127])) * sscale;
+          const bool grow = top > m_used + C::kLazy;
           float alpha = 1.f;
           if (grow) {
-            alpha = fast_exp2(m_used - mx);  // 0 while the row has seen nothing
+            alpha = fast_exp2(m_used - top);  // 0 while the row has seen nothing
             l *= alpha;
-            m_used = mx;
+            m_used = top;
+          }
+          // P V of the previous step was issued before these scores: it is done
+          if (t > 0 && __any_sync(kFull, grow)) {
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+              float o[16];
+              tmem_ld16(ocol + D * g + 16 * ch, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st16(ocol + D * g + 16 * ch, o);
+            }
           }
           // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
           const float negm = (m_used == -INFINITY ? 0.f : -m_used) + C::kBias;
           const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
-          float2 sum = make_float2(0.f, 0.f);
+          float2 sum[4] = {};
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t pw[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              float2 x = ffma2(make_float2(s[hf][2 * i], s[hf][2 * i + 1]), sc2, nm2);
+              float2 x = ffma2(make_float2(s[64 * hf + 2 * i], s[64 * hf + 2 * i + 1]), sc2, nm2);
               x.x = exp2_ftz(x.x);
               x.y = exp2_ftz(x.y);
-              sum = fadd2(sum, x);
+              sum[i & 3] = fadd2(sum[i & 3], x);
               pw[i] = pack16<FP8>(x.x, x.y);
             }
             tmem_st32u(scol + 32 * hf, pw);
-          }
-          l += sum.x + sum.y;
-          // P V of the previous step was issued before these scores: it is done
-          if (t > 0 && __any_sync(kFull, grow)) {
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              float o[32];
-              tmem_ld32(ocol + D * g + 32 * ch, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(ocol + D * g + 32 * ch, o);
+            tmem_wait_st();
+            if (hf == 0) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.p_half[g]);
             }
           }
-          tmem_wait_st();
+          sum[0] = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[g]);
         }
         tc_fence_before();
         __syncwarp();
