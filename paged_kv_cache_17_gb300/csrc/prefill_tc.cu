@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 
 #include "mma_ops.cuh"
 #include "pkv_device.cuh"
@@ -70,8 +71,13 @@ struct PrefillCfg {
   // 1008: alignment slack (the start of dynamic shared memory is 16-byte aligned)
   static constexpr int kBytes = 1008 + kOffPoison + kKinds * D * 4;
   static constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
-  static constexpr int kThreads = 384;
-  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kFixWarp0 = 10;
+  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kIssuer2Warp = 10, kFixWarp0 = FP8 ? 12 : 11;
+  static constexpr int kFixWarps = FP8 ? 4 : 1;
+  static constexpr int kThreads = (kFixWarp0 + kFixWarps) * 32;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;           // per thread
+  static constexpr int kSoftRegs = 208;
+  static constexpr int kAuxRegs = (kLaunchRegs * kThreads - kSoftRegs * 256) / (kThreads - 256) / 8 * 8;
+  static_assert(kSoftRegs * 256 + kAuxRegs * (kThreads - 256) <= kLaunchRegs * kThreads, "register split");
   static constexpr float kLazy = 8.f;
   static constexpr float kBias = FP8 ? kPrefillWeightBias : 0.f;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -81,8 +87,7 @@ struct PrefillCfg {
 struct PrefillShared {
   uint64_t full[8], empty[8];  // ring: tile landed, tile consumed
   uint64_t s_full[2];          // scores of a step done (and every product issued before)
-  uint64_t p_half[2];          // weights of a step's first 64 keys written, output rescaled (one arrival per warp)
-  uint64_t p_full[2];          // all weights of a step written
+  uint64_t p_full[2];          // weights of a step written (an arrival per warp; wide: and the other tile's turn over)
   uint64_t o_full[2];          // every product of the group's work done
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
@@ -90,7 +95,7 @@ struct PrefillShared {
   uint64_t q_full, q_empty;
   uint64_t work_full[2], work_empty[2];
   uint64_t clc;                // answer of the work query landed
-  uint64_t drain;              // every MMA issued so far done
+  uint64_t drain[2];           // every MMA that an issuer has issued done
   alignas(16) uint4 clc_answer;
   int4 work[2][2];
   uint32_t tmem;
@@ -238,6 +243,10 @@ __device__ __forceinline__ uint32_t e4m3x4_rest(float (&x)[4]) {
   return w;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // Ask for the next CTA of the grid that has not started, to do its work here; the 16-byte
 // answer lands in shared memory and completes on the barrier.
 __device__ __forceinline__ void clc_ask(uint4* answer, uint64_t* bar) {
@@ -265,6 +274,17 @@ __device__ __forceinline__ bool clc_read(const uint4* answer, uint32_t& x, uint3
   return ok != 0;
 }
 
+// One box of a 3-D tensor into shared memory, issued by the leader of the calling warp
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar,
+                                        uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(leader)
+      : "memory");
+}
+
 // 2^x by the hardware approximation, subnormal results flushed to zero
 __device__ __forceinline__ float exp2_ftz(float x) {
   float y;
@@ -280,6 +300,24 @@ struct Work {
   int ctx;    // cached tokens
   int shift;  // causal: the work's token i sees keys < shift + i + 1
   int h, split;
+};
+
+// A position in the ring and the parity of its round
+template <int N>
+struct Cursor {
+  unsigned slot, phase;
+  __device__ __forceinline__ void advance(unsigned k) {  // k < N
+    slot += k;
+    if (slot >= N) {
+      slot -= N;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void advance_by(unsigned k) {
+    slot += k;
+    phase ^= (slot / N) & 1;
+    slot %= N;
+  }
 };
 
 template <bool WIDE>
@@ -312,7 +350,7 @@ struct Steps {
 }  // namespace
 
 template <int D, bool FP8, bool WIDE>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
   using C = PrefillCfg<D, FP8>;
@@ -325,6 +363,7 @@ __global__ void __launch_bounds__(384, 1)
   int* poison = reinterpret_cast<int*>(smem + C::kOffPoison);  // [kinds][D] first key with such a value
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kIssuers = WIDE ? 2 : 1;
   const int G = p.group;
   const int tile_tok = C::kRows / G;                   // tokens of a 128-row tile
   const int cta_tok = WIDE ? 2 * tile_tok : tile_tok;  // tokens of a work
@@ -337,23 +376,23 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == C::kIssuerWarp * 32) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.empty[i], kIssuers);
       mbar_init(&sh.fixed[i], 1);
       mbar_init(&sh.v_sent[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_half[i], 4);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], WIDE ? 5 : 4);
       mbar_init(&sh.o_full[i], 1);
-      mbar_init(&sh.exp_free[i], 1);
+      mbar_init(&sh.exp_free[i], kIssuers);
       mbar_init(&sh.work_full[i], 1);
-      mbar_init(&sh.work_empty[i], 11);  // the issuer, warps 10 and 11, 8 softmax warps
+      mbar_init(&sh.work_empty[i], kIssuers + C::kFixWarps + 8);  // one arrival per warp that reads it
     }
     mbar_init(&sh.q_full, FP8 ? (WIDE ? 8 : 4) : 1);
-    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.q_empty, kIssuers);
     mbar_init(&sh.clc, 1);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     sh.abort = 0;
     sh.poisoned = 0;
     sh.epilogues = 0;
@@ -387,13 +426,15 @@ __global__ void __launch_bounds__(384, 1)
     return w.seq >= 0;
   };
 
-  // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+  // the registers of the launch, dealt out anew: 208 to the softmax threads
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == C::kIssuerWarp) {
-    // ======================================================================== MMA issuer
-    const uint32_t leader = elect_one();
-    {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
+  if (warp == C::kIssuerWarp || warp == C::kIssuer2Warp) {
+    // ======================================================================== MMA issuers
+    // wide: one warp per tile, each going through every step of K and V in order; narrow: one warp
+    // for both groups
+    if (warp == C::kIssuerWarp || WIDE) {
+      const uint32_t leader = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_or_abort(bar, parity, abort)); };
       auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
       constexpr uint32_t kIdO = idesc_f16(C::kRows, D, !FP8, true);
@@ -402,9 +443,12 @@ __global__ void __launch_bounds__(384, 1)
                                  : idesc_f16(C::kRows, C::kKeys, true, false)) |
                             (p.negate ? 1u << 13 : 0u);
       const uint32_t tm = same(tmem);
-      auto issue_s = [&](int g, unsigned item) {
-        const uint32_t k_lo = same(desc_lo(ring + (item % NS) * C::kSlot, 16));
-        const uint32_t q_lo = same(desc_lo(q_base + (WIDE ? g : 0) * C::kQTile, 16));
+      const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, C::kHalf16));
+      const uint32_t exp_v_lo = same(desc_lo(smem_u32(smem + C::kOffExp), C::kHalf16));
+      const uint32_t q0_lo = same(desc_lo(q_base, 16));
+      auto issue_s = [&](int g, unsigned slot) {
+        const uint32_t k_lo = same(ring_lo + slot * (C::kSlot / 16));
+        const uint32_t q_lo = q0_lo + (WIDE ? g : 0) * (C::kQTile / 16);
         const uint32_t d = tm + C::kColS + 128 * g;
         if constexpr (FP8) {
           constexpr uint32_t hi = D == 128 ? kDescK128 : kDescK64;
@@ -423,18 +467,16 @@ __global__ void __launch_bounds__(384, 1)
         }
         commit(&sh.s_full[g], leader);
       };
-      // keys 64 part .. of a step
-      auto issue_o = [&](int g, int t, uint32_t vt, int part) {
-        const uint32_t pt = tm + C::kColS + 128 * g + 32 * part;
-        const uint32_t v_lo = same(desc_lo(vt + part * 8192, C::kHalf16));
+      auto issue_o = [&](int g, bool first, uint32_t v_lo0) {
+        const uint32_t pt = tm + C::kColS + 128 * g;
+        const uint32_t v_lo = same(v_lo0);
 #pragma unroll
-        for (int kk = 0; kk < C::kKeys / 32; ++kk)
-          mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, t > 0 || part > 0 || kk > 0,
-                 leader);
+        for (int kk = 0; kk < C::kKeys / 16; ++kk)
+          mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, !first || kk > 0, leader);
       };
-      auto wait_full = [&](unsigned item) { return wait(&sh.full[item % NS], (item / NS) & 1); };
 
-      unsigned base = 0, steps_done = 0, cuts = 0, q_count = 0;
+      Cursor<C::kSlots> base{0, 0};  // ring position of the work's first tile
+      unsigned steps_done = 0, cuts = 0, q_count = 0;
       unsigned c_p[2] = {0, 0};  // steps of the groups so far
       bool ok = true;
       Work w;
@@ -442,100 +484,110 @@ __global__ void __launch_bounds__(384, 1)
         const Steps<WIDE> st(w, p, tile_tok);
         const int nstep = st.nstep;
         if (nstep == 0) continue;
+        Cursor<C::kSlots> kc = base, vc = base;
+        vc.advance(nstep == 1 ? 1 : 2);
+        auto next_k = [&](int j) { kc.advance(j == 0 ? 1 : 2); };               // from K of step j to the next
+        auto next_v = [&](int j) { vc.advance(j + 2 == nstep ? 1 : 2); };       // from V of step j to the next
+        auto wait_k = [&]() { return wait(&sh.full[kc.slot], kc.phase); };
         // V of step j is ready for the tensor cores
         auto wait_v = [&](int j) {
           if constexpr (FP8) {
             const unsigned v = steps_done + j;
             return wait(&sh.fixed[v & 1], (v >> 1) & 1);
+          } else {
+            if (j >= st.first_cut) {
+              const unsigned c = cuts + j - st.first_cut;
+              return wait(&sh.fixed[c & 7], (c >> 3) & 1);
+            }
+            return wait(&sh.full[vc.slot], vc.phase);
           }
-          if (j >= st.first_cut) {
-            const unsigned c = cuts + j - st.first_cut;
-            return wait(&sh.fixed[c & 7], (c >> 3) & 1);
-          }
-          return wait_full(base + st.v_item(j));
         };
-        auto v_tile = [&](int j) {
-          return FP8 ? smem_u32(smem + C::kOffExp + ((steps_done + j) & 1) * C::kTile16)
-                     : ring + ((base + st.v_item(j)) % NS) * C::kSlot;
+        auto v_lo = [&](int j) {
+          return FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16) : ring_v_lo + vc.slot * (C::kSlot / 16);
         };
-        auto free_v = [&](int j) {
-          commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[(base + st.v_item(j)) % NS], leader);
-        };
-        auto k_item = [&](int j) { return base + st.k_item(j); };
+        auto free_v = [&](int j) { commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader); };
         ok = wait(&sh.q_full, q_count & 1);
         ++q_count;
         if constexpr (WIDE) {
-          // step j of both tiles: S of step j + 1 follows P V of step j in the same columns, in
-          // issue order
-          if (ok) ok = wait_full(k_item(0));
+          // The scores of step j + 1 follow P V of step j in the same columns, in issue order.  The
+          // tiles take turns, so that one's products run under the other's softmax (left to themselves
+          // they fell into step and waited for the tensor cores together: 1681 against 1508 us for
+          // 4096 tokens over 32768, 32 heads).  The fifth arrival on p_full is the other issuer's, once its
+          // turn before is over: on tile 0's for a work's first step when tile 1 is through with the work
+          // before, then after tile 1's step before; on tile 1's after tile 0's same step, or, past
+          // tile 0's last, issuer 1's own.  A tile 1 without steps watches tile 0's instead.  So no
+          // arrival comes before the phase it belongs to: whoever arrives has seen the one before.
+          // Steps past the tile's own are waited for all the same: a slot's phases are seen in order.
+          const int g = warp == C::kIssuerWarp ? 0 : 1;
+          const int mine = g == 0 ? st.n_of[0] : st.n_of[1], other = g == 0 ? st.n_of[1] : st.n_of[0];
+          unsigned parity = (g == 0 ? c_p[0] : c_p[1]) & 1;
+          if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_full[0]);
+          ok = ok && wait_k();
           if (ok) {
             tc_fence_after();
-            if (st.n_of[0] > 0) issue_s(0, k_item(0));
-            if (st.n_of[1] > 0) issue_s(1, k_item(0));
-            commit(&sh.empty[k_item(0) % NS], leader);
+            if (mine > 0) issue_s(g, kc.slot);
+            commit(&sh.empty[kc.slot], leader);
             if (nstep == 1) commit(&sh.q_empty, leader);
           }
           for (int j = 0; j < nstep && ok; ++j) {
-            bool k_ready = false;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (ok && j < st.n_of[g]) {
-                ok = wait(&sh.p_half[g], (c_p[g] + j) & 1) && wait_v(j);
-                if (!ok) break;
-                tc_fence_after();
-                issue_o(g, j, v_tile(j), 0);
-                ok = wait(&sh.p_full[g], (c_p[g] + j) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_o(g, j, v_tile(j), 1);
-                if (j + 1 == st.n_of[g]) commit(&sh.o_full[g], leader);
-              }
-              if (g == 1) free_v(j);
-              if (ok && j + 1 < st.n_of[g]) {
-                if (!k_ready) ok = wait_full(k_item(j + 1));
-                if (!ok) break;
-                k_ready = true;
-                tc_fence_after();
-                issue_s(g, k_item(j + 1));
-              }
+            const bool more = j + 1 < nstep;
+            ok = wait_v(j);
+            if (more && ok) {
+              next_k(j);
+              ok = wait_k();
             }
-            if (ok && j + 1 < nstep) {
-              commit(&sh.empty[k_item(j + 1) % NS], leader);
-              if (j + 2 == nstep) commit(&sh.q_empty, leader);
+            if (!ok) break;
+            if (j < mine) {
+              if (g == 1 && j >= other && leader) mbar_arrive(&sh.p_full[1]);
+              ok = wait(&sh.p_full[g], parity);
+              if (!ok) break;
+              parity ^= 1;
+              tc_fence_after();
+              issue_o(g, j == 0, v_lo(j));
+              if (j + 1 < mine) issue_s(g, kc.slot);
+              else commit(&sh.o_full[g], leader);
+              if ((g == 0 ? j < other : j + 1 < other) && leader) mbar_arrive(&sh.p_full[g ^ 1]);
+            } else if (g == 1 && mine == 0 && j < other) {
+              ok = wait(&sh.p_full[0], (c_p[0] + j) & 1);
+              if (!ok) break;
+              if (j + 1 < other && leader) mbar_arrive(&sh.p_full[0]);
             }
+            free_v(j);
+            next_v(j);
+            if (more) commit(&sh.empty[kc.slot], leader);
+            if (j + 2 == nstep) commit(&sh.q_empty, leader);
           }
         } else {
           for (int j = 0; j < min(2, nstep) && ok; ++j) {
-            ok = wait_full(k_item(j));
+            if (j > 0) next_k(j - 1);
+            ok = wait_k();
             if (!ok) break;
             tc_fence_after();
-            issue_s(j, k_item(j));
-            commit(&sh.empty[k_item(j) % NS], leader);
+            issue_s(j, kc.slot);
+            commit(&sh.empty[kc.slot], leader);
             if (j + 1 == nstep) commit(&sh.q_empty, leader);
           }
           for (int j = 0; j < nstep && ok; ++j) {
             const int g = j & 1, t = j >> 1;
-            ok = wait(&sh.p_half[g], (c_p[g] + t) & 1) && wait_v(j);
+            ok = wait(&sh.p_full[g], ((g == 0 ? c_p[0] : c_p[1]) + t) & 1) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_o(g, t, v_tile(j), 0);
-            ok = wait(&sh.p_full[g], (c_p[g] + t) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(g, t, v_tile(j), 1);
+            issue_o(g, t == 0, v_lo(j));
             free_v(j);
+            next_v(j);
             if (j + 2 >= nstep) commit(&sh.o_full[g], leader);
             if (j + 2 < nstep) {
-              ok = wait_full(k_item(j + 2));
+              next_k(j + 1);
+              ok = wait_k();
               if (!ok) break;
               tc_fence_after();
-              issue_s(g, k_item(j + 2));
-              commit(&sh.empty[k_item(j + 2) % NS], leader);
+              issue_s(g, kc.slot);
+              commit(&sh.empty[kc.slot], leader);
               if (j + 3 == nstep) commit(&sh.q_empty, leader);
             }
           }
         }
-        base += 2 * nstep;
+        base.advance_by(2 * nstep);
         steps_done += nstep;
         cuts += nstep - st.first_cut;
         c_p[0] += st.n_of[0];
@@ -543,24 +595,30 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok && !*abort && lane == 0) fail();
       // nothing may run on the tensor cores when the CTA frees its tensor memory
-      commit(&sh.drain, leader);
-      mbar_wait(&sh.drain, 0);
+      commit(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], leader);
+      mbar_wait(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], 0);
     }
     __syncwarp();
   } else if (warp == C::kProducerWarp) {
     // ======================================================================== work and TMA producer
-    // bf16 at D = 128: lane 2 b + half takes half of block b; else lane b takes block b
-    constexpr int kPer = FP8 ? 1 : C::kHalves;
-    const bool loads = lane < C::kStepBlocks * kPer;
-    const int blk = lane / kPer, hf = lane % kPer;
+    // lane b < 8 knows the pool row of block b of a step; the warp goes through the blocks as one
+    // and the elected lane issues each box (16 lanes issuing their own took 100 cycles a box)
+    const uint32_t leader = elect_one();
     auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row) {
-      const unsigned st = item % NS;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
+      const unsigned st = __shfl_sync(kFull, item % NS, 0);
+      const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * C::kSlot;
+      if (leader) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
       __syncwarp();
-      if (loads) {
-        uint8_t* dst = smem + C::kOffRing + st * C::kSlot;
-        if constexpr (FP8) tma_load_3d(dst + blk * kBlockSize * D, tm, 0, head, row, &sh.full[st]);
-        else tma_load_3d(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, row, &sh.full[st]);
+#pragma unroll
+      for (int blk = 0; blk < C::kStepBlocks; ++blk) {
+        const int r = __shfl_sync(kFull, row, blk);
+        if constexpr (FP8) {
+          tma_box(dst + blk * kBlockSize * D, tm, 0, head, r, bar, leader);
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+            tma_box(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, r, bar, leader);
+        }
       }
     };
     auto slot_free = [&](unsigned item) {
@@ -638,19 +696,20 @@ __global__ void __launch_bounds__(384, 1)
         if (ok && nstep > 0) {
           const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
           const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
-          // pool row of this lane's block in step j; a block past the context, or with an id
-          // outside the pool, becomes a box entirely outside the tensor, which reads zeros
-          auto row_of = [&](int j) {
-            int row = -kBlockSize;
-            const int at = (st.k0 + j) * C::kStepBlocks + blk;
-            if (loads && j < nstep && at < nblk) {
-              const int id = table[at];
-              if (id >= 0 && id < p.num_blocks) row = id * kBlockSize;
-              else set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
-            }
-            return row;
+          // id of this lane's block in step j, asked for two steps ahead of its use: INT_MIN for a block
+          // past the context; its pool row: a block past the context, or with an id outside the
+          // pool, becomes a box entirely outside the tensor, which reads zeros
+          auto id_of = [&](int j) {
+            const int at = (st.k0 + j) * C::kStepBlocks + lane;
+            return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldg(table + at) : INT_MIN;
           };
-          int cur = row_of(0), nxt = row_of(1), ahead = row_of(2);
+          auto row_of = [&](int id) {
+            if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
+            if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
+            return -kBlockSize;
+          };
+          int cur = row_of(id_of(0)), nxt = row_of(id_of(1));
+          int id2 = id_of(2), id3 = id_of(3);
           if constexpr (!FP8) {
             // Q's tiles are free once the last scores of the work before are done
             if (q_count > 0) ok = wait_or_abort(&sh.q_empty, (q_count - 1) & 1, abort);
@@ -681,8 +740,9 @@ __global__ void __launch_bounds__(384, 1)
             if (lane == 0 && (FP8 || j >= st.first_cut))
               mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
             cur = nxt;
-            nxt = ahead;
-            ahead = row_of(j + 3);
+            nxt = row_of(id2);
+            id2 = id3;
+            id3 = id_of(j + 4);
           }
           base = ok ? base + 2 * nstep : issued;
           steps_done += nstep;
@@ -714,23 +774,24 @@ __global__ void __launch_bounds__(384, 1)
       if (!FP8 && q_count > 0) mbar_wait(&sh.q_full, (q_count - 1) & 1);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= C::kFixWarp0) {
     // ======================================================================== V: cut tiles, expansion
-    const int ft = threadIdx.x - C::kFixWarp0 * 32;  // 0 .. 63
+    constexpr int kFix = C::kFixWarps * 32;
+    const int ft = threadIdx.x - C::kFixWarp0 * 32;
     unsigned number = 0;
     auto note = [&](int kind, int dim, int key) {
       atomicMin(&poison[kind * D + dim], key);
       *poisoned = static_cast<int>(number) + 1;
     };
     constexpr int kChunks = D / 8;  // 8-element pieces of a row
-    constexpr int kStep = 64 / kChunks;
+    constexpr int kStep = kFix / kChunks;
     const int c = ft % kChunks, r0 = ft / kChunks;
     unsigned base = 0, steps_done = 0, cuts = 0, with_steps = 0;
     bool ok = true;
     Work w;
     for (unsigned n = 0; ok; ++n) {
-      // both warps leave together
-      if (named_sync_or(1, 64, !next_work(n, w))) break;
+      // the warps leave together
+      if (named_sync_or(1, kFix, !next_work(n, w))) break;
       number = n;
       const Steps<WIDE> st(w, p, tile_tok);
       const int nstep = st.nstep;
@@ -750,11 +811,11 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         const bool any = *poisoned != 0;
-        named_sync(3, 64);
+        named_sync(3, kFix);
         if (any) {
-          for (int i = ft; i < C::kKinds * D; i += 64) poison[i] = 0x7fffffff;
+          for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
           *poisoned = 0;
-          named_sync(3, 64);
+          named_sync(3, kFix);
         }
       };
       for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
@@ -824,13 +885,13 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         fence_proxy_async_smem();  // the tile is read by the tensor cores
-        if (named_sync_or(1, 64, *abort != 0)) {
+        if (named_sync_or(1, kFix, *abort != 0)) {
           ok = false;
           break;
         }
         if (ft == 0) {
           if constexpr (FP8) {
-            mbar_arrive(&sh.empty[item % NS]);
+            mbar_arrive_n(&sh.empty[item % NS], kIssuers);  // what both issuers would arrive
             mbar_arrive(&sh.fixed[sent & 1]);
           } else {
             mbar_arrive(&sh.fixed[sent & 7]);
@@ -844,7 +905,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ======================================================================== softmax
     const int g = warp >> 2;               // accumulators: the tile (wide) or the parity of the steps (narrow)
     const int r = threadIdx.x & 127;       // row of the tile, TMEM lane
@@ -957,7 +1018,12 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         if (!idle) {
           float s[128];
-          tmem_ld128(scol, s);
+          if constexpr (FP8) {  // (the one load wants more registers than 512 threads start with)
+            tmem_ld64(scol, *reinterpret_cast<float(*)[64]>(s));
+            tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
+          } else {
+            tmem_ld128(scol, s);
+          }
           if (key0 + C::kKeys > warp_lim) {
             const int left = my_lim - key0;
 #pragma unroll
@@ -1005,18 +1071,10 @@ __global__ void __launch_bounds__(384, 1)
               pw[i] = pack16<FP8>(x.x, x.y);
             }
             tmem_st32u(scol + 32 * hf, pw);
-            tmem_wait_st();
-            if (hf == 0) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.p_half[g]);
-            }
           }
+          tmem_wait_st();
           sum[0] = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
           l += sum[0].x + sum[0].y;
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_half[g]);
         }
         tc_fence_before();
         __syncwarp();
