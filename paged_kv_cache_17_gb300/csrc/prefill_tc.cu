@@ -71,8 +71,8 @@ struct PrefillCfg {
   // 1008: alignment slack (the start of dynamic shared memory is 16-byte aligned)
   static constexpr int kBytes = 1008 + kOffPoison + kKinds * D * 4;
   static constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
-  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kIssuer2Warp = 10, kFixWarp0 = FP8 ? 12 : 11;
-  static constexpr int kFixWarps = FP8 ? 4 : 1;
+  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kIssuer2Warp = 10, kFixWarp0 = 12;
+  static constexpr int kFixWarps = 4;
   static constexpr int kThreads = (kFixWarp0 + kFixWarps) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;           // per thread
   static constexpr int kSoftRegs = 208;
@@ -87,7 +87,9 @@ struct PrefillCfg {
 struct PrefillShared {
   uint64_t full[8], empty[8];  // ring: tile landed, tile consumed
   uint64_t s_full[2];          // scores of a step done (and every product issued before)
-  uint64_t p_full[2];          // weights of a step written (an arrival per warp; wide: and the other tile's turn over)
+  uint64_t p_half[2];          // weights of a step's first 64 keys written, the output rescaled (an arrival
+                               // per warp; wide: and the other tile's turn over)
+  uint64_t p_full[2];          // all weights of a step written (an arrival per warp)
   uint64_t o_full[2];          // every product of the group's work done
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
@@ -168,19 +170,6 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
       : "memory");
 }
 
-// 128 consecutive columns of this thread's lane in one load; the wait is inside.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // 16 consecutive columns of this thread's lane; the waits are inside.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -201,21 +190,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       : "memory");
 }
 
+// the largest of three; a NaN among them is the result
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+// 16 consecutive columns of this thread's lane; no wait (see tmem_wait_st).
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -292,6 +277,25 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
+// Four lanes hold four 16-byte pieces of a row each; afterwards lane k of the four holds piece k of
+// all four rows, so that together they store 64 contiguous bytes of a row at a time.  (A lane storing
+// its own row touches 32 lines per instruction: a work's epilogue took 4000 to 8000 cycles.)
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+  auto swap = [](uint4& keep0, uint4& keep1, bool upper, int m) {
+    uint4 a = upper ? keep0 : keep1;
+    a.x = __shfl_xor_sync(kFull, a.x, m);
+    a.y = __shfl_xor_sync(kFull, a.y, m);
+    a.z = __shfl_xor_sync(kFull, a.z, m);
+    a.w = __shfl_xor_sync(kFull, a.w, m);
+    if (upper) keep0 = a;
+    else keep1 = a;
+  };
+  swap(v[0], v[1], lane & 1, 1);
+  swap(v[2], v[3], lane & 1, 1);
+  swap(v[0], v[2], lane & 2, 2);
+  swap(v[1], v[3], lane & 2, 2);
+}
+
 // One CTA's worth of work, and what every role derives from it
 struct Work {
   int tok0;   // first query token (row of q)
@@ -364,8 +368,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kIssuers = WIDE ? 2 : 1;
-  const int G = p.group;
-  const int tile_tok = C::kRows / G;                   // tokens of a 128-row tile
+  const int G = p.group, log_g = 31 - __clz(G);  // a power of two
+  const int tile_tok = C::kRows >> log_g;                   // tokens of a 128-row tile
   const int cta_tok = WIDE ? 2 * tile_tok : tile_tok;  // tokens of a work
 
   if (warp == 0) {
@@ -382,7 +386,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], WIDE ? 5 : 4);
+      mbar_init(&sh.p_half[i], WIDE ? 5 : 4);
+      mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.exp_free[i], kIssuers);
       mbar_init(&sh.work_full[i], 1);
@@ -467,11 +472,12 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
         commit(&sh.s_full[g], leader);
       };
-      auto issue_o = [&](int g, bool first, uint32_t v_lo0) {
+      // keys 64 half .. of a step
+      auto issue_o = [&](int g, int half, bool first, uint32_t v_lo0) {
         const uint32_t pt = tm + C::kColS + 128 * g;
         const uint32_t v_lo = same(v_lo0);
 #pragma unroll
-        for (int kk = 0; kk < C::kKeys / 16; ++kk)
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
           mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, !first || kk > 0, leader);
       };
 
@@ -512,7 +518,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           // The scores of step j + 1 follow P V of step j in the same columns, in issue order.  The
           // tiles take turns, so that one's products run under the other's softmax (left to themselves
           // they fell into step and waited for the tensor cores together: 1681 against 1508 us for
-          // 4096 tokens over 32768, 32 heads).  The fifth arrival on p_full is the other issuer's, once its
+          // 4096 tokens over 32768, 32 heads).  The fifth arrival on p_half is the other issuer's, once its
           // turn before is over: on tile 0's for a work's first step when tile 1 is through with the work
           // before, then after tile 1's step before; on tile 1's after tile 0's same step, or, past
           // tile 0's last, issuer 1's own.  A tile 1 without steps watches tile 0's instead.  So no
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           const int g = warp == C::kIssuerWarp ? 0 : 1;
           const int mine = g == 0 ? st.n_of[0] : st.n_of[1], other = g == 0 ? st.n_of[1] : st.n_of[0];
           unsigned parity = (g == 0 ? c_p[0] : c_p[1]) & 1;
-          if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_full[0]);
+          if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_half[0]);
           ok = ok && wait_k();
           if (ok) {
             tc_fence_after();
@@ -532,28 +538,37 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           for (int j = 0; j < nstep && ok; ++j) {
             const bool more = j + 1 < nstep;
             ok = wait_v(j);
-            if (more && ok) {
-              next_k(j);
-              ok = wait_k();
-            }
+            if (more) next_k(j);
+            if (!FP8 && more && ok) ok = wait_k();  // before the weights, where waiting costs nothing
             if (!ok) break;
             if (j < mine) {
-              if (g == 1 && j >= other && leader) mbar_arrive(&sh.p_full[1]);
+              if (g == 1 && j >= other && leader) mbar_arrive(&sh.p_half[1]);
+              ok = wait(&sh.p_half[g], parity);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(g, 0, j == 0, v_lo(j));
               ok = wait(&sh.p_full[g], parity);
               if (!ok) break;
               parity ^= 1;
               tc_fence_after();
-              issue_o(g, j == 0, v_lo(j));
+              issue_o(g, 1, false, v_lo(j));
+              if (FP8 && j + 1 < mine) {  // K may come later than the weights: V's expansion holds up the ring
+                ok = wait_k();
+                if (!ok) break;
+                tc_fence_after();
+              }
               if (j + 1 < mine) issue_s(g, kc.slot);
               else commit(&sh.o_full[g], leader);
-              if ((g == 0 ? j < other : j + 1 < other) && leader) mbar_arrive(&sh.p_full[g ^ 1]);
+              if ((g == 0 ? j < other : j + 1 < other) && leader) mbar_arrive(&sh.p_half[g ^ 1]);
             } else if (g == 1 && mine == 0 && j < other) {
-              ok = wait(&sh.p_full[0], (c_p[0] + j) & 1);
+              ok = wait(&sh.p_half[0], (c_p[0] + j) & 1);
               if (!ok) break;
-              if (j + 1 < other && leader) mbar_arrive(&sh.p_full[0]);
+              if (j + 1 < other && leader) mbar_arrive(&sh.p_half[0]);
             }
             free_v(j);
             next_v(j);
+            if (FP8 && more && j + 1 >= mine) ok = wait_k();
+            if (!ok) break;
             if (more) commit(&sh.empty[kc.slot], leader);
             if (j + 2 == nstep) commit(&sh.q_empty, leader);
           }
@@ -569,10 +584,15 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           }
           for (int j = 0; j < nstep && ok; ++j) {
             const int g = j & 1, t = j >> 1;
-            ok = wait(&sh.p_full[g], ((g == 0 ? c_p[0] : c_p[1]) + t) & 1) && wait_v(j);
+            const unsigned parity = ((g == 0 ? c_p[0] : c_p[1]) + t) & 1;
+            ok = wait(&sh.p_half[g], parity) && wait_v(j);
             if (!ok) break;
             tc_fence_after();
-            issue_o(g, t == 0, v_lo(j));
+            issue_o(g, 0, t == 0, v_lo(j));
+            ok = wait(&sh.p_full[g], parity);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(g, 1, false, v_lo(j));
             free_v(j);
             next_v(j);
             if (j + 2 >= nstep) commit(&sh.o_full[g], leader);
@@ -796,8 +816,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       const Steps<WIDE> st(w, p, tile_tok);
       const int nstep = st.nstep;
       if (nstep == 0) continue;
-      // before this work's cut steps: the works before are through their epilogues, and what they
-      // left in the list of values that are not finite is cleared
+      // before values that are not finite are listed: the works before are through their epilogues,
+      // and what they left in the list is cleared
       bool cleared = false;
       auto clear = [&]() {
         cleared = true;
@@ -810,17 +830,12 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             fail();
           }
         }
-        const bool any = *poisoned != 0;
         named_sync(3, kFix);
-        if (any) {
-          for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
-          *poisoned = 0;
-          named_sync(3, kFix);
-        }
+        for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
+        named_sync(3, kFix);
       };
       for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
         const bool cut = j >= st.first_cut;
-        if (cut && !cleared) clear();
         const unsigned item = base + st.v_item(j);
         // the parity of `full` means this load only once it is issued (the slot's loads before it
         // are not waited for here); v_sent itself is never a phase ahead: eight V tiles on, the
@@ -835,52 +850,82 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         // rows below seen: every row's; from end on: no row's
         const int seen = st.lim_min - key0, end = w.ctx - key0;
         uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
+        // E4M3: expand the tile, eight pieces in registers at a time (one by one, a load and a store
+        // each, a tile took 2600 cycles and the step waited for it); rows no row sees become zeros.
+        // bf16: only the rows that not every row sees, four pieces at a time.  True if one of those
+        // that some row sees is not finite.
+        auto odd8 = [](uint32_t x) { return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u; };    // E4M3 NaN
+        auto odd16 = [](uint32_t x) { return (((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u; };   // bf16
+        const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
+        auto at16 = [&](int row) {
+          return reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        auto expand = [&](int row, uint2 v) {
+          st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
+                       e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
+        };
+        bool odd = false;
         if (ok) {
           if constexpr (FP8) {
-            const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
-#pragma unroll 4
-            for (int row = r0; row < C::kKeys; row += kStep) {
-              uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
-              if (cut && row >= seen) {
-                if (row >= end) {
-                  v = make_uint2(0u, 0u);
-                } else {
-                  uint8_t* b = reinterpret_cast<uint8_t*>(&v);
+            constexpr int kBatch = 8;
+            static_assert(C::kKeys % (kBatch * kStep) == 0, "whole batches");
+#pragma unroll 1
+            for (int b0 = r0; b0 < C::kKeys; b0 += kBatch * kStep) {
+              uint2 v[kBatch];
 #pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    if ((b[e] & 0x7f) == 0x7f) {  // NaN, the only E4M3 code that is not finite
-                      note(0, c * 8 + e, key0 + row);
-                      b[e] = 0;
-                    }
+              for (int i = 0; i < kBatch; ++i)
+                v[i] = *reinterpret_cast<const uint2*>(src + (b0 + i * kStep) * D + c * 8);
+              if (cut) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                  const int row = b0 + i * kStep;
+                  if (row >= end) v[i] = make_uint2(0u, 0u);
+                  else if (row >= seen) odd |= odd8(v[i].x) || odd8(v[i].y);
                 }
               }
-              st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
-                           e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) expand(b0 + i * kStep, v[i]);
             }
           } else {
-#pragma unroll 2
-            for (int row = max(0, seen) + r0; row < C::kKeys; row += kStep) {
-              uint4* at =
-                  reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-              if (row >= end) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                uint4 v = *at;
-                uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-                uint32_t odd = 0;
+            constexpr int kBatch = 4;
+#pragma unroll 1
+            for (int b0 = max(0, seen) + r0; b0 < min(end, C::kKeys); b0 += kBatch * kStep) {
+              uint4 v[kBatch];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) odd |= ((e[k] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-                if (odd) {  // exponent all ones somewhere
-                  for (int k = 0; k < 8; ++k) {
-                    const uint32_t x = (e[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-                    if ((x & 0x7f80u) == 0x7f80u) {
-                      note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + k, key0 + row);
-                      e[k >> 1] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
-                    }
-                  }
-                  *at = v;
+              for (int i = 0; i < kBatch; ++i) {
+                const int row = b0 + i * kStep;
+                v[i] = row < min(end, C::kKeys) ? *at16(row) : make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) odd |= odd16(v[i].x) || odd16(v[i].y) || odd16(v[i].z) || odd16(v[i].w);
+            }
+            for (int row = max(0, end) + r0; row < C::kKeys; row += kStep) *at16(row) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (cut && named_sync_or(3, kFix, odd)) {  // rare: list them and take them out of the tile
+          if (!cleared) clear();
+          for (int row = max(0, seen) + r0; ok && row < min(end, C::kKeys); row += kStep) {
+            if constexpr (FP8) {
+              uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
+              if (!odd8(v.x) && !odd8(v.y)) continue;
+              uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+              for (int e = 0; e < 8; ++e)
+                if (((word[e >> 2] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {  // the only code that is not finite
+                  note(0, c * 8 + e, key0 + row);
+                  word[e >> 2] &= ~(0xffu << (8 * (e & 3)));
+                }
+              expand(row, v);
+            } else {
+              uint4 v = *at16(row);
+              uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t x = (word[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                if ((x & 0x7f80u) == 0x7f80u) {
+                  note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + e, key0 + row);
+                  word[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
                 }
               }
+              *at16(row) = v;
             }
           }
         }
@@ -909,7 +954,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     // ======================================================================== softmax
     const int g = warp >> 2;               // accumulators: the tile (wide) or the parity of the steps (narrow)
     const int r = threadIdx.x & 127;       // row of the tile, TMEM lane
-    const int my_i = (WIDE ? g * tile_tok : 0) + r / G;  // token within the work
+    const int my_i = (WIDE ? g * tile_tok : 0) + (r >> log_g);  // token within the work
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t scol = tmem + lane_base + C::kColS + 128 * g;
     const uint32_t ocol = tmem + lane_base + C::kColO;
@@ -927,7 +972,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       const Steps<WIDE> st(w, p, tile_tok);
       const int nloc = st.n_of[g];
       const bool rv = my_i < w.ntok;
-      const int hq = w.h * G + r % G;
+      const int hq = w.h * G + (r & (G - 1));
       const int64_t orow = static_cast<int64_t>(w.tok0 + my_i) * p.hq + hq;
       const int64_t rec = static_cast<int64_t>(w.split) * p.total_q * p.hq + orow;
       const bool split_out = p.splits > 1;
@@ -1018,63 +1063,82 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         tc_fence_after();
         if (!idle) {
           float s[128];
-          if constexpr (FP8) {  // (the one load wants more registers than 512 threads start with)
-            tmem_ld64(scol, *reinterpret_cast<float(*)[64]>(s));
-            tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
-          } else {
-            tmem_ld128(scol, s);
-          }
+          // (one load of 128 columns wants more registers than 512 threads start with)
+          tmem_ld64(scol, *reinterpret_cast<float(*)[64]>(s));
+          tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
           if (key0 + C::kKeys > warp_lim) {
             const int left = my_lim - key0;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i >= left) s[i] = -INFINITY;
           }
+          // 32 weights from their scores, as 16-bit pairs into the columns of the scores
+          float2 sum[2] = {};
+          auto weights = [&](int q, float negm, uint32_t (&pw)[16]) {
+            const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 x = ffma2(make_float2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), sc2, nm2);
+              x.x = exp2_ftz(x.x);
+              x.y = exp2_ftz(x.y);
+              sum[i & 1] = fadd2(sum[i & 1], x);
+              pw[i] = pack16<FP8>(x.x, x.y);
+            }
+          };
+          // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
+          auto minus_m = [&]() { return (m_used == -INFINITY ? 0.f : -m_used) + C::kBias; };
+          // the first weights by the reference as it stands, while the maximum is being found; it
+          // moves rarely, and they are then taken again
+          uint32_t pw[16];
+          weights(0, minus_m(), pw);
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int i = 4; i < 124; i += 8) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
           }
-          const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(fmaxf(s[124], s[125]), s[126], s[127])) * sscale;
+          const float top =
+              max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[124], s[125], s[125]), s[126], s[127])) * sscale;
+          if (!(top < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or an infinity among the scores
           const bool grow = top > m_used + C::kLazy;
-          float alpha = 1.f;
-          if (grow) {
-            alpha = fast_exp2(m_used - top);  // 0 while the row has seen nothing
-            l *= alpha;
-            m_used = top;
-          }
-          // P V of the previous step was issued before these scores: it is done
-          if (t > 0 && __any_sync(kFull, grow)) {
+          if (__any_sync(kFull, grow)) {
+            float alpha = 1.f;
+            if (grow) {
+              alpha = fast_exp2(m_used - top);  // 0 while the row has seen nothing
+              l *= alpha;
+              m_used = top;
+            }
+            if (t > 0) {  // P V of the previous step was issued before these scores: it is done
 #pragma unroll 1
-            for (int ch = 0; ch < D / 16; ++ch) {
-              float o[16];
-              tmem_ld16(ocol + D * g + 16 * ch, o);
+              for (int ch = 0; ch < D / 16; ++ch) {
+                float o[16];
+                tmem_ld16(ocol + D * g + 16 * ch, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= alpha;
-              tmem_st16(ocol + D * g + 16 * ch, o);
+                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                tmem_st16(ocol + D * g + 16 * ch, o);
+              }
             }
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            weights(0, minus_m(), pw);
           }
-          // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
-          const float negm = (m_used == -INFINITY ? 0.f : -m_used) + C::kBias;
-          const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
-          float2 sum[4] = {};
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t pw[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float2 x = ffma2(make_float2(s[64 * hf + 2 * i], s[64 * hf + 2 * i + 1]), sc2, nm2);
-              x.x = exp2_ftz(x.x);
-              x.y = exp2_ftz(x.y);
-              sum[i & 3] = fadd2(sum[i & 3], x);
-              pw[i] = pack16<FP8>(x.x, x.y);
-            }
-            tmem_st32u(scol + 32 * hf, pw);
-          }
+          const float negm = minus_m();
+          tmem_st16u(scol, pw);
+          weights(1, negm, pw);
+          tmem_st16u(scol + 16, pw);
+          weights(2, negm, pw);
           tmem_wait_st();
-          sum[0] = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[g]);
+          tmem_st16u(scol + 32, pw);
+          weights(3, negm, pw);
+          tmem_st16u(scol + 48, pw);
+          sum[0] = fadd2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
+          tmem_wait_st();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[g]);
         }
         tc_fence_before();
         __syncwarp();
@@ -1120,6 +1184,13 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           else if (p.lse != nullptr)
             p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
         }
+        // output row of row k of this lane's four (-1: no such row)
+        const int64_t split_rows = static_cast<int64_t>(w.split) * p.total_q * p.hq;
+        auto row_at = [&](int k) -> int64_t {
+          const int rr = (r & ~3) + k;
+          const int i = (WIDE ? g * tile_tok : 0) + (rr >> log_g);
+          return i < w.ntok ? static_cast<int64_t>(w.tok0 + i) * p.hq + w.h * G + (rr & (G - 1)) : -1;
+        };
         constexpr int kMine = WIDE ? D : D / 2;  // columns of this group
         const int col0 = WIDE ? 0 : g * kMine;
 #pragma unroll 1
@@ -1150,27 +1221,42 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               }
             }
           }
-          if (rv) {
-            if (split_out) {
-              float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * D + col);
+          if (split_out) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + col);
+            for (int half = 0; half < 2; ++half) {
+              uint4 v[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                v[i] = make_uint4(__float_as_uint(o[16 * half + 4 * i]), __float_as_uint(o[16 * half + 4 * i + 1]),
+                                  __float_as_uint(o[16 * half + 4 * i + 2]), __float_as_uint(o[16 * half + 4 * i + 3]));
+              transpose4(v, lane);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int64_t at = row_at(k);
+                if (at >= 0)
+                  reinterpret_cast<uint4*>(p.part_acc + (split_rows + at) * D + col + 16 * half)[lane & 3] = v[k];
+              }
+            }
+          } else {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            transpose4(v, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int64_t at = row_at(k);
+              if (at >= 0) reinterpret_cast<uint4*>(p.out + at * D + col)[lane & 3] = v[k];
             }
           }
         }
       }
       tc_fence_before();
       if constexpr (!WIDE) dead = named_sync_or(2, 256, dead);  // both are through with both outputs
-      __syncwarp();
-      __threadfence_block();
+      __syncwarp();  // (the list of values was read above; the output's stores need not have landed)
       if (lane == 0) atomicAdd(&sh.epilogues, 1);
     }
   }
