@@ -277,25 +277,6 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
-// Four lanes hold four 16-byte pieces of a row each; afterwards lane k of the four holds piece k of
-// all four rows, so that together they store 64 contiguous bytes of a row at a time.  (A lane storing
-// its own row touches 32 lines per instruction: a work's epilogue took 4000 to 8000 cycles.)
-__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
-  auto swap = [](uint4& keep0, uint4& keep1, bool upper, int m) {
-    uint4 a = upper ? keep0 : keep1;
-    a.x = __shfl_xor_sync(kFull, a.x, m);
-    a.y = __shfl_xor_sync(kFull, a.y, m);
-    a.z = __shfl_xor_sync(kFull, a.z, m);
-    a.w = __shfl_xor_sync(kFull, a.w, m);
-    if (upper) keep0 = a;
-    else keep1 = a;
-  };
-  swap(v[0], v[1], lane & 1, 1);
-  swap(v[2], v[3], lane & 1, 1);
-  swap(v[0], v[2], lane & 2, 2);
-  swap(v[1], v[3], lane & 2, 2);
-}
-
 // One CTA's worth of work, and what every role derives from it
 struct Work {
   int tok0;   // first query token (row of q)
@@ -1173,7 +1154,6 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         m_used = top;
       }
       if (!dead && !idle) {
-        const bool bad = *poisoned == static_cast<int>(n) + 1;
         float inv = 1.f;
         if (!split_out) {
           inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -1184,13 +1164,6 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           else if (p.lse != nullptr)
             p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
         }
-        // output row of row k of this lane's four (-1: no such row)
-        const int64_t split_rows = static_cast<int64_t>(w.split) * p.total_q * p.hq;
-        auto row_at = [&](int k) -> int64_t {
-          const int rr = (r & ~3) + k;
-          const int i = (WIDE ? g * tile_tok : 0) + (rr >> log_g);
-          return i < w.ntok ? static_cast<int64_t>(w.tok0 + i) * p.hq + w.h * G + (rr & (G - 1)) : -1;
-        };
         constexpr int kMine = WIDE ? D : D / 2;  // columns of this group
         const int col0 = WIDE ? 0 : g * kMine;
 #pragma unroll 1
@@ -1210,46 +1183,36 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], a1, o[i]);
             }
           }
-          if (bad) {
+          if (rv) {
+            if (split_out) {
+              float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * D + col);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int dim = col + i;
-              if (poison[dim] < my_lim) o[i] = __int_as_float(0x7fffffff);
-              if constexpr (!FP8) {
-                if (poison[D + dim] < my_lim) o[i] += INFINITY;
-                if (poison[2 * D + dim] < my_lim) o[i] -= INFINITY;
-              }
-            }
-          }
-          if (split_out) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint4 v[4];
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + col);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                v[i] = make_uint4(__float_as_uint(o[16 * half + 4 * i]), __float_as_uint(o[16 * half + 4 * i + 1]),
-                                  __float_as_uint(o[16 * half + 4 * i + 2]), __float_as_uint(o[16 * half + 4 * i + 3]));
-              transpose4(v, lane);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int64_t at = row_at(k);
-                if (at >= 0)
-                  reinterpret_cast<uint4*>(p.part_acc + (split_rows + at) * D + col + 16 * half)[lane & 3] = v[k];
-              }
+                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
             }
-          } else {
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-            transpose4(v, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int64_t at = row_at(k);
-              if (at >= 0) reinterpret_cast<uint4*>(p.out + at * D + col)[lane & 3] = v[k];
+          }
+        }
+        // rare: values of V taken out of the cut tiles are added to the rows that see them (this thread
+        // stored the row just now)
+        if (*poisoned == static_cast<int>(n) + 1 && rv) {
+#pragma unroll 1
+          for (int dim = col0; dim < col0 + kMine; ++dim) {
+            const bool nan = poison[dim] < my_lim, up = !FP8 && poison[(C::kKinds - 2) * D + dim] < my_lim,
+                       down = !FP8 && poison[(C::kKinds - 1) * D + dim] < my_lim;
+            if (!nan && !up && !down) continue;
+            const float x = nan || (up && down) ? __int_as_float(0x7fffffff) : up ? INFINITY : -INFINITY;
+            if (split_out) {
+              p.part_acc[rec * D + dim] += x;
+            } else {
+              __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + dim;
+              *at = __float2bfloat16_rn(__bfloat162float(*at) + x);
             }
           }
         }
