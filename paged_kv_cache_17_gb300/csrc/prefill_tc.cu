@@ -277,6 +277,47 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
+// A warp's 32 rows of N 32-bit words, each row in its own thread, turned so that four lanes hold
+// 16 consecutive bytes each of one row: lane t gets, for i < N / 16, words 16 i + 4 (t % 4) .. + 3 of
+// rows t / 4 and t / 4 + 8 (first 16 rows, then the others), which it stores as 64 contiguous bytes
+// with its neighbours.  (Lanes storing their own rows touch 32 lines an instruction: 4100 cycles for a
+// 256-row epilogue at D = 128.)  The turn goes through tensor memory: written a row a thread, read
+// back with four lanes to a row's four columns.
+template <int N>
+struct TmemTurn;
+template <>
+struct TmemTurn<32> {
+  static __device__ __forceinline__ void put(uint32_t taddr, const uint32_t (&w)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+                 "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15]), "r"(w[16]), "r"(w[20]), "r"(w[24]), "r"(w[28]), "r"(w[17]), "r"(w[21]), "r"(w[25]), "r"(w[29]), "r"(w[18]), "r"(w[22]), "r"(w[26]), "r"(w[30]), "r"(w[19]), "r"(w[23]), "r"(w[27]), "r"(w[31])
+                 : "memory");
+  }
+  // rows of one half of the warp's 32 (taddr's lane: the first of the 16): v[2 j + k], j < N / 4: word
+  // 16 (j / 4) + 4 (lane % 4) + j % 4 of row lane / 4 + 8 k
+  static __device__ __forceinline__ void get(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+  }
+};
+template <>
+struct TmemTurn<64> {
+  static __device__ __forceinline__ void put(uint32_t taddr, const uint32_t (&w)[64]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+                 "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15]), "r"(w[16]), "r"(w[20]), "r"(w[24]), "r"(w[28]), "r"(w[17]), "r"(w[21]), "r"(w[25]), "r"(w[29]), "r"(w[18]), "r"(w[22]), "r"(w[26]), "r"(w[30]), "r"(w[19]), "r"(w[23]), "r"(w[27]), "r"(w[31]), "r"(w[32]), "r"(w[36]), "r"(w[40]), "r"(w[44]), "r"(w[33]), "r"(w[37]), "r"(w[41]), "r"(w[45]), "r"(w[34]), "r"(w[38]), "r"(w[42]), "r"(w[46]), "r"(w[35]), "r"(w[39]), "r"(w[43]), "r"(w[47]), "r"(w[48]), "r"(w[52]), "r"(w[56]), "r"(w[60]), "r"(w[49]), "r"(w[53]), "r"(w[57]), "r"(w[61]), "r"(w[50]), "r"(w[54]), "r"(w[58]), "r"(w[62]), "r"(w[51]), "r"(w[55]), "r"(w[59]), "r"(w[63])
+                 : "memory");
+  }
+  // rows of one half of the warp's 32 (taddr's lane: the first of the 16): v[2 j + k], j < N / 4: word
+  // 16 (j / 4) + 4 (lane % 4) + j % 4 of row lane / 4 + 8 k
+  static __device__ __forceinline__ void get(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 : "r"(taddr)
+                 : "memory");
+  }
+};
+
 // One CTA's worth of work, and what every role derives from it
 struct Work {
   int tok0;   // first query token (row of q)
@@ -1043,16 +1084,24 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
         tc_fence_after();
         if (!idle) {
+          // keys that a row does not see: -inf over their scores, in the columns (a loop of 32: this is
+          // for a work's last steps, and straight code for 128 is slow to fetch)
+          if (key0 + C::kKeys > warp_lim) {
+            const int left = my_lim - key0;
+#pragma unroll 1
+            for (int c = max(0, warp_lim - key0) & ~31; c < C::kKeys; c += 32) {
+              float x[32];
+              tmem_ld32(scol + c, x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >= left - c) x[i] = -INFINITY;
+              tmem_st32(scol + c, x);
+            }
+          }
           float s[128];
           // (one load of 128 columns wants more registers than 512 threads start with)
           tmem_ld64(scol, *reinterpret_cast<float(*)[64]>(s));
           tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
-          if (key0 + C::kKeys > warp_lim) {
-            const int left = my_lim - key0;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= left) s[i] = -INFINITY;
-          }
           // 32 weights from their scores, as 16-bit pairs into the columns of the scores
           float2 sum[2] = {};
           auto weights = [&](int q, float negm, uint32_t (&pw)[16]) {
@@ -1164,10 +1213,40 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           else if (p.lse != nullptr)
             p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
         }
+        if constexpr (WIDE) {
+          if (!split_out) {
+            uint32_t words[D / 2];
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float o[32];
+              tmem_ld32(ocol + D * g + 32 * ch, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) words[16 * ch + i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+            }
+            TmemTurn<D / 2>::put(ocol + D * g, words);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[D / 4];
+              TmemTurn<D / 2>::get(ocol + D * g + (static_cast<uint32_t>(16 * half) << 16), v);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int rr = (r & ~31) + 16 * half + 8 * k + (lane >> 2);
+                const int i = g * tile_tok + (rr >> log_g);
+                if (i >= w.ntok) continue;
+                uint4* dst = reinterpret_cast<uint4*>(
+                                 p.out + (static_cast<int64_t>(w.tok0 + i) * p.hq + w.h * G + (rr & (G - 1))) * D) +
+                             (lane & 3);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                  dst[4 * c] = make_uint4(v[8 * c + k], v[8 * c + 2 + k], v[8 * c + 4 + k], v[8 * c + 6 + k]);
+              }
+            }
+          }
+        }
         constexpr int kMine = WIDE ? D : D / 2;  // columns of this group
         const int col0 = WIDE ? 0 : g * kMine;
 #pragma unroll 1
-        for (int ch = 0; ch < kMine / 32; ++ch) {
+        for (int ch = 0; (!WIDE || split_out) && ch < kMine / 32; ++ch) {
           const int col = col0 + 32 * ch;
           float o[32];
           if constexpr (WIDE) {
@@ -1199,8 +1278,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             }
           }
         }
-        // rare: values of V taken out of the cut tiles are added to the rows that see them (this thread
-        // stored the row just now)
+        // rare: values of V taken out of the cut tiles are added to the rows that see them (the warp
+        // stored them just now)
+        __syncwarp();
         if (*poisoned == static_cast<int>(n) + 1 && rv) {
 #pragma unroll 1
           for (int dim = col0; dim < col0 + kMine; ++dim) {
