@@ -75,7 +75,7 @@ struct PrefillCfg {
   static constexpr int kFixWarps = 4;
   static constexpr int kThreads = (kFixWarp0 + kFixWarps) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;           // per thread
-  static constexpr int kSoftRegs = 208;
+  static constexpr int kSoftRegs = 184;
   static constexpr int kAuxRegs = (kLaunchRegs * kThreads - kSoftRegs * 256) / (kThreads - 256) / 8 * 8;
   static_assert(kSoftRegs * 256 + kAuxRegs * (kThreads - 256) <= kLaunchRegs * kThreads, "register split");
   static constexpr float kLazy = 8.f;
@@ -425,6 +425,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     sh.epilogues = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x == C::kProducerWarp * 32) {
+    if (!FP8) tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   for (int i = threadIdx.x; i < C::kKinds * D; i += C::kThreads) poison[i] = 0x7fffffff;
   tc_fence_before();
   __syncthreads();
@@ -453,7 +458,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     return w.seq >= 0;
   };
 
-  // the registers of the launch, dealt out anew: 208 to the softmax threads
+  // the registers of the launch, dealt out anew: 184 to a softmax thread, 72 to another (208 and 48:
+  // the other roles spill, 158 against 149 us for nine prompts of 257 to 2048 tokens)
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
   if (warp == C::kIssuerWarp || warp == C::kIssuer2Warp) {
@@ -675,10 +681,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       int before = 0;
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
-        int first = 0, n = 0;
+        int first = 0, n = 0, len = 0;
         if (b < p.batch) {
           first = p.q_indptr[b];
           const int last = p.q_indptr[b + 1];
+          len = p.context_lens[b];
           n = last - first;
           if (first < 0 || last < first || last > p.total_q) {
             set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           first = __shfl_sync(kFull, first, src);
           n = __shfl_sync(kFull, n, src);
           w.seq = b0 + src;
-          int ctx = p.context_lens[w.seq];
+          int ctx = __shfl_sync(kFull, len, src);
           const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
           if (ctx < 0 || ctx > cap) {
             set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
