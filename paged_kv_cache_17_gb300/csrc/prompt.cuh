@@ -28,7 +28,7 @@ struct RopeAppendParams {
   uint32_t* status;
   int64_t num_tokens, pool_slots;
   int hq, hkv, rot;  // rot: elements of a head that are rotated (0: none)
-  int tokens_per_cta;
+  int rows_per_cta, groups;  // launch shape (launch_qk_rope_append)
   float eps, rope_scale;
 };
 

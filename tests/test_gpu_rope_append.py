@@ -121,6 +121,30 @@ def test_equals_append_without_norm_and_rotation(pkv):
                 assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(0), b.nan_to_num(0))
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.015625, 0.0117, 3.0, 1e-3, 7e37, 1e-39])
+def test_codes_are_those_of_the_append(pkv, scale):
+    """Values at and next to every border of two codes, under scales that divide exactly or not."""
+    hkv, d = 2, 128
+    codes = torch.arange(0, 0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = (codes[1:] + codes[:-1]) / 2
+    x = torch.cat([codes, mid, mid * (1 + 2 ** -7), mid * (1 - 2 ** -7), torch.tensor([449.0, 464.0, 470.0, 1e4])])
+    x = torch.cat([x, -x]).double() * scale
+    x = x.clamp(-3e38, 3e38).to(torch.bfloat16)
+    T = (x.numel() + hkv * d - 1) // (hkv * d)
+    k = torch.zeros(T * hkv * d, dtype=torch.bfloat16)
+    k[: x.numel()] = x
+    k = k.view(T, hkv, d).cuda()
+    v = k.flip(0).contiguous()
+    q = torch.zeros((T, 2, d), dtype=torch.bfloat16, device="cuda")
+    kc, vc, scales, _ = make_pool([T], hkv, d, True, 4)
+    scales.fill_(scale)
+    kd, vd = kc.clone(), vc.clone()
+    slots = torch.arange(T, device="cuda")
+    pkv.qk_norm_rope_append(q, k, v, None, slots, kc, vc, scales=scales)
+    pkv.paged_kv_append(k, v, slots, kd, vd, scales=scales)
+    assert torch.equal(kc.view(torch.uint8), kd.view(torch.uint8)) and torch.equal(vc.view(torch.uint8), vd.view(torch.uint8))
+
+
 def test_in_place_and_strided_output(pkv):
     packed, pos, w = inputs(77, 8, 2, 64, 9)
     kc, vc, _, _ = make_pool([77], 2, 64, False, 1)
