@@ -931,7 +931,7 @@ struct PrefillPlan {
 
 constexpr double kPrefillStepUs[2] = {0.75, 1.15};  // a narrow / wide step of 128 keys
 constexpr double kPrefillCtaUs = 4.0;               // a CTA's start and end
-constexpr double kPrefillMergeUs = 4.0;             // the merge kernel's launch
+constexpr double kPrefillMergeUs = 6.0;             // the merge kernel, and its launch on the host
 constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
 constexpr long long kPrefillMaxRecords = 1LL << 20;
 
@@ -957,7 +957,7 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
     pp.splits = (steps + forced - 1) / forced;
   } else {
     double best = -1;
-    for (int n = 1; n <= std::min(steps, 64); ++n) {
+    for (int n = 1; n <= std::min(steps, 48); ++n) {
       const int run = (steps + n - 1) / n;
       if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
       if (n > 1 && rows * n > kPrefillMaxRecords) break;
