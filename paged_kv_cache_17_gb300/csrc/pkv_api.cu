@@ -931,7 +931,7 @@ struct PrefillPlan {
 
 constexpr double kPrefillStepUs[2] = {0.75, 1.15};  // a narrow / wide step of 128 keys
 constexpr double kPrefillCtaUs = 4.0;               // a CTA's start and end
-constexpr double kPrefillMergeUs = 6.0;             // the merge kernel, and its launch on the host
+constexpr double kPrefillMergeUs = 4.0;             // the merge kernel
 constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
 constexpr long long kPrefillMaxRecords = 1LL << 20;
 
