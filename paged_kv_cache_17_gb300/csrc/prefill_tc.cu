@@ -170,6 +170,21 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
       : "memory");
 }
 
+// Wait for a phase; false when the CTA has aborted or after 2^23 tries (each suspended by the hardware for
+// a time, so seconds).  Shorter code than wait_or_abort, at 30 places: the roles together do not
+// fit the SM's instruction cache, and the fetches beyond it were at 83 % of their peak rate.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int n = 0; n < (1 << 23) && !*abort; ++n)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ void give_up(uint32_t* status, volatile int* abort) {
+  set_flag(status, PKV_DEVFLAG_WAIT_TIMEOUT);
+  *abort = 1;
+}
+
 // 16 consecutive columns of this thread's lane; the waits are inside.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -277,46 +292,23 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
-// A warp's 32 rows of N 32-bit words, each row in its own thread, turned so that four lanes hold
-// 16 consecutive bytes each of one row: lane t gets, for i < N / 16, words 16 i + 4 (t % 4) .. + 3 of
-// rows t / 4 and t / 4 + 8 (first 16 rows, then the others), which it stores as 64 contiguous bytes
-// with its neighbours.  (Lanes storing their own rows touch 32 lines an instruction: 4100 cycles for a
-// 256-row epilogue at D = 128.)  The turn goes through tensor memory: written a row a thread, read
-// back with four lanes to a row's four columns.
-template <int N>
-struct TmemTurn;
-template <>
-struct TmemTurn<32> {
-  static __device__ __forceinline__ void put(uint32_t taddr, const uint32_t (&w)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-                 "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15]), "r"(w[16]), "r"(w[20]), "r"(w[24]), "r"(w[28]), "r"(w[17]), "r"(w[21]), "r"(w[25]), "r"(w[29]), "r"(w[18]), "r"(w[22]), "r"(w[26]), "r"(w[30]), "r"(w[19]), "r"(w[23]), "r"(w[27]), "r"(w[31])
-                 : "memory");
-  }
-  // rows of one half of the warp's 32 (taddr's lane: the first of the 16): v[2 j + k], j < N / 4: word
-  // 16 (j / 4) + 4 (lane % 4) + j % 4 of row lane / 4 + 8 k
-  static __device__ __forceinline__ void get(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr)
-                 : "memory");
-  }
-};
-template <>
-struct TmemTurn<64> {
-  static __device__ __forceinline__ void put(uint32_t taddr, const uint32_t (&w)[64]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-                 "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15]), "r"(w[16]), "r"(w[20]), "r"(w[24]), "r"(w[28]), "r"(w[17]), "r"(w[21]), "r"(w[25]), "r"(w[29]), "r"(w[18]), "r"(w[22]), "r"(w[26]), "r"(w[30]), "r"(w[19]), "r"(w[23]), "r"(w[27]), "r"(w[31]), "r"(w[32]), "r"(w[36]), "r"(w[40]), "r"(w[44]), "r"(w[33]), "r"(w[37]), "r"(w[41]), "r"(w[45]), "r"(w[34]), "r"(w[38]), "r"(w[42]), "r"(w[46]), "r"(w[35]), "r"(w[39]), "r"(w[43]), "r"(w[47]), "r"(w[48]), "r"(w[52]), "r"(w[56]), "r"(w[60]), "r"(w[49]), "r"(w[53]), "r"(w[57]), "r"(w[61]), "r"(w[50]), "r"(w[54]), "r"(w[58]), "r"(w[62]), "r"(w[51]), "r"(w[55]), "r"(w[59]), "r"(w[63])
-                 : "memory");
-  }
-  // rows of one half of the warp's 32 (taddr's lane: the first of the 16): v[2 j + k], j < N / 4: word
-  // 16 (j / 4) + 4 (lane % 4) + j % 4 of row lane / 4 + 8 k
-  static __device__ __forceinline__ void get(uint32_t taddr, uint32_t (&v)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x128b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-                 : "r"(taddr)
-                 : "memory");
-  }
-};
+// A warp's 32 rows of 32-bit words, each row in its own thread, turned so that four lanes hold 16
+// consecutive bytes each of one row and store 64 contiguous bytes together.  (Lanes storing their own
+// rows touch 32 lines an instruction: 4100 cycles for a 256-row epilogue at D = 128.)  The turn goes
+// through tensor memory: written a row a thread, 16 words at a time, read back with four lanes to a
+// row's four columns.  No wait in put.
+__device__ __forceinline__ void turn_put(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15])
+               : "memory");
+}
+// 32 words of rows lane / 4 and lane / 4 + 8 of the 16 from taddr's lane: v[8 c + 2 j + k], word
+// 16 c + 4 (lane % 4) + j of row lane / 4 + 8 k
+__device__ __forceinline__ void turn_get(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+               : "r"(taddr)
+               : "memory");
+}
 
 // One CTA's worth of work, and what every role derives from it
 struct Work {
@@ -440,13 +432,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
 
   const uint32_t q_base = smem_u32(smem + C::kOffQ);
   const uint32_t ring = smem_u32(smem + C::kOffRing);
-  auto fail = [&]() {
-    set_flag(p.status, PKV_DEVFLAG_WAIT_TIMEOUT);
-    *abort = 1;
-  };
+  auto fail = [&]() { give_up(p.status, abort); };
   // the work number n (all roles see the same sequence); false: there is none left, or abort
   auto next_work = [&](unsigned n, Work& w, unsigned lanes = kFull) -> bool {
-    const bool ok = wait_or_abort(&sh.work_full[n & 1], (n >> 1) & 1, abort);
+    const bool ok = wait_for(&sh.work_full[n & 1], (n >> 1) & 1, abort);
     if (!__all_sync(lanes, ok)) {
       if (!*abort) fail();
       return false;
@@ -468,7 +457,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     // for both groups
     if (warp == C::kIssuerWarp || WIDE) {
       const uint32_t leader = elect_one();
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_or_abort(bar, parity, abort)); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_for(bar, parity, abort)); };
       auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
       constexpr uint32_t kIdO = idesc_f16(C::kRows, D, !FP8, true);
       // scores: A = Q with its sign turned (bit 13) for a negative scale; E4M3 formats are 0
@@ -657,7 +646,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * C::kSlot;
       if (leader) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
       __syncwarp();
-#pragma unroll
+#pragma unroll(FP8 ? 2 : C::kStepBlocks)
       for (int blk = 0; blk < C::kStepBlocks; ++blk) {
         const int r = __shfl_sync(kFull, row, blk);
         if constexpr (FP8) {
@@ -670,7 +659,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       }
     };
     auto slot_free = [&](unsigned item) {
-      const bool ok = item < NS || wait_or_abort(&sh.empty[item % NS], ((item / NS) - 1) & 1, abort);
+      const bool ok = item < NS || wait_for(&sh.empty[item % NS], ((item / NS) - 1) & 1, abort);
       return __all_sync(kFull, ok);
     };
     // the tokens of the work at (x, y) of the grid: tile slots count the sequences' tiles in
@@ -732,7 +721,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       if (w.seq >= 0) {
         const Steps<WIDE> st(w, p, tile_tok);
         const int nstep = st.nstep;
-        ok = n < 2 || wait_or_abort(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+        ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
         ok = __all_sync(kFull, ok);
         if (ok) {
           if (lane == 0) {
@@ -761,7 +750,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           int id2 = id_of(2), id3 = id_of(3);
           if constexpr (!FP8) {
             // Q's tiles are free once the last scores of the work before are done
-            if (q_count > 0) ok = wait_or_abort(&sh.q_empty, (q_count - 1) & 1, abort);
+            if (q_count > 0) ok = wait_for(&sh.q_empty, (q_count - 1) & 1, abort);
             ok = __all_sync(kFull, ok);
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
@@ -774,24 +763,28 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             }
           }
           if (ok) ++q_count;
-          ok = ok && slot_free(base);
-          if (ok) load(&tm_k, base, w.h, cur);
-          unsigned issued = base + (ok ? 1 : 0);
-          for (int j = 0; j < nstep && ok; ++j) {
-            if (j + 1 < nstep) {
-              if (!(ok = slot_free(base + st.k_item(j + 1)))) break;
-              load(&tm_k, base + st.k_item(j + 1), w.h, nxt);
-              issued = base + st.k_item(j + 1) + 1;
+          // tiles in the ring's order: K of step 0, then K of step j + 1 and V of step j in turns
+          unsigned issued = base;
+          int j = 0;
+          bool is_v = false;
+#pragma unroll 1
+          for (int i = 0; i < 2 * nstep && ok; ++i) {
+            ok = slot_free(base + i);
+            if (!ok) break;
+            load(is_v ? &tm_v : &tm_k, base + i, w.h, i == 0 || is_v ? cur : nxt);
+            issued = base + i + 1;
+            if (is_v) {
+              if (lane == 0 && (FP8 || j >= st.first_cut))
+                mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
+              cur = nxt;
+              nxt = row_of(id2);
+              id2 = id3;
+              id3 = id_of(j + 4);
+              ++j;
+              is_v = j + 1 >= nstep;
+            } else {
+              is_v = i > 0 || nstep == 1;
             }
-            if (!(ok = slot_free(base + st.v_item(j)))) break;
-            load(&tm_v, base + st.v_item(j), w.h, cur);
-            issued = base + st.v_item(j) + 1;
-            if (lane == 0 && (FP8 || j >= st.first_cut))
-              mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
-            cur = nxt;
-            nxt = row_of(id2);
-            id2 = id3;
-            id3 = id_of(j + 4);
           }
           base = ok ? base + 2 * nstep : issued;
           steps_done += nstep;
@@ -808,7 +801,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     }
     // no work left: tell the other roles
     if (ok) {
-      ok = n < 2 || wait_or_abort(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+      ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
       if (ok && lane == 0) {
         sh.work[n & 1][0] = make_int4(0, 0, -1, 0);
         sh.work[n & 1][1] = make_int4(0, 0, 0, 0);
@@ -870,10 +863,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         // are not waited for here); v_sent itself is never a phase ahead: eight V tiles on, the
         // ring has come round
         const unsigned sent = FP8 ? steps_done + j : cuts + j - st.first_cut;
-        if (ok) ok = wait_or_abort(&sh.v_sent[sent & 7], (sent >> 3) & 1, abort);
-        if (ok) ok = wait_or_abort(&sh.full[item % NS], (item / NS) & 1, abort);
+        if (ok) ok = wait_for(&sh.v_sent[sent & 7], (sent >> 3) & 1, abort);
+        if (ok) ok = wait_for(&sh.full[item % NS], (item / NS) & 1, abort);
         if constexpr (FP8)
-          if (ok && sent >= 2) ok = wait_or_abort(&sh.exp_free[sent & 1], ((sent >> 1) - 1) & 1, abort);
+          if (ok && sent >= 2) ok = wait_for(&sh.exp_free[sent & 1], ((sent >> 1) - 1) & 1, abort);
         if (!ok && !*abort) fail();
         const int key0 = (st.k0 + j) * C::kKeys;
         // rows below seen: every row's; from end on: no row's
@@ -1031,13 +1024,12 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         if (WIDE || g == 0) {
           const uint4* qr =
               reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(w.tok0 + my_i) * p.q_stride + hq * D);
-          uint4 v[D / 8];
           float top = 0.f;
           bool odd = false;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
-            v[c] = rv ? qr[c] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            const uint4 v = rv ? qr[c] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               top = fmaxf(top, fmaxf(fabsf(bf16_lo(e[k])), fabsf(bf16_hi(e[k]))));
@@ -1049,12 +1041,14 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           ex = min(ex, 126);  // rows below 2^-119: their codes lose what lies under 2^-135
           const float up = __uint_as_float(static_cast<uint32_t>(max(ex, -126) + 127) << 23);
           const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {  // 16 codes: one 16-byte piece of the row
+            const uint4 v[2] = {rv ? qr[2 * c] : make_uint4(0u, 0u, 0u, 0u),
+                                rv ? qr[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u)};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t a = u4_word(v[2 * c + k / 2], 2 * (k & 1)), b = u4_word(v[2 * c + k / 2], 2 * (k & 1) + 1);
+              const uint32_t a = u4_word(v[k / 2], 2 * (k & 1)), b = u4_word(v[k / 2], 2 * (k & 1) + 1);
               float x[4] = {bf16_lo(a) * up, bf16_hi(a) * up, bf16_lo(b) * up, bf16_hi(b) * up};
               hi[k] = e4m3x4_rest(x);
               lo[k] = e4m3x4_rest(x);
@@ -1083,7 +1077,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       float m_used = -INFINITY, l = 0.f;
       for (int t = 0; t < nloc; ++t) {
         const int key0 = (st.k0 + (WIDE ? t : 2 * t + g)) * C::kKeys;
-        const bool ok = wait_or_abort(&sh.s_full[g], (c_s + t) & 1, abort);
+        const bool ok = wait_for(&sh.s_full[g], (c_s + t) & 1, abort);
         if (!__all_sync(kFull, ok)) {  // tensor-memory loads are warp-collective: leave as a warp
           if (!*abort) fail();
           dead = true;
@@ -1128,17 +1122,18 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           // moves rarely, and they are then taken again
           uint32_t pw[16];
           weights(0, minus_m(), pw);
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          do {
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < 124; i += 8) {
+            for (int i = 4; i < 124; i += 8) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
-          }
-          const float top =
-              max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[124], s[125], s[125]), s[126], s[127])) * sscale;
-          if (!(top < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or an infinity among the scores
-          const bool grow = top > m_used + C::kLazy;
-          if (__any_sync(kFull, grow)) {
+              for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
+            }
+            const float top =
+                max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[124], s[125], s[125]), s[126], s[127])) * sscale;
+            if (!(top < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or an infinity among the scores
+            const bool grow = top > m_used + C::kLazy;
+            if (!__any_sync(kFull, grow)) break;
             float alpha = 1.f;
             if (grow) {
               alpha = fast_exp2(m_used - top);  // 0 while the row has seen nothing
@@ -1157,7 +1152,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             }
             sum[0] = sum[1] = make_float2(0.f, 0.f);
             weights(0, minus_m(), pw);
-          }
+          } while (false);
           const float negm = minus_m();
           tmem_st16u(scol, pw);
           weights(1, negm, pw);
@@ -1185,7 +1180,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
 
       // ---- epilogue: the output row, or its record
       if (!dead && nloc > 0) {
-        const bool ok = wait_or_abort(&sh.o_full[g], c_o & 1, abort);
+        const bool ok = wait_for(&sh.o_full[g], c_o & 1, abort);
         if (!__all_sync(kFull, ok)) {
           if (!*abort) fail();
           dead = true;
@@ -1222,19 +1217,21 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
         if constexpr (WIDE) {
           if (!split_out) {
-            uint32_t words[D / 2];
-#pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {  // (the words go to columns already read)
               float o[32];
               tmem_ld32(ocol + D * g + 32 * ch, o);
+              uint32_t words[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) words[16 * ch + i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+              for (int i = 0; i < 16; ++i) words[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+              turn_put(ocol + D * g + 16 * ch, words);
             }
-            TmemTurn<D / 2>::put(ocol + D * g, words);
+            tmem_wait_st();
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              uint32_t v[D / 4];
-              TmemTurn<D / 2>::get(ocol + D * g + (static_cast<uint32_t>(16 * half) << 16), v);
+            for (int it = 0; it < 2 * (D / 64); ++it) {
+              const int half = it & 1, c = it >> 1;  // rows, 64 columns
+              uint32_t v[16];
+              turn_get(ocol + D * g + 32 * c + (static_cast<uint32_t>(16 * half) << 16), v);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int rr = (r & ~31) + 16 * half + 8 * k + (lane >> 2);
@@ -1242,10 +1239,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
                 if (i >= w.ntok) continue;
                 uint4* dst = reinterpret_cast<uint4*>(
                                  p.out + (static_cast<int64_t>(w.tok0 + i) * p.hq + w.h * G + (rr & (G - 1))) * D) +
-                             (lane & 3);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                  dst[4 * c] = make_uint4(v[8 * c + k], v[8 * c + 2 + k], v[8 * c + 4 + k], v[8 * c + 6 + k]);
+                             8 * c + (lane & 3);
+                dst[0] = make_uint4(v[k], v[2 + k], v[4 + k], v[6 + k]);
+                dst[4] = make_uint4(v[8 + k], v[10 + k], v[12 + k], v[14 + k]);
               }
             }
           }
