@@ -721,6 +721,23 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       if (w.seq >= 0) {
         const Steps<WIDE> st(w, p, tile_tok);
         const int nstep = st.nstep;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
+        const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
+        // id of this lane's block in step j, asked for two steps ahead of its use (the first ones before
+        // the work is passed on and Q asked for): INT_MIN for a block past the context; its pool
+        // row: a block past the context, or with an id outside the pool, becomes a box entirely
+        // outside the tensor, which reads zeros
+        auto id_of = [&](int j) {
+          const int at = (st.k0 + j) * C::kStepBlocks + lane;
+          return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldcg(table + at) : INT_MIN;
+        };
+        auto row_of = [&](int id) {
+          if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
+          if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
+          return -kBlockSize;
+        };
+        const int id0 = id_of(0), id1 = id_of(1);
+        int id2 = id_of(2), id3 = id_of(3);
         ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
         ok = __all_sync(kFull, ok);
         if (ok) {
@@ -732,27 +749,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           ++n;
         }
         if (ok && nstep > 0) {
-          const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
-          const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
-          // id of this lane's block in step j, asked for two steps ahead of its use: INT_MIN for a block
-          // past the context; its pool row: a block past the context, or with an id outside the
-          // pool, becomes a box entirely outside the tensor, which reads zeros
-          auto id_of = [&](int j) {
-            const int at = (st.k0 + j) * C::kStepBlocks + lane;
-            return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldg(table + at) : INT_MIN;
-          };
-          auto row_of = [&](int id) {
-            if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
-            if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
-            return -kBlockSize;
-          };
-          int cur = row_of(id_of(0)), nxt = row_of(id_of(1));
-          int id2 = id_of(2), id3 = id_of(3);
           if constexpr (!FP8) {
             // Q's tiles are free once the last scores of the work before are done
             if (q_count > 0) ok = wait_for(&sh.q_empty, (q_count - 1) & 1, abort);
             ok = __all_sync(kFull, ok);
-            if (ok && lane == 0) {
+            if (ok && leader) {
               mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
 #pragma unroll
               for (int t = 0; t < (WIDE ? 2 : 1); ++t)
@@ -763,6 +764,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             }
           }
           if (ok) ++q_count;
+          int cur = row_of(id0), nxt = row_of(id1);
           // tiles in the ring's order: K of step 0, then K of step j + 1 and V of step j in turns
           unsigned issued = base;
           int j = 0;
