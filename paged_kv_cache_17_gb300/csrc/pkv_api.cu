@@ -920,17 +920,20 @@ namespace {
 // Query rows of a chunk (tokens x the heads of a group) per sequence, and how the chunk
 // attention is laid out over the SMs (one CTA each).
 //   wide: 256-row CTAs when a sequence has more than 128 rows on average.
-//   splits: the context is cut into runs of whole 128-key steps when the tiles alone leave SMs
-//   idle; the count minimises  waves x (steps per CTA x step time + CTA start and end)  plus, when
-//   there is more than one, writing and reading the records.  PKV_SPLIT_TOKENS fixes the run.
+//   splits: the context is cut into runs of whole 128-key steps, for SMs that the tiles alone would
+//   leave idle.  CTAs take works as they finish, so the time is modelled as the larger of one
+//   work's (when there are fewer works than SMs) and an SM's share of all steps and works plus half a work
+//   for the uneven end; with records, their writing and reading and the merge kernel on top.  The
+//   choice was the best or within 3 % of it on a sweep of runs for one token over 777, 24 x 3-8 tokens over
+//   1800-12,000, 4096 over 32,768 and 16 x 1-448 over 750-1500.  PKV_SPLIT_TOKENS fixes the run.
 struct PrefillPlan {
   bool wide;
   int tile_slots, splits, split_tiles;
   size_t ml_bytes, ws_bytes;
 };
 
-constexpr double kPrefillStepUs[2] = {0.75, 1.15};  // a narrow / wide step of 128 keys
-constexpr double kPrefillCtaUs = 4.0;               // a CTA's start and end
+constexpr double kPrefillStepUs[2] = {1.0, 1.6};    // a narrow / wide step of 128 keys, head_dim 128
+constexpr double kPrefillWorkUs = 3.0;              // a work's start and end
 constexpr double kPrefillMergeUs = 4.0;             // the merge kernel
 constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
 constexpr long long kPrefillMaxRecords = 1LL << 20;
@@ -961,8 +964,9 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
       const int run = (steps + n - 1) / n;
       if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
       if (n > 1 && rows * n > kPrefillMaxRecords) break;
-      const long long waves = (tiles * hkv * n + sm_count - 1) / sm_count;
-      double us = static_cast<double>(waves) * (run * kPrefillStepUs[pp.wide] + kPrefillCtaUs);
+      const double one = run * kPrefillStepUs[pp.wide];
+      const double share = static_cast<double>(tiles * hkv * n) / sm_count;
+      double us = std::max(one + kPrefillWorkUs, share * (one + kPrefillWorkUs) + one / 2);
       if (n > 1) us += kPrefillMergeUs + 2.0 * static_cast<double>(rows) * n * (d + 2) * 4 / kPrefillRecordBytesPerUs;
       if (best < 0 || us < best) {
         best = us;

@@ -874,7 +874,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         // rows below seen: every row's; from end on: no row's
         const int seen = st.lim_min - key0, end = w.ctx - key0;
         uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
-        // E4M3: expand the tile, eight pieces in registers at a time (one by one, a load and a store
+        // E4M3: expand the tile, four pieces in registers at a time (one by one, a load and a store
         // each, a tile took 2600 cycles and the step waited for it); rows no row sees become zeros.
         // bf16: only the rows that not every row sees, four pieces at a time.  True if one of those
         // that some row sees is not finite.
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         bool odd = false;
         if (ok) {
           if constexpr (FP8) {
-            constexpr int kBatch = 8;
+            constexpr int kBatch = 4;
             static_assert(C::kKeys % (kBatch * kStep) == 0, "whole batches");
 #pragma unroll 1
             for (int b0 = r0; b0 < C::kKeys; b0 += kBatch * kStep) {
