@@ -24,7 +24,16 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PrefillParams 
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
   if (row >= rows) return;
   const int tok = static_cast<int>(row / p.hq), head = static_cast<int>(row - static_cast<int64_t>(tok) * p.hq);
-  if (tok < p.q_indptr[0] || tok >= p.q_indptr[p.batch]) return;  // behind the last sequence: left as it was
+  // the row's sequence: the last that starts at or before it.  A row of none, behind the last one or of
+  // a bad range (which the attention skipped), is left as it was
+  int b = 0, e = p.batch;
+  while (e - b > 1) {
+    const int mid = (b + e) >> 1;
+    if (p.q_indptr[mid] <= tok) b = mid;
+    else e = mid;
+  }
+  const int first = p.q_indptr[b], last = p.q_indptr[b + 1];
+  if (tok < first || tok >= last || first < 0 || last > p.total_q) return;
 
   float M = -INFINITY;
   for (int j = lane; j < p.splits; j += 32) M = fmaxf(M, p.part_ml[j * rows + row].x);
@@ -34,20 +43,19 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PrefillParams 
   float num[DPL];
 #pragma unroll
   for (int i = 0; i < DPL; ++i) num[i] = 0.f;
-  if (M != -INFINITY) {
 #pragma unroll 4
-    for (int j = 0; j < p.splits; ++j) {
-      const float2 ml = p.part_ml[j * rows + row];
-      if (ml.x == -INFINITY) continue;  // an empty record has no output part
-      const float wgt = fast_exp2(ml.x - M);
-      const VecT v = __ldcs(reinterpret_cast<const VecT*>(p.part_acc + (j * rows + row) * D) + lane);
-      den = fmaf(wgt, ml.y, den);
-      num[0] = fmaf(wgt, v.x, num[0]);
-      num[1] = fmaf(wgt, v.y, num[1]);
-      if constexpr (DPL == 4) {
-        num[2] = fmaf(wgt, v.z, num[2]);
-        num[3] = fmaf(wgt, v.w, num[3]);
-      }
+  for (int j = 0; j < p.splits; ++j) {
+    const float2 ml = p.part_ml[j * rows + row];
+    if (ml.y == 0.f) continue;  // an empty record has no output part
+    // (a record whose first scores held a NaN has reference -inf and a sum that is NaN)
+    const float wgt = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    const VecT v = __ldcs(reinterpret_cast<const VecT*>(p.part_acc + (j * rows + row) * D) + lane);
+    den = fmaf(wgt, ml.y, den);
+    num[0] = fmaf(wgt, v.x, num[0]);
+    num[1] = fmaf(wgt, v.y, num[1]);
+    if constexpr (DPL == 4) {
+      num[2] = fmaf(wgt, v.z, num[2]);
+      num[3] = fmaf(wgt, v.w, num[3]);
     }
   }
   float inv = den > 0.f || den != den ? 1.f / den : 0.f;

@@ -993,6 +993,7 @@ pkv_status check_prefill_sizes(int32_t batch, int32_t total_q, int32_t hq, int32
     return fail(PKV_ERR_UNSUPPORTED, "query-group size %d not in {1, 2, 4, 8}", g);
   if (d != 64 && d != 128) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
   if (max_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len must be >= 0");
+  if (max_len > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "max_context_len above 2^30");
   // CTAs of the attention (a slot per tile and kv head) and rows of the merge
   if ((static_cast<long long>(total_q) + batch) * hkv > 0x7fffffffLL ||
       static_cast<long long>(total_q) * hq > 8LL * 0x7fffffff)
@@ -1061,7 +1062,7 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
     return fail(PKV_ERR_INVALID_ARG, "max_context_len %d exceeds max_blocks_per_seq * 16 = %lld", max_context_len,
                 static_cast<long long>(max_blocks_per_seq) * 16);
   if (causal != 0 && causal != 1) return fail(PKV_ERR_INVALID_ARG, "causal must be 0 or 1");
-  if (!std::isfinite(softmax_scale)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (!(std::fabs(softmax_scale) < 1e38f)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite, below 1e38");
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
   const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;

@@ -1041,7 +1041,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           int ex = 0;
           if (top > 0.f && !odd) ex = 7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
           ex = min(ex, 126);  // rows below 2^-119: their codes lose what lies under 2^-135
-          const float up = __uint_as_float(static_cast<uint32_t>(max(ex, -126) + 127) << 23);
+          const float k_scale = p.scales[w.h];
+          const float size = __uint_as_float(static_cast<uint32_t>(max(ex, -126) + 127) << 23);
+          const float up = k_scale < 0.f ? -size : size;  // the scores' factor below stays positive
           const uint32_t qt = q_base + (WIDE ? g : 0) * C::kQTile;
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {  // 16 codes: one 16-byte piece of the row
@@ -1063,7 +1065,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.q_full);
           // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
-          sscale = odd ? __int_as_float(0x7fffffff) : sscale * p.scales[w.h] / up;
+          // (a zero scale: a factor that leaves every score at 0 while masked ones stay -inf)
+          sscale = odd || k_scale != k_scale ? __int_as_float(0x7fffffff) : fmaxf(sscale * fabsf(k_scale) / size, 1e-37f);
         }
         if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
           if (g == 0) join_scale[r] = sscale;

@@ -302,3 +302,146 @@ def test_other_stream(pkv):
     for o in got[1:]:
         assert torch.equal(o, got[0])
     assert float((got[0].float() - want.float()).abs().max()) < 0.05
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 128])
+def test_scores_not_finite(pkv, e4m3, split):
+    """A key that is NaN spoils the rows that see it and no others, whichever part of the context it is in."""
+    lens, ctx = [40, 2], [300, 260]
+    for j in (3, 130, 280):
+        data = list(make(lens, ctx, 8, 2, 64, e4m3, 61))
+        k, tables = data[1], data[4]
+        blk = int(tables[0, j // 16])
+        if e4m3:
+            k.view(torch.uint8)[blk, j % 16, 1, 9] = 0x7F
+        else:
+            k[blk, j % 16, 1, 9] = math.nan
+        with split_tokens(split):
+            out = pkv.paged_prefill_attention(data[0], indptr(lens), k, data[2], tables,
+                                              torch.tensor(ctx, dtype=torch.int32, device="cuda"), 0.125, scales=data[3])
+        bad = torch.isnan(out).all(-1)
+        want = torch.zeros_like(bad)
+        first = max(0, j - (300 - 40))
+        want[first:40, 4:8] = True  # the rows at or past position j, the heads of kv head 1
+        assert torch.equal(bad, want) and torch.equal(torch.isnan(out).any(-1), want)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_scales_of_the_pool_of_any_sign(pkv, causal):
+    lens, ctx = [70, 300], [400, 500]
+    data = list(make(lens, ctx, 8, 4, 64, True, 67))
+    data[3][0, 1] *= -1
+    data[3][0, 2] = 0
+    data[3][1, 0] *= -1
+    check(pkv, lens, ctx, 8, 4, 64, True, causal=causal, data=data)
+    check(pkv, lens, ctx, 8, 4, 64, True, causal=causal, data=data, scale=-0.1, split=128)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_sequences(pkv, e4m3):
+    """More sequences than one warp looks over at a time, some without rows, some without context."""
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 4, (150,), generator=g).tolist()
+    ctx = [max(n, int(c)) for n, c in zip(lens, torch.randint(0, 200, (150,), generator=g))]
+    ctx[7] = 0
+    check(pkv, lens, ctx, 8, 2, 64, e4m3)
+    lens[100] = 900  # a long one among them: 256-row works on average no more
+    ctx[100] = 1000
+    check(pkv, lens, ctx, 8, 2, 64, e4m3)
+
+
+@pytest.mark.parametrize("split", [None, 128])
+def test_bad_range_leaves_its_rows(pkv, split):
+    lens, ctx = [5, 6, 4], [300, 200, 260]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 64, False, 71, junk=0.0)
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    ip = indptr(lens)
+    ip[3] = 99
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    pkv.check_device_status()
+    with split_tokens(split):
+        pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.125, out)
+    assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+    assert bool((out[11:] == 7).all()) and not bool((out[:11] == 7).all(-1).any())
+
+
+def test_replay_with_other_lengths(pkv):
+    """A captured call replayed after its offsets, lengths, tables and queries were overwritten: a padded batch
+    whose real tokens change from step to step."""
+    lens, ctx = [9, 30, 0, 25], [500, 30, 70, 400]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, False, 81)
+    c, ip = torch.tensor(ctx, dtype=torch.int32, device="cuda"), indptr(lens)
+    out = torch.empty_like(q)
+    pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1, out)
+    for lens2, ctx2 in (([9, 30, 0, 25], [500, 30, 70, 400]), ([1, 1, 1, 1], [499, 30, 2, 17]), ([0, 0, 60, 2], [3, 3, 70, 390])):
+        ip.copy_(indptr(lens2))
+        c.copy_(torch.tensor(ctx2, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        want = torch.full_like(out, 7.0)
+        pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1, want)
+        assert torch.equal(out, want) and bool((out[sum(lens2):] == 7).all())
+
+
+def test_two_streams_at_once(pkv):
+    jobs = []
+    for seed in (91, 92):
+        lens, ctx = [700, 3], [900, 2000]
+        q, k, v, scales, tables = make(lens, ctx, 16, 2, 128, seed == 92, seed)
+        c, ip = torch.tensor(ctx, dtype=torch.int32, device="cuda"), indptr(lens)
+        want = pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.1, scales=scales)
+        jobs.append(((q, ip, k, v, tables, c, 0.1), scales, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (args, scales, _, s) in enumerate(jobs):
+            with torch.cuda.stream(s):
+                got[i].append(pkv.paged_prefill_attention(*args, scales=scales))
+    torch.cuda.synchronize()
+    for i, (_, _, want, _) in enumerate(jobs):
+        assert all(torch.equal(o, want) for o in got[i])
+
+
+def test_binding_refusals_on_the_gpu(pkv):
+    lens, ctx = [5], [40]
+    q, k, v, scales, tables = make(lens, ctx, 8, 2, 64, False, 3)
+    c, ip = torch.tensor(ctx, dtype=torch.int32, device="cuda"), indptr(lens)
+    f = pkv.paged_prefill_attention
+    with pytest.raises(TypeError):
+        f(q.float(), ip, k, v, tables, c, 0.1)
+    with pytest.raises(ValueError):
+        f(q[:, :, :32], ip, k, v, tables, c, 0.1)
+    with pytest.raises(ValueError):
+        f(q, ip.cpu(), k, v, tables, c, 0.1)
+    with pytest.raises(ValueError):
+        f(q, ip.long(), k, v, tables, c, 0.1)
+    with pytest.raises(TypeError):
+        f(q, ip, k, v, tables.long(), c, 0.1)
+    with pytest.raises(ValueError):
+        f(q, ip, k, v[:, :, :1], tables, c, 0.1)
+    with pytest.raises(ValueError):
+        f(q, ip, k, v, tables, c, 0.1, torch.empty((5, 8, 64), device="cuda"))
+    with pytest.raises(ValueError):
+        f(q, ip, k, v, tables, c, 0.1, lse=torch.empty((5, 9), device="cuda"))
+    with pytest.raises(pkv.PkvError):
+        f(q, ip, k, v, tables, c, 0.1, max_context_len=10 ** 6)
+    with pytest.raises(pkv.PkvError):
+        f(q[:, :6].contiguous(), ip, k, v, tables, c, 0.1)
+    with pytest.raises(ValueError):
+        f(q, ip, k, v, tables, c, 0.1, scales=torch.ones((2, 3), device="cuda"))
+    with split_tokens(128):  # a workspace that is too small
+        q2, k2, v2, _, t2 = make([5], [400], 8, 2, 64, False, 3)
+        c2 = torch.tensor([400], dtype=torch.int32, device="cuda")
+        with pytest.raises(pkv.PkvError) as e:
+            f(q2, ip, k2, v2, t2, c2, 0.1, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == pkv.PKV_ERR_WORKSPACE
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope_append(q, q[:, :2], q[:, :2], None, torch.arange(5, device="cuda"), k, v,
+                                inv_freq=torch.ones(32, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError):
+        pkv.paged_kv_gather(k, v, tables, ip, q[:, :3], q[:, :3])
