@@ -373,7 +373,7 @@ pkv_status pkv_stage_copy(void* dst, const void* src, size_t bytes, pkv_stream_t
  *   q_weight, k_weight: [head_dim] bf16, 16-byte aligned, or NULL.
  *   q_out: may be q itself (same pointer and stride); any other overlap with the inputs is not
  *     allowed (with q it is refused).
- *   num_tokens == 0 is a no-op.
+ *   At most 4096 query and 4096 kv heads.  num_tokens == 0 is a no-op.
  */
 typedef struct {
   const void* q;
@@ -417,12 +417,14 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
  *     [total_q][num_q_heads], or NULL).  A row that sees no key: out 0, lse -inf.
  *   What the pages hold past a context or at positions a row does not see does not reach that
  *   row, NaN and infinities included.
- *   num_q_heads / num_kv_heads in {1, 2, 4, 8}, head_dim 64 or 128, bf16 or E4M3 pools.
+ *   num_q_heads / num_kv_heads in {1, 2, 4, 8}, head_dim 64 or 128, bf16 or E4M3 pools;
+ *   max_context_len at most 2^30, |softmax_scale| below 1e38 (it may be zero or negative).
  *   Arithmetic: tensor-core products with fp32 accumulation and fp32 softmax statistics; the
  *   softmax weights enter the second product rounded to bf16 (bf16 pools) or fp16 (E4M3 pools);
  *   q enters as it is (E4M3 pools: elements smaller than 2^-10 of their row's largest to within
  *   2^-18 of it).  Deterministic for given sizes and values; PKV_SPLIT_TOKENS fixes the partition
- *   length (rounded up to a multiple of 128).
+ *   length (rounded up to a multiple of 128, at most 65,536: longer sums of products would lose
+ *   accuracy, the tensor cores' additions being truncated).
  *   workspace: pkv_prefill_workspace_size(...) bytes, 256-byte aligned, any contents, NULL when
  *     0; not to be used by two calls that can run at the same time.
  *   batch == 0 or total_q == 0 is a no-op.
@@ -449,7 +451,7 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
  *   A position outside [0, max_blocks_per_seq * 16) reads as zeros and sets
  *   PKV_DEVFLAG_BAD_CONTEXT_LEN; a block id outside the pool reads as zeros and sets
  *   PKV_DEVFLAG_BAD_BLOCK_ID.
- *   batch == 0 or num_rows == 0 is a no-op.
+ *   At most 4096 kv heads.  batch == 0 or num_rows == 0 is a no-op.
  */
 pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
                                const int32_t* kv_indptr, const int32_t* starts, int32_t batch, int64_t num_rows,

@@ -926,6 +926,10 @@ namespace {
 //   for the uneven end; with records, their writing and reading and the merge kernel on top.  The
 //   choice was the best or within 3 % of it on a sweep of runs for one token over 777, 24 x 3-8 tokens over
 //   1800-12,000, 4096 over 32,768 and 16 x 1-448 over 750-1500.  PKV_SPLIT_TOKENS fixes the run.
+//   A run has at most 512 steps (65,536 keys), however many records that takes: the tensor cores add
+//   to their fp32 accumulators by truncation, up to 2^-23 of the sum for each of a step's 8 additions,
+//   all towards zero.  One run over 2^20 keys of positive V came out 0.67 % low, over 2^17 0.09 %; the
+//   limit keeps it below 2^-11, an eighth of the output's rounding to bf16.  (The merge adds in rounded fp32.)
 struct PrefillPlan {
   bool wide;
   int tile_slots, splits, split_tiles;
@@ -937,6 +941,7 @@ constexpr double kPrefillWorkUs = 3.0;              // a work's start and end
 constexpr double kPrefillMergeUs = 4.0;             // the merge kernel
 constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
 constexpr long long kPrefillMaxRecords = 1LL << 20;
+constexpr int kPrefillMaxRun = 512;                 // steps
 
 PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max_context_len, int sm_count) {
   const int g = hq / hkv;
@@ -953,17 +958,18 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
   int forced = 0;
   if (const char* env = std::getenv("PKV_SPLIT_TOKENS")) {
     const long v = std::strtol(env, nullptr, 10);
-    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, steps));
+    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, std::min(steps, kPrefillMaxRun)));
   }
   if (forced > 0) {
     pp.split_tiles = forced;
     pp.splits = (steps + forced - 1) / forced;
   } else {
     double best = -1;
-    for (int n = 1; n <= std::min(steps, 48); ++n) {
+    const int least = (steps + kPrefillMaxRun - 1) / kPrefillMaxRun;
+    for (int n = least; n <= std::max(least, std::min(steps, 48)); ++n) {
       const int run = (steps + n - 1) / n;
       if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
-      if (n > 1 && rows * n > kPrefillMaxRecords) break;
+      if (n > least && rows * n > kPrefillMaxRecords) break;
       const double one = run * kPrefillStepUs[pp.wide];
       const double share = static_cast<double>(tiles * hkv * n) / sm_count;
       double us = std::max(one + kPrefillWorkUs, share * (one + kPrefillWorkUs) + one / 2);

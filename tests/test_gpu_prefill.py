@@ -203,6 +203,36 @@ def test_long_context_long_offsets(pkv):
     assert torch.equal(ko, k[-40:].flatten(0, 1)) and torch.equal(vo, v[-40:].flatten(0, 1))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 1 << 22])
+def test_long_sums_keep_their_size(pkv, e4m3, split):
+    """2^20 keys (256 blocks over and over) of values in [0.5, 1.5): all terms of the sums have one
+    sign, and the tensor cores truncate their additions.  A run of at most 512 steps adds 8 x 512
+    times, each off by at most 2^-23 of the sum: 2^-11.  Roundings of the weights and the output have
+    either sign; over the 25,600 elements of the mean they leave under 2^-12.  One run over all keys was off by
+    2^-7.2."""
+    d, n = 64, 1 << 20
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn((256, 16, 1, d), generator=g).to(torch.bfloat16).cuda()
+    v = (torch.rand((256, 16, 1, d), generator=g) + 0.5).to(torch.bfloat16).cuda()
+    scales = None
+    if e4m3:
+        k, v, scales = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), torch.ones(2, 1, device="cuda")
+    q = torch.randn((100, 4, d), generator=g).to(torch.bfloat16).cuda()
+    tables = (torch.arange(n // 16, dtype=torch.int32, device="cuda") % 256).view(1, -1)
+    c = torch.tensor([n], dtype=torch.int32, device="cuda")
+    with split_tokens(split):
+        out = pkv.paged_prefill_attention(q, indptr([100]), k, v, tables, c, 0.125, causal=False, scales=scales)
+        assert pkv.check_device_status() == 0
+    s = torch.einsum("thd,jd->thj", q.double(), k.double().view(-1, d)) * 0.125
+    ref = torch.softmax(s, -1) @ v.double().view(-1, d)
+    off = (out.double() - ref) / ref
+    assert abs(float(off.mean())) <= 2.0 ** -11 + 2.0 ** -12
+    # one element: the output's rounding, the sums' 2^-11, and as much for the weights' (the mean of over a
+    # thousand of their roundings)
+    assert float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -10
+
+
 def test_strided_queries(pkv):
     lens, ctx = [37, 90], [200, 90]
     q, k, v, scales, tables = make(lens, ctx, 8, 2, 128, False, 17)
