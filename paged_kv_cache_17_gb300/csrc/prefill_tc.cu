@@ -22,19 +22,36 @@
 //   narrow  128 rows (few new tokens): one tile, whose 128-key steps are dealt alternately to
 //           the two softmax groups, each with its own statistics and output; joined at the end.
 //
-//   warps 0-3, 4-7  softmax groups 0 and 1: thread r owns row r (TMEM lane r): scores in,
-//                   weights out over them as 16-bit pairs, rare rescale of the output, epilogue
-//   warp 8          lane 0 issues every MMA
-//   warp 9          TMA: one 16-token block (and 64-column half) per lane and step
-//   warps 10, 11    V: zero the rows past the context in the last tile, so that what a page
-//                   holds there (NaN included) meets weight 0 as 0; E4M3: expand V to fp16
+//   warps 0-3, 4-7  softmax groups 0 and 1: thread r owns row r (TMEM lane r): scores in, weights
+//                   out over them as 16-bit pairs, rare rescale of the output, epilogue
+//   warps 8, 10     issue the MMAs, a warp per tile (narrow: warp 8 for both groups)
+//   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block (and
+//                   64-column half) at a time
+//   warps 12-15     V: zero the rows past the context in the last tile, so that what a page holds
+//                   there (NaN included) meets weight 0 as 0; E4M3: expand V to fp16
 // A value of V that is not finite at a position some rows see and others do not would reach
 // the latter as 0 * NaN; in the tiles where the mask cuts, such values are taken out of the
 // tile, and added to the rows that see them in the epilogue.
 //
+// A CTA stays: when its work (a tile or two of one kv head, or one of its context's splits) is
+// done it takes the next that no CTA has started (cluster launch control), so that Q, K, V and
+// the first scores of the next work come in under the softmax and the epilogue of the last.
+//
 // Shared memory: Q (both tiles, or E4M3 hi and lo), a ring of K and V tiles of 128 keys in the
 // order K0 K1 V0 K2 V1 .., E4M3 two fp16 V tiles.  TMEM (512 columns): scores, then weights, of
 // group w at 128 w; outputs at 256 + w D.
+//
+// What bounds it.  A wide step is 2048 cycles of products at D = 128; the tensor cores are kept fed
+// but for the part of the chain scores -> weights -> products that the other tile does not cover:
+// 4096 tokens over 32,768, 32 + 8 heads, bf16: 1.29 ms = 1.60 PFLOP/s, 86 % of the measured cuBLAS
+// rate (1.08 ms with the softmax left out).  The exponentials, 32 a cycle and SM, take half of a
+// step; a polynomial on the FMA pipe for a share of them costs more than it saves, and two threads a
+// row, 16 softmax warps, slow the other roles down more than they gain (1.46 ms).  Prompts of 257 to
+// 2048 tokens: 118 us, 59 % of the rate: a work is a handful of steps there, and its start, masked
+// steps and epilogue weigh beside them.  24 x 3 to 8 tokens over 1800 to 12,000 (narrow, split in
+// 3): 117 us = 5.3 TB/s of K and V, 78 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
+// 3000 to 9000, 64 + 8 heads: 0.52 ms = 1.39 PFLOP/s; V's expansion takes shared-memory
+// bandwidth and issue slots from the products and the softmax.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -93,7 +110,7 @@ struct PrefillShared {
   uint64_t o_full[2];          // every product of the group's work done
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
-  uint64_t v_sent[8];          // load of a V tile that warps 10, 11 work on issued
+  uint64_t v_sent[8];          // load of a V tile that warps 12-15 work on issued
   uint64_t q_full, q_empty;
   uint64_t work_full[2], work_empty[2];
   uint64_t clc;                // answer of the work query landed
@@ -189,9 +206,11 @@ __device__ __forceinline__ void give_up(uint32_t* status, volatile int* abort) {
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 #pragma unroll
@@ -199,9 +218,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+      "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
       "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
       : "memory");
 }
 
@@ -214,8 +239,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // 16 consecutive columns of this thread's lane; no wait (see tmem_wait_st).
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-               : "memory");
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+      "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -298,16 +327,24 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 // through tensor memory: written a row a thread, 16 words at a time, read back with four lanes to a
 // row's four columns.  No wait in put.
 __device__ __forceinline__ void turn_put(uint32_t taddr, const uint32_t (&w)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]), "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15])
-               : "memory");
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+      "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[4]), "r"(w[8]), "r"(w[12]), "r"(w[1]), "r"(w[5]), "r"(w[9]), "r"(w[13]), "r"(w[2]),
+      "r"(w[6]), "r"(w[10]), "r"(w[14]), "r"(w[3]), "r"(w[7]), "r"(w[11]), "r"(w[15])
+      : "memory");
 }
 // 32 words of rows lane / 4 and lane / 4 + 8 of the 16 from taddr's lane: v[8 c + 2 j + k], word
 // 16 c + 4 (lane % 4) + j of row lane / 4 + 8 k
 __device__ __forceinline__ void turn_get(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-               : "r"(taddr)
-               : "memory");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // One CTA's worth of work, and what every role derives from it
@@ -450,529 +487,531 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
   // the registers of the launch, dealt out anew: 184 to a softmax thread, 72 to another (208 and 48:
   // the other roles spill, 158 against 149 us for nine prompts of 257 to 2048 tokens)
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
-  if (warp == C::kIssuerWarp || warp == C::kIssuer2Warp) {
-    // ======================================================================== MMA issuers
-    // wide: one warp per tile, each going through every step of K and V in order; narrow: one warp
-    // for both groups
-    if (warp == C::kIssuerWarp || WIDE) {
-      const uint32_t leader = elect_one();
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_for(bar, parity, abort)); };
-      auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
-      constexpr uint32_t kIdO = idesc_f16(C::kRows, D, !FP8, true);
-      // scores: A = Q with its sign turned (bit 13) for a negative scale; E4M3 formats are 0
-      const uint32_t id_s = (FP8 ? idesc_f16(C::kRows, C::kKeys, false, false)
-                                 : idesc_f16(C::kRows, C::kKeys, true, false)) |
-                            (p.negate ? 1u << 13 : 0u);
-      const uint32_t tm = same(tmem);
-      const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, C::kHalf16));
-      const uint32_t exp_v_lo = same(desc_lo(smem_u32(smem + C::kOffExp), C::kHalf16));
-      const uint32_t q0_lo = same(desc_lo(q_base, 16));
-      auto issue_s = [&](int g, unsigned slot) {
-        const uint32_t k_lo = same(ring_lo + slot * (C::kSlot / 16));
-        const uint32_t q_lo = q0_lo + (WIDE ? g : 0) * (C::kQTile / 16);
-        const uint32_t d = tm + C::kColS + 128 * g;
-        if constexpr (FP8) {
-          constexpr uint32_t hi = D == 128 ? kDescK128 : kDescK64;
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, hi, id_s, part > 0 || kk > 0,
-                           leader);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = ((kk >> 2) * C::kHalf16 + (kk & 3) * 32) / 16;
-            mma_ss<false>(d, q_lo + at, k_lo + at, kDescK128, id_s, kk > 0, leader);
-          }
-        }
-        commit(&sh.s_full[g], leader);
-      };
-      // keys 64 half .. of a step
-      auto issue_o = [&](int g, int half, bool first, uint32_t v_lo0) {
-        const uint32_t pt = tm + C::kColS + 128 * g;
-        const uint32_t v_lo = same(v_lo0);
-#pragma unroll
-        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-          mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, !first || kk > 0, leader);
-      };
-
-      Cursor<C::kSlots> base{0, 0};  // ring position of the work's first tile
-      unsigned steps_done = 0, cuts = 0, q_count = 0;
-      unsigned c_p[2] = {0, 0};  // steps of the groups so far
-      bool ok = true;
-      Work w;
-      for (unsigned n = 0; ok && next_work(n, w); ++n) {
-        const Steps<WIDE> st(w, p, tile_tok);
-        const int nstep = st.nstep;
-        if (nstep == 0) continue;
-        Cursor<C::kSlots> kc = base, vc = base;
-        vc.advance(nstep == 1 ? 1 : 2);
-        auto next_k = [&](int j) { kc.advance(j == 0 ? 1 : 2); };               // from K of step j to the next
-        auto next_v = [&](int j) { vc.advance(j + 2 == nstep ? 1 : 2); };       // from V of step j to the next
-        auto wait_k = [&]() { return wait(&sh.full[kc.slot], kc.phase); };
-        // V of step j is ready for the tensor cores
-        auto wait_v = [&](int j) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
+    if (warp == C::kIssuerWarp || warp == C::kIssuer2Warp) {
+      // ======================================================================== MMA issuers
+      // wide: one warp per tile, each going through every step of K and V in order; narrow: one warp
+      // for both groups
+      if (warp == C::kIssuerWarp || WIDE) {
+        const uint32_t leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_for(bar, parity, abort)); };
+        auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
+        constexpr uint32_t kIdO = idesc_f16(C::kRows, D, !FP8, true);
+        // scores: A = Q with its sign turned (bit 13) for a negative scale; E4M3 formats are 0
+        const uint32_t id_s = (FP8 ? idesc_f16(C::kRows, C::kKeys, false, false)
+                                   : idesc_f16(C::kRows, C::kKeys, true, false)) |
+                              (p.negate ? 1u << 13 : 0u);
+        const uint32_t tm = same(tmem);
+        const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, C::kHalf16));
+        const uint32_t exp_v_lo = same(desc_lo(smem_u32(smem + C::kOffExp), C::kHalf16));
+        const uint32_t q0_lo = same(desc_lo(q_base, 16));
+        auto issue_s = [&](int g, unsigned slot) {
+          const uint32_t k_lo = same(ring_lo + slot * (C::kSlot / 16));
+          const uint32_t q_lo = q0_lo + (WIDE ? g : 0) * (C::kQTile / 16);
+          const uint32_t d = tm + C::kColS + 128 * g;
           if constexpr (FP8) {
-            const unsigned v = steps_done + j;
-            return wait(&sh.fixed[v & 1], (v >> 1) & 1);
+            constexpr uint32_t hi = D == 128 ? kDescK128 : kDescK64;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, hi, id_s, part > 0 || kk > 0,
+                             leader);
           } else {
-            if (j >= st.first_cut) {
-              const unsigned c = cuts + j - st.first_cut;
-              return wait(&sh.fixed[c & 7], (c >> 3) & 1);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = ((kk >> 2) * C::kHalf16 + (kk & 3) * 32) / 16;
+              mma_ss<false>(d, q_lo + at, k_lo + at, kDescK128, id_s, kk > 0, leader);
             }
-            return wait(&sh.full[vc.slot], vc.phase);
           }
+          commit(&sh.s_full[g], leader);
         };
-        auto v_lo = [&](int j) {
-          return FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16) : ring_v_lo + vc.slot * (C::kSlot / 16);
+        // keys 64 half .. of a step
+        auto issue_o = [&](int g, int half, bool first, uint32_t v_lo0) {
+          const uint32_t pt = tm + C::kColS + 128 * g;
+          const uint32_t v_lo = same(v_lo0);
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, !first || kk > 0, leader);
         };
-        auto free_v = [&](int j) { commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader); };
-        ok = wait(&sh.q_full, q_count & 1);
-        ++q_count;
-        if constexpr (WIDE) {
-          // The scores of step j + 1 follow P V of step j in the same columns, in issue order.  The
-          // tiles take turns, so that one's products run under the other's softmax (left to themselves
-          // they fell into step and waited for the tensor cores together: 1681 against 1508 us for
-          // 4096 tokens over 32768, 32 heads).  The fifth arrival on p_half is the other issuer's, once its
-          // turn before is over: on tile 0's for a work's first step when tile 1 is through with the work
-          // before, then after tile 1's step before; on tile 1's after tile 0's same step, or, past
-          // tile 0's last, issuer 1's own.  A tile 1 without steps watches tile 0's instead.  So no
-          // arrival comes before the phase it belongs to: whoever arrives has seen the one before.
-          // Steps past the tile's own are waited for all the same: a slot's phases are seen in order.
-          const int g = warp == C::kIssuerWarp ? 0 : 1;
-          const int mine = g == 0 ? st.n_of[0] : st.n_of[1], other = g == 0 ? st.n_of[1] : st.n_of[0];
-          unsigned parity = (g == 0 ? c_p[0] : c_p[1]) & 1;
-          if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_half[0]);
-          ok = ok && wait_k();
-          if (ok) {
-            tc_fence_after();
-            if (mine > 0) issue_s(g, kc.slot);
-            commit(&sh.empty[kc.slot], leader);
-            if (nstep == 1) commit(&sh.q_empty, leader);
-          }
-          for (int j = 0; j < nstep && ok; ++j) {
-            const bool more = j + 1 < nstep;
-            ok = wait_v(j);
-            if (more) next_k(j);
-            if (!FP8 && more && ok) ok = wait_k();  // before the weights, where waiting costs nothing
-            if (!ok) break;
-            if (j < mine) {
-              if (g == 1 && j >= other && leader) mbar_arrive(&sh.p_half[1]);
-              ok = wait(&sh.p_half[g], parity);
-              if (!ok) break;
+
+        Cursor<C::kSlots> base{0, 0};  // ring position of the work's first tile
+        unsigned steps_done = 0, cuts = 0, q_count = 0;
+        unsigned c_p[2] = {0, 0};  // steps of the groups so far
+        bool ok = true;
+        Work w;
+        for (unsigned n = 0; ok && next_work(n, w); ++n) {
+          const Steps<WIDE> st(w, p, tile_tok);
+          const int nstep = st.nstep;
+          if (nstep == 0) continue;
+          Cursor<C::kSlots> kc = base, vc = base;
+          vc.advance(nstep == 1 ? 1 : 2);
+          auto next_k = [&](int j) { kc.advance(j == 0 ? 1 : 2); };               // from K of step j to the next
+          auto next_v = [&](int j) { vc.advance(j + 2 == nstep ? 1 : 2); };       // from V of step j to the next
+          auto wait_k = [&]() { return wait(&sh.full[kc.slot], kc.phase); };
+          // V of step j is ready for the tensor cores
+          auto wait_v = [&](int j) {
+            if constexpr (FP8) {
+              const unsigned v = steps_done + j;
+              return wait(&sh.fixed[v & 1], (v >> 1) & 1);
+            } else {
+              if (j >= st.first_cut) {
+                const unsigned c = cuts + j - st.first_cut;
+                return wait(&sh.fixed[c & 7], (c >> 3) & 1);
+              }
+              return wait(&sh.full[vc.slot], vc.phase);
+            }
+          };
+          auto v_lo = [&](int j) {
+            return FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16) : ring_v_lo + vc.slot * (C::kSlot / 16);
+          };
+          auto free_v = [&](int j) { commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader); };
+          ok = wait(&sh.q_full, q_count & 1);
+          ++q_count;
+          if constexpr (WIDE) {
+            // The scores of step j + 1 follow P V of step j in the same columns, in issue order.  The
+            // tiles take turns, so that one's products run under the other's softmax (left to themselves
+            // they fall into step and wait for the tensor cores together: a tenth slower for 4096 tokens
+            // over 32768, 32 heads).  The fifth arrival on p_half is the other issuer's, once its
+            // turn before is over: on tile 0's for a work's first step when tile 1 is through with the work
+            // before, then after tile 1's step before; on tile 1's after tile 0's same step, or, past
+            // tile 0's last, issuer 1's own.  A tile 1 without steps watches tile 0's instead.  So no
+            // arrival comes before the phase it belongs to: whoever arrives has seen the one before.
+            // Steps past the tile's own are waited for all the same: a slot's phases are seen in order.
+            const int g = warp == C::kIssuerWarp ? 0 : 1;
+            const int mine = g == 0 ? st.n_of[0] : st.n_of[1], other = g == 0 ? st.n_of[1] : st.n_of[0];
+            unsigned parity = (g == 0 ? c_p[0] : c_p[1]) & 1;
+            if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_half[0]);
+            ok = ok && wait_k();
+            if (ok) {
               tc_fence_after();
-              issue_o(g, 0, j == 0, v_lo(j));
-              ok = wait(&sh.p_full[g], parity);
+              if (mine > 0) issue_s(g, kc.slot);
+              commit(&sh.empty[kc.slot], leader);
+              if (nstep == 1) commit(&sh.q_empty, leader);
+            }
+            for (int j = 0; j < nstep && ok; ++j) {
+              const bool more = j + 1 < nstep;
+              ok = wait_v(j);
+              if (more) next_k(j);
+              if (!FP8 && more && ok) ok = wait_k();  // before the weights, where waiting costs nothing
               if (!ok) break;
-              parity ^= 1;
-              tc_fence_after();
-              issue_o(g, 1, false, v_lo(j));
-              if (FP8 && j + 1 < mine) {  // K may come later than the weights: V's expansion holds up the ring
-                ok = wait_k();
+              if (j < mine) {
+                if (g == 1 && j >= other && leader) mbar_arrive(&sh.p_half[1]);
+                ok = wait(&sh.p_half[g], parity);
                 if (!ok) break;
                 tc_fence_after();
+                issue_o(g, 0, j == 0, v_lo(j));
+                ok = wait(&sh.p_full[g], parity);
+                if (!ok) break;
+                parity ^= 1;
+                tc_fence_after();
+                issue_o(g, 1, false, v_lo(j));
+                if (FP8 && j + 1 < mine) {  // K may come later than the weights: V's expansion holds up the ring
+                  ok = wait_k();
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                if (j + 1 < mine) issue_s(g, kc.slot);
+                else commit(&sh.o_full[g], leader);
+                if ((g == 0 ? j < other : j + 1 < other) && leader) mbar_arrive(&sh.p_half[g ^ 1]);
+              } else if (g == 1 && mine == 0 && j < other) {
+                ok = wait(&sh.p_half[0], (c_p[0] + j) & 1);
+                if (!ok) break;
+                if (j + 1 < other && leader) mbar_arrive(&sh.p_half[0]);
               }
-              if (j + 1 < mine) issue_s(g, kc.slot);
-              else commit(&sh.o_full[g], leader);
-              if ((g == 0 ? j < other : j + 1 < other) && leader) mbar_arrive(&sh.p_half[g ^ 1]);
-            } else if (g == 1 && mine == 0 && j < other) {
-              ok = wait(&sh.p_half[0], (c_p[0] + j) & 1);
+              free_v(j);
+              next_v(j);
+              if (FP8 && more && j + 1 >= mine) ok = wait_k();
               if (!ok) break;
-              if (j + 1 < other && leader) mbar_arrive(&sh.p_half[0]);
+              if (more) commit(&sh.empty[kc.slot], leader);
+              if (j + 2 == nstep) commit(&sh.q_empty, leader);
             }
-            free_v(j);
-            next_v(j);
-            if (FP8 && more && j + 1 >= mine) ok = wait_k();
-            if (!ok) break;
-            if (more) commit(&sh.empty[kc.slot], leader);
-            if (j + 2 == nstep) commit(&sh.q_empty, leader);
-          }
-        } else {
-          for (int j = 0; j < min(2, nstep) && ok; ++j) {
-            if (j > 0) next_k(j - 1);
-            ok = wait_k();
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(j, kc.slot);
-            commit(&sh.empty[kc.slot], leader);
-            if (j + 1 == nstep) commit(&sh.q_empty, leader);
-          }
-          for (int j = 0; j < nstep && ok; ++j) {
-            const int g = j & 1, t = j >> 1;
-            const unsigned parity = ((g == 0 ? c_p[0] : c_p[1]) + t) & 1;
-            ok = wait(&sh.p_half[g], parity) && wait_v(j);
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(g, 0, t == 0, v_lo(j));
-            ok = wait(&sh.p_full[g], parity);
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(g, 1, false, v_lo(j));
-            free_v(j);
-            next_v(j);
-            if (j + 2 >= nstep) commit(&sh.o_full[g], leader);
-            if (j + 2 < nstep) {
-              next_k(j + 1);
+          } else {
+            for (int j = 0; j < min(2, nstep) && ok; ++j) {
+              if (j > 0) next_k(j - 1);
               ok = wait_k();
               if (!ok) break;
               tc_fence_after();
-              issue_s(g, kc.slot);
+              issue_s(j, kc.slot);
               commit(&sh.empty[kc.slot], leader);
-              if (j + 3 == nstep) commit(&sh.q_empty, leader);
+              if (j + 1 == nstep) commit(&sh.q_empty, leader);
+            }
+            for (int j = 0; j < nstep && ok; ++j) {
+              const int g = j & 1, t = j >> 1;
+              const unsigned parity = ((g == 0 ? c_p[0] : c_p[1]) + t) & 1;
+              ok = wait(&sh.p_half[g], parity) && wait_v(j);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(g, 0, t == 0, v_lo(j));
+              ok = wait(&sh.p_full[g], parity);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(g, 1, false, v_lo(j));
+              free_v(j);
+              next_v(j);
+              if (j + 2 >= nstep) commit(&sh.o_full[g], leader);
+              if (j + 2 < nstep) {
+                next_k(j + 1);
+                ok = wait_k();
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(g, kc.slot);
+                commit(&sh.empty[kc.slot], leader);
+                if (j + 3 == nstep) commit(&sh.q_empty, leader);
+              }
             }
           }
-        }
-        base.advance_by(2 * nstep);
-        steps_done += nstep;
-        cuts += nstep - st.first_cut;
-        c_p[0] += st.n_of[0];
-        c_p[1] += st.n_of[1];
-      }
-      if (!ok && !*abort && lane == 0) fail();
-      // nothing may run on the tensor cores when the CTA frees its tensor memory
-      commit(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], leader);
-      mbar_wait(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], 0);
-    }
-    __syncwarp();
-  } else if (warp == C::kProducerWarp) {
-    // ======================================================================== work and TMA producer
-    // lane b < 8 knows the pool row of block b of a step; the warp goes through the blocks as one
-    // and the elected lane issues each box (16 lanes issuing their own took 100 cycles a box)
-    const uint32_t leader = elect_one();
-    auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row) {
-      const unsigned st = __shfl_sync(kFull, item % NS, 0);
-      const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * C::kSlot;
-      if (leader) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
-      __syncwarp();
-#pragma unroll(FP8 ? 2 : C::kStepBlocks)
-      for (int blk = 0; blk < C::kStepBlocks; ++blk) {
-        const int r = __shfl_sync(kFull, row, blk);
-        if constexpr (FP8) {
-          tma_box(dst + blk * kBlockSize * D, tm, 0, head, r, bar, leader);
-        } else {
-#pragma unroll
-          for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_box(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, r, bar, leader);
-        }
-      }
-    };
-    auto slot_free = [&](unsigned item) {
-      const bool ok = item < NS || wait_for(&sh.empty[item % NS], ((item / NS) - 1) & 1, abort);
-      return __all_sync(kFull, ok);
-    };
-    // the tokens of the work at (x, y) of the grid: tile slots count the sequences' tiles in
-    // order, each sequence's longest (last) tile first.  seq < 0: a slot past the last tile
-    auto find = [&](unsigned x, unsigned y) {
-      Work w{0, 0, -1, 0, 0, static_cast<int>(x % p.hkv), static_cast<int>(y)};
-      const int slot = x / p.hkv;
-      int before = 0;
-      for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        int first = 0, n = 0, len = 0;
-        if (b < p.batch) {
-          first = p.q_indptr[b];
-          const int last = p.q_indptr[b + 1];
-          len = p.context_lens[b];
-          n = last - first;
-          if (first < 0 || last < first || last > p.total_q) {
-            set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
-            n = 0;
-          }
-        }
-        const int tiles = (n + cta_tok - 1) / cta_tok;
-        int upto = tiles;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const int v = __shfl_up_sync(kFull, upto, m);
-          if (lane >= m) upto += v;
-        }
-        const unsigned hit = __ballot_sync(kFull, slot < before + upto);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          const int tile = __shfl_sync(kFull, before + upto - 1 - slot, src);  // tiles after this one
-          first = __shfl_sync(kFull, first, src);
-          n = __shfl_sync(kFull, n, src);
-          w.seq = b0 + src;
-          int ctx = __shfl_sync(kFull, len, src);
-          const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
-          if (ctx < 0 || ctx > cap) {
-            set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
-            ctx = max(0, min(ctx, cap));
-          }
-          w.ctx = ctx;
-          w.tok0 = first + tile * cta_tok;
-          w.ntok = min(cta_tok, n - tile * cta_tok);
-          w.shift = ctx - n + tile * cta_tok;
-          break;
-        }
-        before += __shfl_sync(kFull, upto, 31);
-      }
-      return w;
-    };
-
-    unsigned n = 0, base = 0, steps_done = 0, cuts = 0, q_count = 0, asked = 0;
-    uint32_t gx = blockIdx.x, gy = blockIdx.y;
-    bool more = true, ok = true;
-    while (more && ok) {
-      const Work w = find(gx, gy);
-      if (lane == 0) clc_ask(&sh.clc_answer, &sh.clc);
-      if (w.seq >= 0) {
-        const Steps<WIDE> st(w, p, tile_tok);
-        const int nstep = st.nstep;
-        const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
-        const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
-        // id of this lane's block in step j, asked for two steps ahead of its use (the first ones before
-        // the work is passed on and Q asked for): INT_MIN for a block past the context; its pool
-        // row: a block past the context, or with an id outside the pool, becomes a box entirely
-        // outside the tensor, which reads zeros
-        auto id_of = [&](int j) {
-          const int at = (st.k0 + j) * C::kStepBlocks + lane;
-          return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldcg(table + at) : INT_MIN;
-        };
-        auto row_of = [&](int id) {
-          if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
-          if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
-          return -kBlockSize;
-        };
-        const int id0 = id_of(0), id1 = id_of(1);
-        int id2 = id_of(2), id3 = id_of(3);
-        ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
-        ok = __all_sync(kFull, ok);
-        if (ok) {
-          if (lane == 0) {
-            sh.work[n & 1][0] = make_int4(w.tok0, w.ntok, w.seq, w.ctx);
-            sh.work[n & 1][1] = make_int4(w.shift, w.h, w.split, 0);
-            mbar_arrive(&sh.work_full[n & 1]);
-          }
-          ++n;
-        }
-        if (ok && nstep > 0) {
-          if constexpr (!FP8) {
-            // Q's tiles are free once the last scores of the work before are done
-            if (q_count > 0) ok = wait_for(&sh.q_empty, (q_count - 1) & 1, abort);
-            ok = __all_sync(kFull, ok);
-            if (ok && leader) {
-              mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
-#pragma unroll
-              for (int t = 0; t < (WIDE ? 2 : 1); ++t)
-#pragma unroll
-                for (int c = 0; c < C::kHalves; ++c)
-                  tma_load_3d(smem + C::kOffQ + t * C::kQTile + c * C::kHalf16, &tm_q, c * 64, w.h * G,
-                              w.tok0 + t * tile_tok, &sh.q_full);
-            }
-          }
-          if (ok) ++q_count;
-          int cur = row_of(id0), nxt = row_of(id1);
-          // tiles in the ring's order: K of step 0, then K of step j + 1 and V of step j in turns
-          unsigned issued = base;
-          int j = 0;
-          bool is_v = false;
-#pragma unroll 1
-          for (int i = 0; i < 2 * nstep && ok; ++i) {
-            ok = slot_free(base + i);
-            if (!ok) break;
-            load(is_v ? &tm_v : &tm_k, base + i, w.h, i == 0 || is_v ? cur : nxt);
-            issued = base + i + 1;
-            if (is_v) {
-              if (lane == 0 && (FP8 || j >= st.first_cut))
-                mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
-              cur = nxt;
-              nxt = row_of(id2);
-              id2 = id3;
-              id3 = id_of(j + 4);
-              ++j;
-              is_v = j + 1 >= nstep;
-            } else {
-              is_v = i > 0 || nstep == 1;
-            }
-          }
-          base = ok ? base + 2 * nstep : issued;
+          base.advance_by(2 * nstep);
           steps_done += nstep;
           cuts += nstep - st.first_cut;
+          c_p[0] += st.n_of[0];
+          c_p[1] += st.n_of[1];
         }
+        if (!ok && !*abort && lane == 0) fail();
+        // nothing may run on the tensor cores when the CTA frees its tensor memory
+        commit(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], leader);
+        mbar_wait(&sh.drain[warp == C::kIssuerWarp ? 0 : 1], 0);
       }
-      // the next work: the answer is always taken, so that none is in flight at the end
-      const bool told = mbar_wait(&sh.clc, asked & 1);
-      ++asked;
-      ok = __all_sync(kFull, told) && ok;
-      more = told && clc_read(&sh.clc_answer, gx, gy);
-      fence_proxy_async_smem();  // read before the next answer is written
       __syncwarp();
-    }
-    // no work left: tell the other roles
-    if (ok) {
-      ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
-      if (ok && lane == 0) {
-        sh.work[n & 1][0] = make_int4(0, 0, -1, 0);
-        sh.work[n & 1][1] = make_int4(0, 0, 0, 0);
-        mbar_arrive(&sh.work_full[n & 1]);
-      }
-    }
-    if (lane == 0) {
-      if (!ok && !*abort) fail();
-      // nothing may be in flight when the CTA exits: the last tiles issued have landed
-      for (unsigned i = base > NS ? base - NS : 0; i < base; ++i)
-        if (!mbar_wait(&sh.full[i % NS], (i / NS) & 1)) break;
-      if (!FP8 && q_count > 0) mbar_wait(&sh.q_full, (q_count - 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp >= C::kFixWarp0) {
-    // ======================================================================== V: cut tiles, expansion
-    constexpr int kFix = C::kFixWarps * 32;
-    const int ft = threadIdx.x - C::kFixWarp0 * 32;
-    unsigned number = 0;
-    auto note = [&](int kind, int dim, int key) {
-      atomicMin(&poison[kind * D + dim], key);
-      *poisoned = static_cast<int>(number) + 1;
-    };
-    constexpr int kChunks = D / 8;  // 8-element pieces of a row
-    constexpr int kStep = kFix / kChunks;
-    const int c = ft % kChunks, r0 = ft / kChunks;
-    unsigned base = 0, steps_done = 0, cuts = 0, with_steps = 0;
-    bool ok = true;
-    Work w;
-    for (unsigned n = 0; ok; ++n) {
-      // the warps leave together
-      if (named_sync_or(1, kFix, !next_work(n, w))) break;
-      number = n;
-      const Steps<WIDE> st(w, p, tile_tok);
-      const int nstep = st.nstep;
-      if (nstep == 0) continue;
-      // before values that are not finite are listed: the works before are through their epilogues,
-      // and what they left in the list is cleared
-      bool cleared = false;
-      auto clear = [&]() {
-        cleared = true;
-        const volatile int* through = &sh.epilogues;
-        const long long start = clock64();
-        while (ok && *through < static_cast<int>(8 * with_steps)) {
-          if (*abort) ok = false;
-          if (clock64() - start > kWaitLimitCycles) {
-            ok = false;
-            fail();
+    } else if (warp == C::kProducerWarp) {
+      // ======================================================================== work and TMA producer
+      // lane b < 8 knows the pool row of block b of a step; the warp goes through the blocks as one
+      // and the elected lane issues each box (16 lanes issuing their own took 100 cycles a box)
+      const uint32_t leader = elect_one();
+      auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row) {
+        const unsigned st = __shfl_sync(kFull, item % NS, 0);
+        const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * C::kSlot;
+        if (leader) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
+        __syncwarp();
+#pragma unroll(FP8 ? 2 : C::kStepBlocks)
+        for (int blk = 0; blk < C::kStepBlocks; ++blk) {
+          const int r = __shfl_sync(kFull, row, blk);
+          if constexpr (FP8) {
+            tma_box(dst + blk * kBlockSize * D, tm, 0, head, r, bar, leader);
+          } else {
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_box(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, r, bar, leader);
           }
         }
-        named_sync(3, kFix);
-        for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
-        named_sync(3, kFix);
       };
-      for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
-        const bool cut = j >= st.first_cut;
-        const unsigned item = base + st.v_item(j);
-        // the parity of `full` means this load only once it is issued (the slot's loads before it
-        // are not waited for here); v_sent itself is never a phase ahead: eight V tiles on, the
-        // ring has come round
-        const unsigned sent = FP8 ? steps_done + j : cuts + j - st.first_cut;
-        if (ok) ok = wait_for(&sh.v_sent[sent & 7], (sent >> 3) & 1, abort);
-        if (ok) ok = wait_for(&sh.full[item % NS], (item / NS) & 1, abort);
-        if constexpr (FP8)
-          if (ok && sent >= 2) ok = wait_for(&sh.exp_free[sent & 1], ((sent >> 1) - 1) & 1, abort);
-        if (!ok && !*abort) fail();
-        const int key0 = (st.k0 + j) * C::kKeys;
-        // rows below seen: every row's; from end on: no row's
-        const int seen = st.lim_min - key0, end = w.ctx - key0;
-        uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
-        // E4M3: expand the tile, four pieces in registers at a time (one by one, a load and a store
-        // each, a tile took 2600 cycles and the step waited for it); rows no row sees become zeros.
-        // bf16: only the rows that not every row sees, four pieces at a time.  True if one of those
-        // that some row sees is not finite.
-        auto odd8 = [](uint32_t x) { return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u; };    // E4M3 NaN
-        auto odd16 = [](uint32_t x) { return (((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u; };   // bf16
-        const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
-        auto at16 = [&](int row) {
-          return reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-        };
-        auto expand = [&](int row, uint2 v) {
-          st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
-                       e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
-        };
-        bool odd = false;
-        if (ok) {
-          if constexpr (FP8) {
-            constexpr int kBatch = 4;
-            static_assert(C::kKeys % (kBatch * kStep) == 0, "whole batches");
-#pragma unroll 1
-            for (int b0 = r0; b0 < C::kKeys; b0 += kBatch * kStep) {
-              uint2 v[kBatch];
+      auto slot_free = [&](unsigned item) {
+        const bool ok = item < NS || wait_for(&sh.empty[item % NS], ((item / NS) - 1) & 1, abort);
+        return __all_sync(kFull, ok);
+      };
+      // the tokens of the work at (x, y) of the grid: tile slots count the sequences' tiles in
+      // order, each sequence's longest (last) tile first.  seq < 0: a slot past the last tile
+      auto find = [&](unsigned x, unsigned y) {
+        Work w{0, 0, -1, 0, 0, static_cast<int>(x % p.hkv), static_cast<int>(y)};
+        const int slot = x / p.hkv;
+        int before = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const int b = b0 + lane;
+          int first = 0, n = 0, len = 0;
+          if (b < p.batch) {
+            first = p.q_indptr[b];
+            const int last = p.q_indptr[b + 1];
+            len = p.context_lens[b];
+            n = last - first;
+            if (first < 0 || last < first || last > p.total_q) {
+              set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
+              n = 0;
+            }
+          }
+          const int tiles = (n + cta_tok - 1) / cta_tok;
+          int upto = tiles;
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i)
-                v[i] = *reinterpret_cast<const uint2*>(src + (b0 + i * kStep) * D + c * 8);
-              if (cut) {
+          for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(kFull, upto, m);
+            if (lane >= m) upto += v;
+          }
+          const unsigned hit = __ballot_sync(kFull, slot < before + upto);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int tile = __shfl_sync(kFull, before + upto - 1 - slot, src);  // tiles after this one
+            first = __shfl_sync(kFull, first, src);
+            n = __shfl_sync(kFull, n, src);
+            w.seq = b0 + src;
+            int ctx = __shfl_sync(kFull, len, src);
+            const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
+            if (ctx < 0 || ctx > cap) {
+              set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
+              ctx = max(0, min(ctx, cap));
+            }
+            w.ctx = ctx;
+            w.tok0 = first + tile * cta_tok;
+            w.ntok = min(cta_tok, n - tile * cta_tok);
+            w.shift = ctx - n + tile * cta_tok;
+            break;
+          }
+          before += __shfl_sync(kFull, upto, 31);
+        }
+        return w;
+      };
+
+      unsigned n = 0, base = 0, steps_done = 0, cuts = 0, q_count = 0, asked = 0;
+      uint32_t gx = blockIdx.x, gy = blockIdx.y;
+      bool more = true, ok = true;
+      while (more && ok) {
+        const Work w = find(gx, gy);
+        if (lane == 0) clc_ask(&sh.clc_answer, &sh.clc);
+        if (w.seq >= 0) {
+          const Steps<WIDE> st(w, p, tile_tok);
+          const int nstep = st.nstep;
+          const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
+          const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
+          // id of this lane's block in step j, asked for two steps ahead of its use (the first ones before
+          // the work is passed on and Q asked for): INT_MIN for a block past the context; its pool
+          // row: a block past the context, or with an id outside the pool, becomes a box entirely
+          // outside the tensor, which reads zeros
+          auto id_of = [&](int j) {
+            const int at = (st.k0 + j) * C::kStepBlocks + lane;
+            return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldcg(table + at) : INT_MIN;
+          };
+          auto row_of = [&](int id) {
+            if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
+            if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
+            return -kBlockSize;
+          };
+          const int id0 = id_of(0), id1 = id_of(1);
+          int id2 = id_of(2), id3 = id_of(3);
+          ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+          ok = __all_sync(kFull, ok);
+          if (ok) {
+            if (lane == 0) {
+              sh.work[n & 1][0] = make_int4(w.tok0, w.ntok, w.seq, w.ctx);
+              sh.work[n & 1][1] = make_int4(w.shift, w.h, w.split, 0);
+              mbar_arrive(&sh.work_full[n & 1]);
+            }
+            ++n;
+          }
+          if (ok && nstep > 0) {
+            if constexpr (!FP8) {
+              // Q's tiles are free once the last scores of the work before are done
+              if (q_count > 0) ok = wait_for(&sh.q_empty, (q_count - 1) & 1, abort);
+              ok = __all_sync(kFull, ok);
+              if (ok && leader) {
+                mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
+#pragma unroll
+                for (int t = 0; t < (WIDE ? 2 : 1); ++t)
+#pragma unroll
+                  for (int c = 0; c < C::kHalves; ++c)
+                    tma_load_3d(smem + C::kOffQ + t * C::kQTile + c * C::kHalf16, &tm_q, c * 64, w.h * G,
+                                w.tok0 + t * tile_tok, &sh.q_full);
+              }
+            }
+            if (ok) ++q_count;
+            int cur = row_of(id0), nxt = row_of(id1);
+            // tiles in the ring's order: K of step 0, then K of step j + 1 and V of step j in turns
+            unsigned issued = base;
+            int j = 0;
+            bool is_v = false;
+#pragma unroll 1
+            for (int i = 0; i < 2 * nstep && ok; ++i) {
+              ok = slot_free(base + i);
+              if (!ok) break;
+              load(is_v ? &tm_v : &tm_k, base + i, w.h, i == 0 || is_v ? cur : nxt);
+              issued = base + i + 1;
+              if (is_v) {
+                if (lane == 0 && (FP8 || j >= st.first_cut))
+                  mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
+                cur = nxt;
+                nxt = row_of(id2);
+                id2 = id3;
+                id3 = id_of(j + 4);
+                ++j;
+                is_v = j + 1 >= nstep;
+              } else {
+                is_v = i > 0 || nstep == 1;
+              }
+            }
+            base = ok ? base + 2 * nstep : issued;
+            steps_done += nstep;
+            cuts += nstep - st.first_cut;
+          }
+        }
+        // the next work: the answer is always taken, so that none is in flight at the end
+        const bool told = mbar_wait(&sh.clc, asked & 1);
+        ++asked;
+        ok = __all_sync(kFull, told) && ok;
+        more = told && clc_read(&sh.clc_answer, gx, gy);
+        fence_proxy_async_smem();  // read before the next answer is written
+        __syncwarp();
+      }
+      // no work left: tell the other roles
+      if (ok) {
+        ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
+        if (ok && lane == 0) {
+          sh.work[n & 1][0] = make_int4(0, 0, -1, 0);
+          sh.work[n & 1][1] = make_int4(0, 0, 0, 0);
+          mbar_arrive(&sh.work_full[n & 1]);
+        }
+      }
+      if (lane == 0) {
+        if (!ok && !*abort) fail();
+        // nothing may be in flight when the CTA exits: the last tiles issued have landed
+        for (unsigned i = base > NS ? base - NS : 0; i < base; ++i)
+          if (!mbar_wait(&sh.full[i % NS], (i / NS) & 1)) break;
+        if (!FP8 && q_count > 0) mbar_wait(&sh.q_full, (q_count - 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp >= C::kFixWarp0) {
+      // ======================================================================== V: cut tiles, expansion
+      constexpr int kFix = C::kFixWarps * 32;
+      const int ft = threadIdx.x - C::kFixWarp0 * 32;
+      unsigned number = 0;
+      auto note = [&](int kind, int dim, int key) {
+        atomicMin(&poison[kind * D + dim], key);
+        *poisoned = static_cast<int>(number) + 1;
+      };
+      constexpr int kChunks = D / 8;  // 8-element pieces of a row
+      constexpr int kStep = kFix / kChunks;
+      const int c = ft % kChunks, r0 = ft / kChunks;
+      unsigned base = 0, steps_done = 0, cuts = 0, with_steps = 0;
+      bool ok = true;
+      Work w;
+      for (unsigned n = 0; ok; ++n) {
+        // the warps leave together
+        if (named_sync_or(1, kFix, !next_work(n, w))) break;
+        number = n;
+        const Steps<WIDE> st(w, p, tile_tok);
+        const int nstep = st.nstep;
+        if (nstep == 0) continue;
+        // before values that are not finite are listed: the works before are through their epilogues,
+        // and what they left in the list is cleared
+        bool cleared = false;
+        auto clear = [&]() {
+          cleared = true;
+          const volatile int* through = &sh.epilogues;
+          const long long start = clock64();
+          while (ok && *through < static_cast<int>(8 * with_steps)) {
+            if (*abort) ok = false;
+            if (clock64() - start > kWaitLimitCycles) {
+              ok = false;
+              fail();
+            }
+          }
+          named_sync(3, kFix);
+          for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
+          named_sync(3, kFix);
+        };
+        for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
+          const bool cut = j >= st.first_cut;
+          const unsigned item = base + st.v_item(j);
+          // the parity of `full` means this load only once it is issued (the slot's loads before it
+          // are not waited for here); v_sent itself is never a phase ahead: eight V tiles on, the
+          // ring has come round
+          const unsigned sent = FP8 ? steps_done + j : cuts + j - st.first_cut;
+          if (ok) ok = wait_for(&sh.v_sent[sent & 7], (sent >> 3) & 1, abort);
+          if (ok) ok = wait_for(&sh.full[item % NS], (item / NS) & 1, abort);
+          if constexpr (FP8)
+            if (ok && sent >= 2) ok = wait_for(&sh.exp_free[sent & 1], ((sent >> 1) - 1) & 1, abort);
+          if (!ok && !*abort) fail();
+          const int key0 = (st.k0 + j) * C::kKeys;
+          // rows below seen: every row's; from end on: no row's
+          const int seen = st.lim_min - key0, end = w.ctx - key0;
+          uint8_t* src = smem + C::kOffRing + (item % NS) * C::kSlot;
+          // E4M3: expand the tile, four pieces in registers at a time (one by one, a load and a store
+          // each, a tile took 2600 cycles and the step waited for it); rows no row sees become zeros.
+          // bf16: only the rows that not every row sees, four pieces at a time.  True if one of those
+          // that some row sees is not finite.
+          auto odd8 = [](uint32_t x) { return (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u; };    // E4M3 NaN
+          auto odd16 = [](uint32_t x) { return (((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u; };   // bf16
+          const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
+          auto at16 = [&](int row) {
+            return reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+          };
+          auto expand = [&](int row, uint2 v) {
+            st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
+                         e4m3_hi(v.x), e4m3_lo(v.y), e4m3_hi(v.y));
+          };
+          bool odd = false;
+          if (ok) {
+            if constexpr (FP8) {
+              constexpr int kBatch = 4;
+              static_assert(C::kKeys % (kBatch * kStep) == 0, "whole batches");
+#pragma unroll 1
+              for (int b0 = r0; b0 < C::kKeys; b0 += kBatch * kStep) {
+                uint2 v[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                  v[i] = *reinterpret_cast<const uint2*>(src + (b0 + i * kStep) * D + c * 8);
+                if (cut) {
+#pragma unroll
+                  for (int i = 0; i < kBatch; ++i) {
+                    const int row = b0 + i * kStep;
+                    if (row >= end) v[i] = make_uint2(0u, 0u);
+                    else if (row >= seen) odd |= odd8(v[i].x) || odd8(v[i].y);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) expand(b0 + i * kStep, v[i]);
+              }
+            } else {
+              constexpr int kBatch = 4;
+#pragma unroll 1
+              for (int b0 = max(0, seen) + r0; b0 < min(end, C::kKeys); b0 += kBatch * kStep) {
+                uint4 v[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                   const int row = b0 + i * kStep;
-                  if (row >= end) v[i] = make_uint2(0u, 0u);
-                  else if (row >= seen) odd |= odd8(v[i].x) || odd8(v[i].y);
+                  v[i] = row < min(end, C::kKeys) ? *at16(row) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                  odd |= odd16(v[i].x) || odd16(v[i].y) || odd16(v[i].z) || odd16(v[i].w);
                 }
               }
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) expand(b0 + i * kStep, v[i]);
+              for (int row = max(0, end) + r0; row < C::kKeys; row += kStep) *at16(row) = make_uint4(0u, 0u, 0u, 0u);
             }
-          } else {
-            constexpr int kBatch = 4;
-#pragma unroll 1
-            for (int b0 = max(0, seen) + r0; b0 < min(end, C::kKeys); b0 += kBatch * kStep) {
-              uint4 v[kBatch];
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int row = b0 + i * kStep;
-                v[i] = row < min(end, C::kKeys) ? *at16(row) : make_uint4(0u, 0u, 0u, 0u);
-              }
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) odd |= odd16(v[i].x) || odd16(v[i].y) || odd16(v[i].z) || odd16(v[i].w);
-            }
-            for (int row = max(0, end) + r0; row < C::kKeys; row += kStep) *at16(row) = make_uint4(0u, 0u, 0u, 0u);
           }
-        }
-        if (cut && named_sync_or(3, kFix, odd)) {  // rare: list them and take them out of the tile
-          if (!cleared) clear();
-          for (int row = max(0, seen) + r0; ok && row < min(end, C::kKeys); row += kStep) {
+          if (cut && named_sync_or(3, kFix, odd)) {  // rare: list them and take them out of the tile
+            if (!cleared) clear();
+            for (int row = max(0, seen) + r0; ok && row < min(end, C::kKeys); row += kStep) {
+              if constexpr (FP8) {
+                uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
+                if (!odd8(v.x) && !odd8(v.y)) continue;
+                uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+                for (int e = 0; e < 8; ++e)
+                  if (((word[e >> 2] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {  // the only code that is not finite
+                    note(0, c * 8 + e, key0 + row);
+                    word[e >> 2] &= ~(0xffu << (8 * (e & 3)));
+                  }
+                expand(row, v);
+              } else {
+                uint4 v = *at16(row);
+                uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t x = (word[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                  if ((x & 0x7f80u) == 0x7f80u) {
+                    note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + e, key0 + row);
+                    word[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                  }
+                }
+                *at16(row) = v;
+              }
+            }
+          }
+          fence_proxy_async_smem();  // the tile is read by the tensor cores
+          if (named_sync_or(1, kFix, *abort != 0)) {
+            ok = false;
+            break;
+          }
+          if (ft == 0) {
             if constexpr (FP8) {
-              uint2 v = *reinterpret_cast<const uint2*>(src + row * D + c * 8);
-              if (!odd8(v.x) && !odd8(v.y)) continue;
-              uint32_t* word = reinterpret_cast<uint32_t*>(&v);
-              for (int e = 0; e < 8; ++e)
-                if (((word[e >> 2] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {  // the only code that is not finite
-                  note(0, c * 8 + e, key0 + row);
-                  word[e >> 2] &= ~(0xffu << (8 * (e & 3)));
-                }
-              expand(row, v);
+              mbar_arrive_n(&sh.empty[item % NS], kIssuers);  // what both issuers would arrive
+              mbar_arrive(&sh.fixed[sent & 1]);
             } else {
-              uint4 v = *at16(row);
-              uint32_t* word = reinterpret_cast<uint32_t*>(&v);
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t x = (word[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                if ((x & 0x7f80u) == 0x7f80u) {
-                  note((x & 0x7fu) ? 0 : (x & 0x8000u) ? 2 : 1, c * 8 + e, key0 + row);
-                  word[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
-                }
-              }
-              *at16(row) = v;
+              mbar_arrive(&sh.fixed[sent & 7]);
             }
           }
         }
-        fence_proxy_async_smem();  // the tile is read by the tensor cores
-        if (named_sync_or(1, kFix, *abort != 0)) {
-          ok = false;
-          break;
-        }
-        if (ft == 0) {
-          if constexpr (FP8) {
-            mbar_arrive_n(&sh.empty[item % NS], kIssuers);  // what both issuers would arrive
-            mbar_arrive(&sh.fixed[sent & 1]);
-          } else {
-            mbar_arrive(&sh.fixed[sent & 7]);
-          }
-        }
+        ++with_steps;
+        base += 2 * nstep;
+        steps_done += nstep;
+        cuts += nstep - st.first_cut;
       }
-      ++with_steps;
-      base += 2 * nstep;
-      steps_done += nstep;
-      cuts += nstep - st.first_cut;
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ======================================================================== softmax
@@ -1066,7 +1105,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           if (lane == 0) mbar_arrive(&sh.q_full);
           // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
           // (a zero scale: a factor that leaves every score at 0 while masked ones stay -inf)
-          sscale = odd || k_scale != k_scale ? __int_as_float(0x7fffffff) : fmaxf(sscale * fabsf(k_scale) / size, 1e-37f);
+          sscale = odd || k_scale != k_scale ? __int_as_float(0x7fffffff)
+                                             : fmaxf(sscale * fabsf(k_scale) / size, 1e-37f);
         }
         if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
           if (g == 0) join_scale[r] = sscale;

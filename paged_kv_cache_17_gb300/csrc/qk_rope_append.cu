@@ -169,7 +169,8 @@ __device__ __forceinline__ void row_pieces(const RopeAppendParams& p, uint4 r0, 
 }
 
 template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads) qk_rope_append_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads)
+    qk_rope_append_kernel(const RopeAppendParams p) {
   constexpr int S = D / 16;  // threads per row
   // two tables, of this round and the next.  Half layout: [token][cos of every pair, then sin];
   // interleaved: [token][pair] (cos, sin)
