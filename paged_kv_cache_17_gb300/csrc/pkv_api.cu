@@ -970,7 +970,7 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
       const int run = (steps + n - 1) / n;
       if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
       if (n > least && rows * n > kPrefillMaxRecords) break;
-      const double one = run * kPrefillStepUs[pp.wide];
+      const double one = (pp.wide ? run : std::max(run, 2)) * kPrefillStepUs[pp.wide];  // narrow: two at once
       const double share = static_cast<double>(tiles * hkv * n) / sm_count;
       double us = std::max(one + kPrefillWorkUs, share * (one + kPrefillWorkUs) + one / 2);
       if (n > 1) us += kPrefillMergeUs + 2.0 * static_cast<double>(rows) * n * (d + 2) * 4 / kPrefillRecordBytesPerUs;
@@ -1005,6 +1005,21 @@ pkv_status check_prefill_sizes(int32_t batch, int32_t total_q, int32_t hq, int32
       static_cast<long long>(total_q) * hq > 8LL * 0x7fffffff)
     return fail(PKV_ERR_UNSUPPORTED, "too many query tokens (%d) for %d heads", total_q, hq);
   return PKV_OK;
+}
+
+// The bf16 pool with a block's rows of one head as one box, laid out for the tensor cores: two groups of
+// eight rows, each with its 64-column halves side by side, 128-byte swizzled.  (A box per half, the
+// largest a 3-D view allows, takes the loading warp twice as many instructions.)
+bool encode_kv_map_groups(CUtensorMap* tm, void* base, int64_t num_blocks, int hkv, int d) {
+  const cuuint64_t row = static_cast<cuuint64_t>(hkv) * d * 2, halves = static_cast<cuuint64_t>(d / 64);
+  const cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(num_blocks) * 2, static_cast<cuuint64_t>(hkv)};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(d) * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(halves), 2, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 // q [total_q][hq][D] as boxes of one tile: 64 columns x the G heads of a group x 128 / G tokens
@@ -1081,15 +1096,15 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
     if (workspace_bytes < pp.ws_bytes)
       return fail(PKV_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", workspace_bytes, pp.ws_bytes);
   }
-  // bf16: 64-column boxes for K and V; E4M3: K rows swizzled for the tensor cores, V rows as they
+  // bf16: a box per block of K and V; E4M3: K rows swizzled for the tensor cores, V rows as they
   // are (its expansion reads them)
   CUtensorMap tq{}, tk, tv;
   const int64_t nb = cache->num_blocks;
   const bool maps_ok = fp8 ? encode_kv_map_e4m3_swz(&tk, cache->k_cache, nb, hkv, d) &&
                                  encode_kv_map(&tv, cache->v_cache, nb, hkv, d, true)
                            : encode_q_map(&tq, q, q_stride, total_q, num_q_heads, g, d) &&
-                                 encode_kv_map_sw128(&tk, cache->k_cache, nb, hkv, d) &&
-                                 encode_kv_map_sw128(&tv, cache->v_cache, nb, hkv, d);
+                                 encode_kv_map_groups(&tk, cache->k_cache, nb, hkv, d) &&
+                                 encode_kv_map_groups(&tv, cache->v_cache, nb, hkv, d);
   if (!maps_ok) return fail(PKV_ERR_INVALID_ARG, "cannot describe q or the KV pool as a TMA tensor map");
 
   pkv::PrefillParams p{};

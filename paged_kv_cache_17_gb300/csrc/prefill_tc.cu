@@ -25,8 +25,7 @@
 //   warps 0-3, 4-7  softmax groups 0 and 1: thread r owns row r (TMEM lane r): scores in, weights
 //                   out over them as 16-bit pairs, rare rescale of the output, epilogue
 //   warps 8, 10     issue the MMAs, a warp per tile (narrow: warp 8 for both groups)
-//   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block (and
-//                   64-column half) at a time
+//   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block at a time
 //   warps 12-15     V: zero the rows past the context in the last tile, so that what a page holds
 //                   there (NaN included) meets weight 0 as 0; E4M3: expand V to fp16
 // A value of V that is not finite at a position some rows see and others do not would reach
@@ -49,8 +48,8 @@
 // row, 16 softmax warps, slow the other roles down more than they gain (1.46 ms).  Prompts of 257 to
 // 2048 tokens: 118 us, 59 % of the rate: a work is a handful of steps there, and its start, masked
 // steps and epilogue weigh beside them.  24 x 3 to 8 tokens over 1800 to 12,000 (narrow, split in
-// 3): 117 us = 5.3 TB/s of K and V, 78 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
-// 3000 to 9000, 64 + 8 heads: 0.52 ms = 1.39 PFLOP/s; V's expansion takes shared-memory
+// 3): 114 us = 5.4 TB/s of K and V, 80 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
+// 3000 to 9000, 64 + 8 heads: 0.505 ms = 1.43 PFLOP/s; V's expansion takes shared-memory
 // bandwidth and issue slots from the products and the softmax.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -74,6 +73,9 @@ struct PrefillCfg {
   static constexpr int kHalf16 = 128 * 128;         // 64 columns of 128 16-bit rows
   static constexpr int kTile16 = kHalves * kHalf16;  // a 16-bit tile of 128 rows
   static constexpr int kCodes = 128 * D;             // an E4M3 tile of 128 rows
+  // bf16 K and V tiles: groups of eight keys, each group's 64-column halves side by side, so that one
+  // TMA box brings a block of the pool
+  static constexpr int kGroup = kHalves * 1024;
   static constexpr int kQTile = FP8 ? 2 * kCodes : kTile16;
   static constexpr int kSlot = FP8 ? kCodes : kTile16;  // a K or V tile as loaded
   static constexpr int kSlots = D == 128 ? (FP8 ? 6 : 5) : 8;
@@ -132,7 +134,9 @@ namespace {
 // that they stay in uniform registers, and only the MMA itself is left to the elected lane: issued
 // from a branch of one lane, each MMA took 70 cycles of moves between register files, more than it
 // executes (64), and the step 4170 cycles for 2050 of products.
-constexpr uint32_t kDescK128 = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, 128-byte swizzle
+template <uint32_t kStride>
+constexpr uint32_t kDesc128 = (kStride >> 4) | (1u << 14) | (2u << 29);  // groups of eight rows apart, 128-byte swizzle
+constexpr uint32_t kDescK128 = kDesc128<1024>;
 constexpr uint32_t kDescK64 = (512u >> 4) | (1u << 14) | (4u << 29);    // stride 512, 64-byte swizzle
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
   return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
@@ -142,23 +146,23 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
 // descriptor); D[tmem] (+)= A[tmem] B[smem], 16-bit operands.  Called by the whole warp; the lane
 // with leader != 0 issues.
 template <bool F8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
-                                       bool accumulate, uint32_t leader) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi,
+                                       uint32_t idesc, bool accumulate, uint32_t leader) {
   if constexpr (F8)
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
         : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader)
         : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
@@ -311,6 +315,17 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int
       "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(leader)
+      : "memory");
+}
+
+// One block's rows of a head, as two groups of eight rows x the 64-column halves
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap* tm, int head, int group, uint32_t bar,
+                                          uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%6, %6, %6, %2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(group), "r"(head), "r"(bar), "r"(leader), "r"(0)
       : "memory");
 }
 
@@ -502,7 +517,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
                                    : idesc_f16(C::kRows, C::kKeys, true, false)) |
                               (p.negate ? 1u << 13 : 0u);
         const uint32_t tm = same(tmem);
-        const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, C::kHalf16));
+        const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, 1024));
         const uint32_t exp_v_lo = same(desc_lo(smem_u32(smem + C::kOffExp), C::kHalf16));
         const uint32_t q0_lo = same(desc_lo(q_base, 16));
         auto issue_s = [&](int g, unsigned slot) {
@@ -515,13 +530,14 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, hi, id_s, part > 0 || kk > 0,
-                             leader);
+                mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, hi, hi, id_s,
+                             part > 0 || kk > 0, leader);
           } else {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = ((kk >> 2) * C::kHalf16 + (kk & 3) * 32) / 16;
-              mma_ss<false>(d, q_lo + at, k_lo + at, kDescK128, id_s, kk > 0, leader);
+              mma_ss<false>(d, q_lo + ((kk >> 2) * C::kHalf16 + (kk & 3) * 32) / 16,
+                            k_lo + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, kDescK128, kDesc128<C::kGroup>, id_s, kk > 0,
+                            leader);
             }
           }
           commit(&sh.s_full[g], leader);
@@ -530,9 +546,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         auto issue_o = [&](int g, int half, bool first, uint32_t v_lo0) {
           const uint32_t pt = tm + C::kColS + 128 * g;
           const uint32_t v_lo = same(v_lo0);
+          constexpr uint32_t kVGroup = FP8 ? 1024 : C::kGroup;  // eight keys
 #pragma unroll
           for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * 128, kDescK128, kIdO, !first || kk > 0, leader);
+            mma_ts(tm + C::kColO + D * g, pt + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO,
+                   !first || kk > 0, leader);
         };
 
         Cursor<C::kSlots> base{0, 0};  // ring position of the work's first tile
@@ -675,23 +693,21 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       __syncwarp();
     } else if (warp == C::kProducerWarp) {
       // ======================================================================== work and TMA producer
-      // lane b < 8 knows the pool row of block b of a step; the warp goes through the blocks as one
+      // the lanes know the pool rows of the blocks of four steps; the warp goes through the blocks as one
       // and the elected lane issues each box (16 lanes issuing their own took 100 cycles a box)
       const uint32_t leader = elect_one();
-      auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row) {
+      auto load = [&](const CUtensorMap* tm, unsigned item, int head, int row, int from) {
         const unsigned st = __shfl_sync(kFull, item % NS, 0);
         const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * C::kSlot;
         if (leader) mbar_arrive_expect_tx(&sh.full[st], C::kSlot);
         __syncwarp();
 #pragma unroll(FP8 ? 2 : C::kStepBlocks)
         for (int blk = 0; blk < C::kStepBlocks; ++blk) {
-          const int r = __shfl_sync(kFull, row, blk);
+          const int r = __shfl_sync(kFull, row, from + blk);
           if constexpr (FP8) {
             tma_box(dst + blk * kBlockSize * D, tm, 0, head, r, bar, leader);
           } else {
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_box(dst + hf * C::kHalf16 + blk * 2048, tm, hf * 64, head, r, bar, leader);
+            tma_block(dst + blk * 2 * C::kGroup, tm, head, r >> 3, bar, leader);
           }
         }
       };
@@ -760,21 +776,22 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           const int nstep = st.nstep;
           const int32_t* table = p.block_tables + static_cast<int64_t>(w.seq) * p.max_blocks;
           const int nblk = (w.ctx + kBlockSize - 1) / kBlockSize;
-          // id of this lane's block in step j, asked for two steps ahead of its use (the first ones before
-          // the work is passed on and Q asked for): INT_MIN for a block past the context; its pool
-          // row: a block past the context, or with an id outside the pool, becomes a box entirely
-          // outside the tensor, which reads zeros
-          auto id_of = [&](int j) {
+          // ids of the blocks of four steps, one a lane, asked for four steps ahead of their use (the first
+          // ones before the work is passed on and Q asked for; a step at a time and two ahead, they
+          // were late when the tables come from HBM: 117 against 114 us for the narrow case above, 521
+          // against 505 for the E4M3 one): INT_MIN for a block past the context; the pool row: a block past the context, or with an id outside
+          // the pool, becomes a box entirely outside the tensor, which reads zeros
+          auto ids_of = [&](int j) {
             const int at = (st.k0 + j) * C::kStepBlocks + lane;
-            return lane < C::kStepBlocks && j < nstep && at < nblk ? __ldcg(table + at) : INT_MIN;
+            return j + lane / C::kStepBlocks < nstep && at < nblk ? __ldcg(table + at) : INT_MIN;
           };
           auto row_of = [&](int id) {
             if (id >= 0 && id < p.num_blocks) return id * kBlockSize;
             if (id != INT_MIN) set_flag(p.status, PKV_DEVFLAG_BAD_BLOCK_ID);
             return -kBlockSize;
           };
-          const int id0 = id_of(0), id1 = id_of(1);
-          int id2 = id_of(2), id3 = id_of(3);
+          const int ids0 = ids_of(0);
+          int ids1 = ids_of(4);
           ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
           ok = __all_sync(kFull, ok);
           if (ok) {
@@ -801,7 +818,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               }
             }
             if (ok) ++q_count;
-            int cur = row_of(id0), nxt = row_of(id1);
+            int rows_k = row_of(ids0), rows_v = rows_k;
             // tiles in the ring's order: K of step 0, then K of step j + 1 and V of step j in turns
             unsigned issued = base;
             int j = 0;
@@ -810,15 +827,17 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             for (int i = 0; i < 2 * nstep && ok; ++i) {
               ok = slot_free(base + i);
               if (!ok) break;
-              load(is_v ? &tm_v : &tm_k, base + i, w.h, i == 0 || is_v ? cur : nxt);
+              const int step = is_v || i == 0 ? j : j + 1;
+              if (!is_v && i > 0 && (step & 3) == 0) {
+                rows_k = row_of(ids1);
+                ids1 = ids_of(step + 4);
+              }
+              if (is_v && (step & 3) == 0) rows_v = rows_k;
+              load(is_v ? &tm_v : &tm_k, base + i, w.h, is_v ? rows_v : rows_k, (step & 3) * C::kStepBlocks);
               issued = base + i + 1;
               if (is_v) {
                 if (lane == 0 && (FP8 || j >= st.first_cut))
                   mbar_arrive(&sh.v_sent[(FP8 ? steps_done + j : cuts + j - st.first_cut) & 7]);
-                cur = nxt;
-                nxt = row_of(id2);
-                id2 = id3;
-                id3 = id_of(j + 4);
                 ++j;
                 is_v = j + 1 >= nstep;
               } else {
@@ -919,7 +938,8 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           auto odd16 = [](uint32_t x) { return (((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0u; };   // bf16
           const uint32_t ex = smem_u32(smem + C::kOffExp + (sent & 1) * C::kTile16) + (c >> 3) * C::kHalf16;
           auto at16 = [&](int row) {
-            return reinterpret_cast<uint4*>(src + (c >> 3) * C::kHalf16 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            return reinterpret_cast<uint4*>(src + (row >> 3) * C::kGroup + (c >> 3) * 1024 + (row & 7) * 128 +
+                                            (((c & 7) ^ (row & 7)) << 4));
           };
           auto expand = [&](int row, uint2 v) {
             st_shared_v4(ex + (row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4), e4m3_lo(v.x),
