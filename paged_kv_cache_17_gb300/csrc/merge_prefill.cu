@@ -3,7 +3,8 @@
 //   out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j,   lse = ln 2 (M + log2 sum ..).
 // One warp per (token, head); records are taken in order, so the result does not depend on
 // timing.  Bound by reading the records once, which the attention before it leaves in L2: 24 x 3 to 8
-// tokens, 32 heads of 128, 3 splits (6 MB): 4 us, most of it launch and first loads.
+// tokens, 32 heads of 128, 3 splits (6 MB): 7.6 us by itself with cold caches, most of it the chain
+// row -> sequence -> records; its launch alone runs under the attention's end.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -94,7 +94,8 @@ template <typename T>
 T* vector(const at::Tensor* t, const char* name, at::ScalarType type, int64_t n) {
   if (!t) return nullptr;
   if (t->scalar_type() != type || t->dim() != 1 || t->size(0) != n || !t->is_contiguous())
-    value_error(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor [" + std::to_string(n) + "]");
+    value_error(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor [" + std::to_string(n) +
+                "]");
   return static_cast<T*>(t->data_ptr());
 }
 
@@ -128,7 +129,14 @@ float number(PyObject* o, const char* name) {
   }
   return static_cast<float>(v);
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be true or false");
+  }
+  return v == 1;
+}
 
 void arguments(Py_ssize_t got, Py_ssize_t want) {
   if (got != want) type_error("expected " + std::to_string(want) + " arguments, got " + std::to_string(got));
@@ -176,7 +184,7 @@ PyObject* append(PyObject* const* a) {
     x.positions = vector<const int32_t>(positions, "positions", at::kInt, tokens);
     x.rotary_dim = static_cast<int32_t>(2 * half);
   }
-  x.interleaved = truth(a[12]);
+  x.interleaved = truth(a[12], "interleaved");
   x.rope_scale = number(a[13], "rope_scale");
   const at::Tensor* given = beside(a[7], "q_out", dev);
   at::Tensor out = given ? *given : fresh({tokens, hq, d}, at::kBFloat16, dev);
@@ -231,7 +239,7 @@ PyObject* prefill(PyObject* const* a) {
     ws = &own;
   }
   const float scale = number(a[6], "softmax_scale");
-  const int32_t causal = truth(a[8]);
+  const int32_t causal = truth(a[8], "causal");
   void* const ws_ptr = need > 0 ? ws->data_ptr() : nullptr;
   const size_t ws_bytes = need > 0 ? ws->numel() * ws->element_size() : 0;
   void *const qp = q.data_ptr(), *const op = out.data_ptr();
