@@ -926,10 +926,12 @@ namespace {
 //   for the uneven end; with records, their writing and reading and the merge kernel on top.  The
 //   choice was the best or within 3 % of it on a sweep of runs for one token over 777, 24 x 3-8 tokens over
 //   1800-12,000, 4096 over 32,768 and 16 x 1-448 over 750-1500.  PKV_SPLIT_TOKENS fixes the run.
-//   A run has at most 512 steps (65,536 keys), however many records that takes: the tensor cores add
-//   to their fp32 accumulators by truncation, up to 2^-23 of the sum for each of a step's 8 additions,
-//   all towards zero.  One run over 2^20 keys of positive V came out 0.67 % low, over 2^17 0.09 %; the
-//   limit keeps it below 2^-11, an eighth of the output's rounding to bf16.  (The merge adds in rounded fp32.)
+//   At most 512 steps (65,536 keys) go into one accumulator: the tensor cores add to it by
+//   truncation, up to 2^-23 of the sum for each of a step's 8 additions, all towards zero.  One run over
+//   2^20 keys of positive V came out 0.67 % low, over 2^17 0.09 %; the limit keeps it below 2^-11, an
+//   eighth of the output's rounding to bf16.  Narrow runs are cut at it (the merge adds in rounded
+//   fp32), however many records that takes; wide ones move their output to their records there, so that a
+//   long prompt at once needs one record a row.
 struct PrefillPlan {
   bool wide;
   int tile_slots, splits, split_tiles;
@@ -941,7 +943,6 @@ constexpr double kPrefillWorkUs = 3.0;              // a work's start and end
 constexpr double kPrefillMergeUs = 4.0;             // the merge kernel
 constexpr double kPrefillRecordBytesPerUs = 4.0e6;  // records written, then read
 constexpr long long kPrefillMaxRecords = 1LL << 20;
-constexpr int kPrefillMaxRun = 512;                 // steps
 
 PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max_context_len, int sm_count) {
   const int g = hq / hkv;
@@ -955,17 +956,18 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
   const int steps = std::max(1, (max_context_len + 127) / 128);
   pp.splits = 1;
   pp.split_tiles = steps;
+  const int most = pp.wide ? steps : pkv::kPrefillMaxRun;
   int forced = 0;
   if (const char* env = std::getenv("PKV_SPLIT_TOKENS")) {
     const long v = std::strtol(env, nullptr, 10);
-    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, std::min(steps, kPrefillMaxRun)));
+    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, std::min(steps, most)));
   }
   if (forced > 0) {
     pp.split_tiles = forced;
     pp.splits = (steps + forced - 1) / forced;
   } else {
     double best = -1;
-    const int least = (steps + kPrefillMaxRun - 1) / kPrefillMaxRun;
+    const int least = (steps + most - 1) / most;
     for (int n = least; n <= std::max(least, std::min(steps, 48)); ++n) {
       const int run = (steps + n - 1) / n;
       if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
@@ -981,7 +983,7 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
       }
     }
   }
-  if (pp.splits > 1) {
+  if (pp.splits > 1 || pp.split_tiles > pkv::kPrefillMaxRun) {
     pp.ml_bytes = round256(static_cast<size_t>(rows) * pp.splits * 2 * sizeof(float));
     pp.ws_bytes = pp.ml_bytes + round256(static_cast<size_t>(rows) * pp.splits * d * sizeof(float));
   }
@@ -1116,7 +1118,7 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
   p.scales = cache->scales;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  if (pp.splits > 1) {
+  if (pp.ws_bytes > 0) {
     p.part_ml = static_cast<float2*>(workspace);
     p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + pp.ml_bytes);
   }

@@ -419,11 +419,17 @@ struct Steps {
 
 }  // namespace
 
-template <int D, bool FP8, bool WIDE>
+// The forms are kernels of their own for the instruction cache's sake: the lines of kWideLong (runs of more
+// than kPrefillMaxRun steps) in every kernel took the E4M3 case above from 505 to 523 us and prompts from 118.6 to
+// 120.8; without those that write records it is 500 and 117.6.
+enum PrefillForm { kNarrow, kWide, kWideSplit, kWideLong };
+
+template <int D, bool FP8, PrefillForm FORM>
 __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
   using C = PrefillCfg<D, FP8>;
+  constexpr bool WIDE = FORM != kNarrow, LONG = FORM == kWideLong;
   constexpr unsigned NS = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
                 ok = wait(&sh.p_half[g], parity);
                 if (!ok) break;
                 tc_fence_after();
-                issue_o(g, 0, j == 0, v_lo(j));
+                issue_o(g, 0, LONG ? (j & (kPrefillMaxRun - 1)) == 0 : j == 0, v_lo(j));
                 ok = wait(&sh.p_full[g], parity);
                 if (!ok) break;
                 parity ^= 1;
@@ -1058,7 +1064,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       const int hq = w.h * G + (r & (G - 1));
       const int64_t orow = static_cast<int64_t>(w.tok0 + my_i) * p.hq + hq;
       const int64_t rec = static_cast<int64_t>(w.split) * p.total_q * p.hq + orow;
-      const bool split_out = p.splits > 1;
+      const bool split_out = FORM == kWideSplit || (FORM != kWide && p.splits > 1);
       if (WIDE ? nloc == 0 : st.nstep == 0) {  // rows that see nothing (of this split)
         if (rv && (WIDE || g == 0)) {
           if (split_out) {
@@ -1140,6 +1146,22 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       const int warp_lim = __reduce_min_sync(kFull, rv ? my_lim : 0x7fffffff);
       const bool idle = !__any_sync(kFull, rv);  // no row of the warp exists: its products go nowhere
       float m_used = -INFINITY, l = 0.f;
+      // LONG: after every kPrefillMaxRun steps the output so far moves to the row's record, in rounded fp32
+      // (the tensor cores' additions truncate), by reference m_moved; the next products start anew
+      float m_moved = -INFINITY;
+      bool moved = false;
+      auto moved_by = [&]() { return m_moved == m_used ? 1.f : fast_exp2(m_moved - m_used); };
+      auto add_moved = [&](float (&o)[32], int col, float by) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_acc + rec * D + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 v = src[i];
+          o[4 * i] = fmaf(v.x, by, o[4 * i]);
+          o[4 * i + 1] = fmaf(v.y, by, o[4 * i + 1]);
+          o[4 * i + 2] = fmaf(v.z, by, o[4 * i + 2]);
+          o[4 * i + 3] = fmaf(v.w, by, o[4 * i + 3]);
+        }
+      };
       for (int t = 0; t < nloc; ++t) {
         const int key0 = (st.k0 + (WIDE ? t : 2 * t + g)) * C::kKeys;
         const bool ok = wait_for(&sh.s_full[g], (c_s + t) & 1, abort);
@@ -1150,6 +1172,23 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
         tc_fence_after();
         if (!idle) {
+          if (LONG && t > 0 && (t & (kPrefillMaxRun - 1)) == 0) {
+            const float by = moved_by();
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+              float o[32];
+              tmem_ld32(ocol + D * g + col, o);
+              if (rv) {
+                if (moved) add_moved(o, col, by);
+                float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * D + col);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+              __syncwarp();
+            }
+            moved = true;
+            m_moved = m_used;
+          }
           // keys that a row does not see: -inf over their scores, in the columns (a loop of 32: this is
           // for a work's last steps, and straight code for 128 is slow to fetch)
           if (key0 + C::kKeys > warp_lim) {
@@ -1286,6 +1325,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             for (int ch = 0; ch < D / 32; ++ch) {  // (the words go to columns already read)
               float o[32];
               tmem_ld32(ocol + D * g + 32 * ch, o);
+              if constexpr (LONG) {
+                if (moved && rv) add_moved(o, 32 * ch, moved_by());
+                __syncwarp();
+              }
               uint32_t words[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) words[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
@@ -1319,6 +1362,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           float o[32];
           if constexpr (WIDE) {
             tmem_ld32(ocol + D * g + col, o);
+            if (LONG && moved && rv) add_moved(o, col, moved_by());
           } else {
             tmem_ld32(ocol + col, o);
 #pragma unroll
@@ -1381,11 +1425,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
   }
 }
 
-template <int D, bool FP8, bool WIDE>
+template <int D, bool FP8, PrefillForm FORM>
 static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillParams& p,
                           int tile_slots, cudaStream_t stream) {
   using C = PrefillCfg<D, FP8>;
-  auto kern = prefill_tc_kernel<D, FP8, WIDE>;
+  auto kern = prefill_tc_kernel<D, FP8, FORM>;
   static std::atomic<bool> configured[64] = {};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -1410,20 +1454,22 @@ static cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CU
   return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
 }
 
+template <int D, bool FP8>
+static cudaError_t launch_form(bool wide, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PrefillParams& p, int tile_slots, cudaStream_t stream) {
+  if (!wide) return launch<D, FP8, kNarrow>(tq, tk, tv, p, tile_slots, stream);
+  if (p.split_tiles > kPrefillMaxRun) return launch<D, FP8, kWideLong>(tq, tk, tv, p, tile_slots, stream);
+  return p.splits > 1 ? launch<D, FP8, kWideSplit>(tq, tk, tv, p, tile_slots, stream)
+                      : launch<D, FP8, kWide>(tq, tk, tv, p, tile_slots, stream);
+}
+
 cudaError_t launch_prefill(int d, bool fp8, bool wide, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, const PrefillParams& p, int tile_slots, cudaStream_t stream) {
-  if (d == 64) {
-    if (fp8)
-      return wide ? launch<64, true, true>(tq, tk, tv, p, tile_slots, stream)
-                  : launch<64, true, false>(tq, tk, tv, p, tile_slots, stream);
-    return wide ? launch<64, false, true>(tq, tk, tv, p, tile_slots, stream)
-                : launch<64, false, false>(tq, tk, tv, p, tile_slots, stream);
-  }
-  if (fp8)
-    return wide ? launch<128, true, true>(tq, tk, tv, p, tile_slots, stream)
-                : launch<128, true, false>(tq, tk, tv, p, tile_slots, stream);
-  return wide ? launch<128, false, true>(tq, tk, tv, p, tile_slots, stream)
-              : launch<128, false, false>(tq, tk, tv, p, tile_slots, stream);
+  if (d == 64)
+    return fp8 ? launch_form<64, true>(wide, tq, tk, tv, p, tile_slots, stream)
+               : launch_form<64, false>(wide, tq, tk, tv, p, tile_slots, stream);
+  return fp8 ? launch_form<128, true>(wide, tq, tk, tv, p, tile_slots, stream)
+             : launch_form<128, false>(wide, tq, tk, tv, p, tile_slots, stream);
 }
 
 }  // namespace pkv

@@ -82,4 +82,7 @@ cudaError_t launch_merge_prefill(int d, const PrefillParams& p, bool fp8, cudaSt
 // Weights are stored times 2^kWeightBias in E4M3 pools' fp16 products (see prefill_tc.cu).
 constexpr float kPrefillWeightBias = 7.f;
 
+// 128-key steps whose products go into one accumulator (see plan_prefill); a power of two
+constexpr int kPrefillMaxRun = 512;
+
 }  // namespace pkv

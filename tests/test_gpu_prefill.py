@@ -205,12 +205,13 @@ def test_long_context_long_offsets(pkv):
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("split", [None, 1 << 22])
-def test_long_sums_keep_their_size(pkv, e4m3, split):
+@pytest.mark.parametrize("tokens", [10, 100])
+def test_long_sums_keep_their_size(pkv, e4m3, split, tokens):
     """2^20 keys (256 blocks over and over) of values in [0.5, 1.5): all terms of the sums have one
-    sign, and the tensor cores truncate their additions.  A run of at most 512 steps adds 8 x 512
-    times, each off by at most 2^-23 of the sum: 2^-11.  Roundings of the weights and the output have
-    either sign; over the 25,600 elements of the mean they leave under 2^-12.  One run over all keys was off by
-    2^-7.2."""
+    sign, and the tensor cores truncate their additions.  An accumulator takes at most 512 steps, 8 x 512
+    additions, each off by at most 2^-23 of the sum: 2^-11.  Roundings of the weights and the output have
+    either sign; over the 2,560 elements or more of the mean they leave under 2^-12.  One accumulator over all keys
+    was off by 2^-7.2."""
     d, n = 64, 1 << 20
     g = torch.Generator().manual_seed(5)
     k = torch.randn((256, 16, 1, d), generator=g).to(torch.bfloat16).cuda()
@@ -218,11 +219,11 @@ def test_long_sums_keep_their_size(pkv, e4m3, split):
     scales = None
     if e4m3:
         k, v, scales = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), torch.ones(2, 1, device="cuda")
-    q = torch.randn((100, 4, d), generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn((tokens, 4, d), generator=g).to(torch.bfloat16).cuda()
     tables = (torch.arange(n // 16, dtype=torch.int32, device="cuda") % 256).view(1, -1)
     c = torch.tensor([n], dtype=torch.int32, device="cuda")
     with split_tokens(split):
-        out = pkv.paged_prefill_attention(q, indptr([100]), k, v, tables, c, 0.125, causal=False, scales=scales)
+        out = pkv.paged_prefill_attention(q, indptr([tokens]), k, v, tables, c, 0.125, causal=False, scales=scales)
         assert pkv.check_device_status() == 0
     s = torch.einsum("thd,jd->thj", q.double(), k.double().view(-1, d)) * 0.125
     ref = torch.softmax(s, -1) @ v.double().view(-1, d)
@@ -231,6 +232,49 @@ def test_long_sums_keep_their_size(pkv, e4m3, split):
     # one element: the output's rounding, the sums' 2^-11, and as much for the weights' (the mean of over a
     # thousand of their roundings)
     assert float(off.abs().max()) <= 2.0 ** -8 + 2.0 ** -10
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 1 << 22])
+@pytest.mark.parametrize("d", [64, 128])
+def test_growing_scores_over_a_long_context(pkv, e4m3, split, d):
+    """131,072 + 70,000 keys, the blocks of the later ones larger: references move after the outputs of
+    the first 65,536 keys have been put aside, and the last part is cut inside a block.  The definition with
+    every key counted as often as the tables have it."""
+    n1, n2, tokens = 131072, 70003, 200
+    g = torch.Generator().manual_seed(9)
+    k = torch.randn((96, 16, 2, d), generator=g)
+    k[32:64] *= 3.0
+    k[64:] *= 9.0
+    k = k.to(torch.bfloat16).cuda()
+    v = torch.randn((96, 16, 2, d), generator=g).to(torch.bfloat16).cuda()
+    scales = None
+    if e4m3:
+        scales = torch.tensor([[0.25, 0.5], [0.125, 0.0625]], device="cuda")
+        k, v = ((x.float() / scales[i][:, None]).to(torch.float8_e4m3fn) for i, x in enumerate((k, v)))
+    kf, vf = ((x.double() if scales is None else x.double() * scales[i].double()[:, None]) for i, x in enumerate((k, v)))
+    q = torch.randn((tokens, 4, d), generator=g).to(torch.bfloat16).cuda()
+    b = torch.arange((n1 + n2 + 15) // 16, dtype=torch.int32, device="cuda")
+    tables = torch.where(b < 4096, b % 32, torch.where(b < n1 // 16, 32 + b % 32, 64 + b % 32)).to(torch.int32)
+    c = torch.tensor([n1 + n2], dtype=torch.int32, device="cuda")
+    lse = torch.empty((tokens, 4), device="cuda")
+    with split_tokens(split):
+        out = pkv.paged_prefill_attention(q, indptr([tokens]), k, v, tables.view(1, -1), c, 1 / math.sqrt(d),
+                                          causal=False, lse=lse, scales=scales)
+        assert pkv.check_device_status() == 0
+    times = torch.zeros(96 * 16, dtype=torch.float64, device="cuda")
+    at = tables.long().repeat_interleave(16) * 16 + torch.arange(16, device="cuda").repeat(len(tables))
+    times.index_add_(0, at[:n1 + n2], torch.ones(n1 + n2, dtype=torch.float64, device="cuda"))
+    for h in range(4):
+        kh, vh = kf[:, :, h // 2].reshape(-1, d), vf[:, :, h // 2].reshape(-1, d)
+        s = q[:, h].double() @ kh.T / math.sqrt(d) + torch.log(times)
+        ref, ref_lse = torch.softmax(s, -1) @ vh, torch.logsumexp(s, -1)
+        # a weight is off by at most 2^-8 of itself, the sums by 2^-11, so the output by that of the weighted
+        # sizes, and half a step of its own; scores of up to 200 or so in fp32: 2^-24 x 2 x 200 x log2(e) in the weights
+        size = torch.softmax(s, -1) @ vh.abs()
+        bound = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * size + 2.0 ** -8 * ref.abs() + 1e-6
+        assert bool(((out[:, h].double() - ref).abs() <= bound).all())
+        assert float((lse[:, h].double() - ref_lse).abs().max()) <= 2.0 ** -10
 
 
 def test_strided_queries(pkv):
