@@ -63,10 +63,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherParams 
       else e = mid;
     }
     const int first = p.kv_indptr[b], last = p.kv_indptr[b + 1];
-    if (first < 0 || last < first || last > p.num_rows) {
-      if (!is_v) set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
-    }
-    if (row >= first && row < last) {
+    if (first >= 0 && row >= first && row < last && last <= p.num_rows) {
       const int64_t n = (p.starts != nullptr ? static_cast<int64_t>(p.starts[b]) : 0) + (row - first);
       slot = -1;
       if (n < 0 || n >= static_cast<int64_t>(p.max_blocks) * kBlockSize) {
@@ -79,6 +76,11 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherParams 
     }
     slot_of[threadIdx.x] = slot;
   }
+  if (blockIdx.x == 0 && is_v)
+    for (int i = threadIdx.x; i < p.batch; i += kThreads) {
+      const int first = p.kv_indptr[i], last = p.kv_indptr[i + 1];
+      if (first < 0 || last < first || last > p.num_rows) set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
+    }
   __syncthreads();
 
   using In = typename std::conditional<FP8, uint2, uint4>::type;  // 8 elements

@@ -1153,7 +1153,8 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
   if (st != PKV_OK) return st;
   if (!a) return fail(PKV_ERR_INVALID_ARG, "descriptor is NULL");
   const int d = cache->head_dim, hkv = cache->num_kv_heads, hq = a->num_q_heads;
-  if (a->num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (a->num_tokens < 0 || a->num_tokens > 0x7fffffffLL)
+    return fail(PKV_ERR_INVALID_ARG, "num_tokens must be in [0, 2^31)");
   if (hq <= 0) return fail(PKV_ERR_INVALID_ARG, "num_q_heads must be positive");
   if (hq > 4096 || hkv > 4096) return fail(PKV_ERR_UNSUPPORTED, "more than 4096 heads");
   if (a->rotary_dim < 0 || a->rotary_dim > d || a->rotary_dim % 16 != 0)

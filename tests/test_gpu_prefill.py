@@ -440,6 +440,22 @@ def test_bad_range_leaves_its_rows(pkv, split):
     assert bool((out[11:] == 7).all()) and not bool((out[:11] == 7).all(-1).any())
 
 
+def test_bad_range_behind_the_last_work_is_flagged(pkv):
+    """64 sequences of a token fill every tile there can be; the 65th, whose range is bad, has none."""
+    lens = [1] * 64
+    q, k, v, scales, tables = make(lens, [20] * 64, 8, 2, 64, False, 72, junk=0.0)
+    tables = torch.cat((tables, tables[:1]))
+    c = torch.full((65,), 20, dtype=torch.int32, device="cuda")
+    ip = torch.tensor(offsets(lens) + [70], dtype=torch.int32, device="cuda")
+    pkv.check_device_status()
+    out = pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.125)
+    assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+    ip[65] = 64
+    again = pkv.paged_prefill_attention(q, ip, k, v, tables, c, 0.125)
+    assert pkv.check_device_status() == 0
+    assert torch.equal(out, again)
+
+
 def test_replay_with_other_lengths(pkv):
     """A captured call replayed after its offsets, lengths, tables and queries were overwritten: a padded batch
     whose real tokens change from step to step."""

@@ -235,6 +235,24 @@ def test_gather_bad_data(pkv):
     assert pkv.check_device_status() & pkv.DEVFLAG_BAD_INDPTR
 
 
+def test_gather_bad_ranges_leave_their_rows(pkv):
+    """A range that ends before it starts has no row to find it by, and one past the last row has: both are
+    flagged, and only the rows of good ranges are written."""
+    lens = [40, 50, 30]
+    k, v, _, tables = make_pool(lens, 2, 64, False, 4)
+    ref_k, ref_v = (torch.empty((120, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.paged_kv_gather(k, v, tables, torch.tensor(offsets(lens), dtype=torch.int32, device="cuda"), ref_k, ref_v)
+    assert pkv.check_device_status() == 0
+    for ip, good in (([0, 40, 30, 30], 40), ([0, 40, 90, 121], 90), ([0, 40, 90, 85], 90)):
+        ko, vo = (torch.full((120, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        pkv.paged_kv_gather(k, v, tables, torch.tensor(ip, dtype=torch.int32, device="cuda"), ko, vo)
+        assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+        for got, ref in ((ko, ref_k), (vo, ref_v)):
+            if ip[2] == 90:
+                assert torch.equal(got[:good], ref[:good])
+            assert bool((got[max(ip):] == 7).all()) and (ip[3] != 121 or bool((got[90:] == 7).all()))
+
+
 def test_prompt_to_decode(pkv):
     """A prompt in two chunks (norm + rotation + append, then attention), a decode step on the
     same pool, and the pages read back: the whole path against one pass in 64 bits."""

@@ -76,7 +76,7 @@ def test_append_refusals(pkv):
     bad, unsup = pkv.PKV_ERR_INVALID_ARG, pkv.PKV_ERR_UNSUPPORTED
     d = desc(pkv)
     assert append(pkv, d, num_tokens=0) == pkv.PKV_OK
-    assert append(pkv, d, num_tokens=-1) == bad
+    assert append(pkv, d, num_tokens=-1) == bad and append(pkv, d, num_tokens=1 << 31) == bad
     assert pkv.lib.pkv_qk_norm_rope_append(ctypes.byref(d), None, None) == bad
     assert append(pkv, desc(pkv, head_dim=80)) == unsup
     assert append(pkv, d, num_q_heads=0) == bad and append(pkv, d, num_q_heads=5000) == unsup
