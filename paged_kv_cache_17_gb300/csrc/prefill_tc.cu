@@ -85,7 +85,7 @@ struct PrefillCfg {
   static constexpr int kOffRing = kOffQ + 2 * kQTile;
   static constexpr int kOffExp = kOffRing + kSlots * kSlot;
   static constexpr int kOffBar = kOffExp + kExp * kTile16;
-  static constexpr int kBarBytes = 512;
+  static constexpr int kBarBytes = 528;
   static constexpr int kOffPoison = kOffBar + kBarBytes;  // int[kinds][D]
   static constexpr int kKinds = FP8 ? 1 : 3;               // NaN, +inf, -inf (E4M3 has no infinity)
   // 1008: alignment slack (the start of dynamic shared memory is 16-byte aligned)
@@ -114,7 +114,7 @@ struct PrefillShared {
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
   uint64_t v_sent[8];          // load of a V tile that warps 12-15 work on issued
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty;  // E4M3 wide: a barrier per tile that has steps, else the first
   uint64_t work_full[2], work_empty[2];
   uint64_t clc;                // answer of the work query landed
   uint64_t drain[2];           // every MMA that an issuer has issued done
@@ -123,9 +123,9 @@ struct PrefillShared {
   uint32_t tmem;
   int abort;
   int poisoned;  // 1 + number of the work whose V held values that are not finite
-  int epilogues;  // softmax warps through the epilogue of a work with steps, all works counted
+  uint16_t epilogues[8];  // of every softmax warp: works with steps that it is through with
 };
-static_assert(sizeof(PrefillShared) <= 512, "shared state");
+static_assert(sizeof(PrefillShared) <= 528, "shared state");
 
 namespace {
 
@@ -466,14 +466,15 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       mbar_init(&sh.work_full[i], 1);
       mbar_init(&sh.work_empty[i], kIssuers + C::kFixWarps + 8);  // one arrival per warp that reads it
     }
-    mbar_init(&sh.q_full, FP8 ? (WIDE ? 8 : 4) : 1);
+    mbar_init(&sh.q_full[0], FP8 ? 4 : 1);
+    mbar_init(&sh.q_full[1], 4);
     mbar_init(&sh.q_empty, kIssuers);
     mbar_init(&sh.clc, 1);
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
     sh.abort = 0;
     sh.poisoned = 0;
-    sh.epilogues = 0;
+    for (int i = 0; i < 8; ++i) sh.epilogues[i] = 0;
     fence_mbar_init();
   }
   if (threadIdx.x == C::kProducerWarp * 32) {
@@ -591,8 +592,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             return FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16) : ring_v_lo + vc.slot * (C::kSlot / 16);
           };
           auto free_v = [&](int j) { commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader); };
-          ok = wait(&sh.q_full, q_count & 1);
-          ++q_count;
+          if (!(FP8 && WIDE)) {
+            ok = wait(&sh.q_full[0], q_count & 1);
+            ++q_count;
+          }
           if constexpr (WIDE) {
             // The scores of step j + 1 follow P V of step j in the same columns, in issue order.  The
             // tiles take turns, so that one's products run under the other's softmax (left to themselves
@@ -607,6 +610,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             const int mine = g == 0 ? st.n_of[0] : st.n_of[1], other = g == 0 ? st.n_of[1] : st.n_of[0];
             unsigned parity = (g == 0 ? c_p[0] : c_p[1]) & 1;
             if (ok && g == 1 && other > 0 && leader) mbar_arrive(&sh.p_half[0]);
+            if (FP8 && mine > 0) {
+              ok = ok && wait(&sh.q_full[g], q_count & 1);
+              ++q_count;
+            }
             ok = ok && wait_k();
             if (ok) {
               tc_fence_after();
@@ -815,13 +822,13 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               if (q_count > 0) ok = wait_for(&sh.q_empty, (q_count - 1) & 1, abort);
               ok = __all_sync(kFull, ok);
               if (ok && leader) {
-                mbar_arrive_expect_tx(&sh.q_full, (WIDE ? 2 : 1) * C::kQTile);
+                mbar_arrive_expect_tx(&sh.q_full[0], (WIDE ? 2 : 1) * C::kQTile);
 #pragma unroll
                 for (int t = 0; t < (WIDE ? 2 : 1); ++t)
 #pragma unroll
                   for (int c = 0; c < C::kHalves; ++c)
                     tma_load_3d(smem + C::kOffQ + t * C::kQTile + c * C::kHalf16, &tm_q, c * 64, w.h * G,
-                                w.tok0 + t * tile_tok, &sh.q_full);
+                                w.tok0 + t * tile_tok, &sh.q_full[0]);
               }
             }
             if (ok) ++q_count;
@@ -878,7 +885,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         // nothing may be in flight when the CTA exits: the last tiles issued have landed
         for (unsigned i = base > NS ? base - NS : 0; i < base; ++i)
           if (!mbar_wait(&sh.full[i % NS], (i / NS) & 1)) break;
-        if (!FP8 && q_count > 0) mbar_wait(&sh.q_full, (q_count - 1) & 1);
+        if (!FP8 && q_count > 0) mbar_wait(&sh.q_full[0], (q_count - 1) & 1);
       }
       __syncwarp();
     } else if (warp < C::kFixWarp0) {
@@ -915,9 +922,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         bool cleared = false;
         auto clear = [&]() {
           cleared = true;
-          const volatile int* through = &sh.epilogues;
+          // (a thread looks at one warp: sums over warps, some of them ahead, would not do)
+          const volatile uint16_t* through = &sh.epilogues[ft & 7];
           const long long start = clock64();
-          while (ok && *through < static_cast<int>(8 * with_steps)) {
+          while (ok && static_cast<int16_t>(*through - with_steps) < 0) {
             if (*abort) ok = false;
             if (clock64() - start > kWaitLimitCycles) {
               ok = false;
@@ -1059,6 +1067,11 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     float2* join_ml = reinterpret_cast<float2*>(smem + C::kOffQ + C::kQTile);
     float* join_scale = reinterpret_cast<float*>(join_ml + 256);
     unsigned c_s = 0, c_o = 0;  // steps and works of the group so far
+    unsigned through = 0;       // works with steps that this warp is through with
+    auto through_with = [&]() {
+      ++through;
+      if (lane == 0) *const_cast<volatile uint16_t*>(&sh.epilogues[warp]) = static_cast<uint16_t>(through);
+    };
     bool dead = false;
     Work w;
     for (unsigned n = 0; !dead; ++n) {
@@ -1084,11 +1097,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             if (p.lse != nullptr) p.lse[orow] = -INFINITY;
           }
         }
-        if (FP8 && st.nstep > 0) {  // the other tile's scores wait for both
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full);
-        }
-        if (st.nstep > 0 && lane == 0) atomicAdd(&sh.epilogues, 1);
+        if (st.nstep > 0) through_with();
         continue;
       }
       float sscale = p.score_scale;
@@ -1136,7 +1145,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full);
+          if (lane == 0) mbar_arrive(&sh.q_full[WIDE ? g : 0]);
           // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
           // (a zero scale: a factor that leaves every score at 0 while masked ones stay -inf)
           sscale = odd || k_scale != k_scale ? __int_as_float(0x7fffffff)
@@ -1420,7 +1429,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       tc_fence_before();
       if constexpr (!WIDE) dead = named_sync_or(2, 256, dead);  // both are through with both outputs
       __syncwarp();  // (the list of values was read above; the output's stores need not have landed)
-      if (lane == 0) atomicAdd(&sh.epilogues, 1);
+      through_with();
     }
   }
 

@@ -456,6 +456,31 @@ def test_bad_range_behind_the_last_work_is_flagged(pkv):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 128), (40, 5, 64), (12, 3, 128)])
+def test_many_short_works_with_one_tile(pkv, e4m3, hq, hkv, d):
+    """Two-tile works whose second tile has no rows, hundreds of them: the softmax warps of that tile run
+    ahead of the first tile's by as many works as they are told of.  (E4M3: they had counted as the
+    first tile's, and scores were taken of the query rows of the work before.)"""
+    for seed in range(8):
+        g = torch.Generator().manual_seed(seed)
+        group = hq // hkv
+        lens = torch.randint(0, 320 // group, (40,), generator=g).tolist()
+        ctx = [n + int(torch.randint(0, 3, (1,), generator=g)) for n in lens]
+        q, k, v, scales, tables = make(lens, ctx, hq, hkv, d, e4m3, 100 + seed)
+        c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        out = pkv.paged_prefill_attention(q, indptr(lens), k, v, tables, c, 1.0, scales=scales)
+        assert pkv.check_device_status() == 0
+        ref, _, mag, size = attention_64(q, lens, k, v, scales, tables, ctx, 1.0, True)
+        bound, _ = attention_bounds(ref, mag, size, q, e4m3, d)
+        # E4M3: weights are fp16 times 2^7 (2^15 at most), whose steps are 2^-24 at the least: a weight below
+        # 2^-21 of the largest is off by up to 2^-32 of it, not of itself.  That shows where the larger weights
+        # meet values that are 0; n keys of at most 448 times a scale add n 2^-32 448 times it
+        small = max(ctx) * 2.0 ** -32 * 448 * float(scales[1].max()) if e4m3 else 0.0
+        off = (out.double() - ref).abs() - bound - small
+        assert not bool(torch.isnan(off).any()) and float(off.max()) <= 0, float(off.max())
+
+
 def test_replay_with_other_lengths(pkv):
     """A captured call replayed after its offsets, lengths, tables and queries were overwritten: a padded batch
     whose real tokens change from step to step."""
