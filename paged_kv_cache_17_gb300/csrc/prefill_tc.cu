@@ -47,10 +47,10 @@
 // rate (1.08 ms with the softmax left out).  The exponentials, 32 a cycle and SM, take half of a
 // step; a polynomial on the FMA pipe for a share of them costs more than it saves, and two threads a
 // row, 16 softmax warps, slow the other roles down more than they gain (1.46 ms).  Prompts of 257 to
-// 2048 tokens: 118 us, 59 % of the rate: a work is a handful of steps there, and its start, masked
+// 2048 tokens: 115 us, 60 % of the rate: a work is a handful of steps there, and its start, masked
 // steps and epilogue weigh beside them.  24 x 3 to 8 tokens over 1800 to 12,000 (narrow, split in
 // 3): 114 us = 5.4 TB/s of K and V, 80 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
-// 3000 to 9000, 64 + 8 heads: 0.505 ms = 1.43 PFLOP/s; V's expansion takes shared-memory
+// 3000 to 9000, 64 + 8 heads: 0.507 ms = 1.43 PFLOP/s; V's expansion takes shared-memory
 // bandwidth and issue slots from the products and the softmax.
 #include <cuda.h>
 #include <cuda_runtime.h>
