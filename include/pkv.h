@@ -425,7 +425,7 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
  *   q enters as it is (E4M3 pools: elements smaller than 2^-10 of their row's largest to within
  *   2^-18 of it).  Deterministic for given sizes and values; PKV_SPLIT_TOKENS fixes the partition
  *   length (rounded up to a multiple of 128; at most 65,536 where a sequence has 128 rows, tokens
- *   times query heads per kv head, or fewer on average).
+ *   times query heads per kv head, or fewer on average, else 2^22).
  *   workspace: pkv_prefill_workspace_size(...) bytes, 256-byte aligned, any contents, NULL when
  *     0; not to be used by two calls that can run at the same time.
  *   batch == 0 or total_q == 0 is a no-op.

@@ -956,11 +956,12 @@ PrefillPlan plan_prefill(int batch, int total_q, int hq, int hkv, int d, int max
   const int steps = std::max(1, (max_context_len + 127) / 128);
   pp.splits = 1;
   pp.split_tiles = steps;
-  const int most = pp.wide ? steps : pkv::kPrefillMaxRun;
+  // (a wide run of 2^15 steps takes 50 ms, well inside the limit of the waits of a tile without rows)
+  const int most = std::min(steps, pp.wide ? 1 << 15 : pkv::kPrefillMaxRun);
   int forced = 0;
   if (const char* env = std::getenv("PKV_SPLIT_TOKENS")) {
     const long v = std::strtol(env, nullptr, 10);
-    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, std::min(steps, most)));
+    if (v >= 16) forced = static_cast<int>(std::min<long>((v + 127) / 128, most));
   }
   if (forced > 0) {
     pp.split_tiles = forced;
