@@ -1138,6 +1138,16 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
   p.score_scale = std::max(std::fabs(softmax_scale) * 1.4426950408889634f, 1e-37f);
   p.splits = pp.splits;
   p.split_tiles = pp.split_tiles;
+  // tests only: waits for work and scores that run out (fewer tries, works held back)
+  p.wait_tries = pkv::kPrefillWaitTries;
+  if (const char* env = std::getenv("PKV_TEST_PREFILL_WAIT_TRIES")) {
+    const long v = std::strtol(env, nullptr, 10);
+    if (v > 0) p.wait_tries = static_cast<int>(std::min<long>(v, pkv::kPrefillWaitTries));
+  }
+  if (const char* env = std::getenv("PKV_TEST_PREFILL_POST_DELAY_CYCLES")) {
+    const long long v = std::strtoll(env, nullptr, 10);
+    p.test_post_delay_cycles = v > 0 ? std::min(v, 100000000LL) : 0;  // at most about 50 ms
+  }
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pkv::launch_prefill(d, fp8, pp.wide, tq, tk, tv, p, pp.tile_slots, cs);
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");

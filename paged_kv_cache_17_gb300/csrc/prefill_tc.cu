@@ -192,13 +192,14 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
       : "memory");
 }
 
-// Wait for a phase; false when the CTA has aborted or after 2^23 tries (each suspended by the hardware for
-// a time, so seconds).  Shorter code than wait_or_abort, at 30 places: the roles together do not
+// Wait for a phase; false when the CTA has aborted or after `tries` tries (2^23, each suspended by the
+// hardware for a time, so seconds; tests set fewer).  Shorter code than wait_or_abort, at 30 places: the roles together do not
 // fit the SM's instruction cache, and the fetches beyond it were at 83 % of their peak rate.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                         int tries = kPrefillWaitTries) {
   if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (int n = 0; n < (1 << 23) && !*abort; ++n)
+  for (int n = 0; n < tries && !*abort; ++n)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
   auto fail = [&]() { give_up(p.status, abort); };
   // the work number n (all roles see the same sequence); false: there is none left, or abort
   auto next_work = [&](unsigned n, Work& w, unsigned lanes = kFull) -> bool {
-    const bool ok = wait_for(&sh.work_full[n & 1], (n >> 1) & 1, abort);
+    const bool ok = wait_for(&sh.work_full[n & 1], (n >> 1) & 1, abort, p.wait_tries);
     if (!__all_sync(lanes, ok)) {
       if (!*abort) fail();
       return false;
@@ -809,6 +810,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           ok = n < 2 || wait_for(&sh.work_empty[n & 1], ((n >> 1) - 1) & 1, abort);
           ok = __all_sync(kFull, ok);
           if (ok) {
+            if (p.test_post_delay_cycles > 0) spin_cycles(p.test_post_delay_cycles);
             if (lane == 0) {
               sh.work[n & 1][0] = make_int4(w.tok0, w.ntok, w.seq, w.ctx);
               sh.work[n & 1][1] = make_int4(w.shift, w.h, w.split, 0);
@@ -1075,10 +1077,14 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
     bool dead = false;
     Work w;
     for (unsigned n = 0; !dead; ++n) {
-      if (!next_work(n, w)) {
-        dead = true;
-        break;
+      bool none = !next_work(n, w);
+      // narrow: the groups meet at barriers below, so all eight warps take the work or none does (one that gave
+      // up just before the work was passed on would leave the others waiting for it there)
+      if constexpr (!WIDE) {
+        __syncwarp();
+        none = named_sync_or(2, 256, none);
       }
+      if (none) break;
       const Steps<WIDE> st(w, p, tile_tok);
       const int nloc = st.n_of[g];
       const bool rv = my_i < w.ntok;
@@ -1181,7 +1187,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       };
       for (int t = 0; t < nloc; ++t) {
         const int key0 = (st.k0 + (WIDE ? t : 2 * t + g)) * C::kKeys;
-        const bool ok = wait_for(&sh.s_full[g], (c_s + t) & 1, abort);
+        const bool ok = wait_for(&sh.s_full[g], (c_s + t) & 1, abort, p.wait_tries);
         if (!__all_sync(kFull, ok)) {  // tensor-memory loads are warp-collective: leave as a warp
           if (!*abort) fail();
           dead = true;

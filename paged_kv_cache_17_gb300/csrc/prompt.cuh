@@ -71,6 +71,8 @@ struct PrefillParams {
   float score_scale;  // |softmax_scale| * log2(e), positive
   int splits;
   int split_tiles;  // 128-key tiles per split
+  int wait_tries;   // of a wait for work or scores: kPrefillWaitTries, or fewer (tests)
+  long long test_post_delay_cycles;  // tests: the loading warp holds every work back so long
 };
 
 // wide: 256 query rows per CTA (two tiles over the same keys); else 128 rows (one tile, its
@@ -78,6 +80,9 @@ struct PrefillParams {
 cudaError_t launch_prefill(int d, bool fp8, bool wide, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, const PrefillParams& p, int tile_slots, cudaStream_t stream);
 cudaError_t launch_merge_prefill(int d, const PrefillParams& p, bool fp8, cudaStream_t stream);
+
+// Tries after which a wait of the attention gives up
+constexpr int kPrefillWaitTries = 1 << 23;
 
 // Weights are stored times 2^kWeightBias in E4M3 pools' fp16 products (see prefill_tc.cu).
 constexpr float kPrefillWeightBias = 7.f;
