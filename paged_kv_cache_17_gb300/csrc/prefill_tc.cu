@@ -282,6 +282,16 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
+// One arrival by the lane with lead != 0, called by the whole warp: no branch, so the warp's lanes stay together for
+// the tensor-memory accesses that follow
+__device__ __forceinline__ void arrive_by(uint64_t* bar, bool lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead ? 1u : 0u)
+      : "memory");
+}
+
 // Ask for the next CTA of the grid that has not started, to do its work here; the 16-byte
 // answer lands in shared memory and completes on the barrier.
 __device__ __forceinline__ void clc_ask(uint4* answer, uint64_t* bar) {
@@ -914,7 +924,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       Work w;
       for (unsigned n = 0; ok; ++n) {
         // the warps leave together
-        if (named_sync_or(1, kFix, !next_work(n, w))) break;
+        const bool none = !next_work(n, w);
+        __syncwarp();
+        if (named_sync_or(1, kFix, none)) break;
         number = n;
         const Steps<WIDE> st(w, p, tile_tok);
         const int nstep = st.nstep;
@@ -934,8 +946,10 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               fail();
             }
           }
+          __syncwarp();
           named_sync(3, kFix);
           for (int i = ft; i < C::kKinds * D; i += kFix) poison[i] = 0x7fffffff;
+          __syncwarp();
           named_sync(3, kFix);
         };
         for (int j = FP8 ? 0 : st.first_cut; j < nstep; ++j) {
@@ -1009,6 +1023,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               for (int row = max(0, end) + r0; row < C::kKeys; row += kStep) *at16(row) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
+          __syncwarp();  // (rows are dealt by lane; the barriers are for whole warps)
           if (cut && named_sync_or(3, kFix, odd)) {  // rare: list them and take them out of the tile
             if (!cleared) clear();
             for (int row = max(0, seen) + r0; ok && row < min(end, C::kKeys); row += kStep) {
@@ -1037,6 +1052,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             }
           }
           fence_proxy_async_smem();  // the tile is read by the tensor cores
+          __syncwarp();
           if (named_sync_or(1, kFix, *abort != 0)) {
             ok = false;
             break;
@@ -1159,6 +1175,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
         if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
           if (g == 0) join_scale[r] = sscale;
+          __syncwarp();
           named_sync(2, 256);
           if (g == 1) sscale = join_scale[r];
         }
@@ -1267,6 +1284,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
               l *= alpha;
               m_used = top;
             }
+            __syncwarp();
             if (t > 0) {  // P V of the previous step was issued before these scores: it is done
 #pragma unroll 1
               for (int ch = 0; ch < D / 16; ++ch) {
@@ -1288,7 +1306,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_half[g]);
+          arrive_by(&sh.p_half[g], lane == 0);
           tmem_st16u(scol + 32, pw);
           weights(3, negm, pw);
           tmem_st16u(scol + 48, pw);
@@ -1321,6 +1339,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       if constexpr (!WIDE) {
         join_ml[g * 128 + r] = make_float2(m_used, l);
         tc_fence_before();
+        __syncwarp();
         dead = named_sync_or(2, 256, dead);
         tc_fence_after();
         const float2 x0 = join_ml[r], x1 = join_ml[128 + r];
@@ -1342,6 +1361,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           else if (p.lse != nullptr)
             p.lse[orow] = l == 0.f ? -INFINITY : (m_used - C::kBias + log2f(l)) * 0.69314718055994531f;
         }
+        // (the tensor-memory loads below are for whole warps, and rows that do not exist part from the others
+        // between them)
+        __syncwarp();
         if constexpr (WIDE) {
           if (!split_out) {
 #pragma unroll 1
@@ -1374,6 +1396,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
                 dst[0] = make_uint4(v[k], v[2 + k], v[4 + k], v[6 + k]);
                 dst[4] = make_uint4(v[8 + k], v[10 + k], v[12 + k], v[14 + k]);
               }
+              __syncwarp();
             }
           }
         }
@@ -1385,7 +1408,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           float o[32];
           if constexpr (WIDE) {
             tmem_ld32(ocol + D * g + col, o);
-            if (LONG && moved && rv) add_moved(o, col, moved_by());
+            if constexpr (LONG) {
+              if (moved && rv) add_moved(o, col, moved_by());
+            }
           } else {
             tmem_ld32(ocol + col, o);
 #pragma unroll
@@ -1412,6 +1437,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
                                     pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
             }
           }
+          __syncwarp();
         }
         // rare: values of V taken out of the cut tiles are added to the rows that see them (the warp
         // stored them just now)
@@ -1433,6 +1459,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         }
       }
       tc_fence_before();
+      __syncwarp();
       if constexpr (!WIDE) dead = named_sync_or(2, 256, dead);  // both are through with both outputs
       __syncwarp();  // (the list of values was read above; the output's stores need not have landed)
       through_with();
