@@ -233,6 +233,8 @@ PyObject* prefill(PyObject* const* a) {
                                                                            cache.head_dim, max_len)
                                               : 0;
   const at::Tensor* ws = beside(a[12], "workspace", dev);
+  // (its size is counted in elements, which an expanded tensor shares)
+  if (ws && !ws->is_contiguous()) value_error("workspace must be contiguous");
   at::Tensor own;
   if (need > 0 && !ws) {
     own = fresh({static_cast<int64_t>(need)}, at::kByte, dev);
