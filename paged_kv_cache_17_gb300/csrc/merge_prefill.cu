@@ -60,8 +60,11 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PrefillParams 
       num[3] = fmaf(wgt, v.w, num[3]);
     }
   }
-  float inv = den > 0.f || den != den ? 1.f / den : 0.f;
-  if constexpr (FP8) inv *= p.scales[p.hkv + head / p.group];
+  float inv = 0.f;  // of a row without keys
+  if (den > 0.f || den != den) {
+    inv = 1.f / den;
+    if constexpr (FP8) inv *= p.scales[p.hkv + head / p.group];
+  }
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * DPL);
   if constexpr (DPL == 4)
     *reinterpret_cast<uint2*>(dst) =

@@ -1168,10 +1168,12 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.q_full[WIDE ? g : 0]);
-          // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value
+          // the row's scores come out times 2^ex; a row with a NaN or an infinity has no value, unless it
+          // sees no key: its scores are all masked, whatever they are
           // (a zero scale: a factor that leaves every score at 0 while masked ones stay -inf)
-          sscale = odd || k_scale != k_scale ? __int_as_float(0x7fffffff)
-                                             : fmaxf(sscale * fabsf(k_scale) / size, 1e-37f);
+          sscale = (odd || k_scale != k_scale) && Steps<WIDE>::lim(w, p, my_i) > 0
+                       ? __int_as_float(0x7fffffff)
+                       : fmaxf(sscale * fabsf(k_scale) / size, 1e-37f);
         }
         if constexpr (!WIDE) {  // group 1 works on the same rows: it takes their factors over
           if (g == 0) join_scale[r] = sscale;
@@ -1351,9 +1353,9 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
         m_used = top;
       }
       if (!dead && !idle) {
-        float inv = 1.f;
-        if (!split_out) {
-          inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        float inv = 0.f;  // of a row without keys
+        if (!split_out && (l > 0.f || l != l)) {
+          inv = 1.f / l;
           if constexpr (FP8) inv *= p.scales[p.hkv + w.h];
         }
         if (rv && (WIDE || g == 0)) {

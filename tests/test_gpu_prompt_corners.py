@@ -1,4 +1,6 @@
 """Corners of the prompt side's calls that the tests by operator leave out."""
+import math
+
 import pytest
 import torch
 
@@ -45,3 +47,45 @@ def test_workspace_without_memory_of_its_own(pkv):
                 pkv.paged_prefill_attention(*args, workspace=bad)
         ws.fill_(0xFF)
         assert torch.equal(pkv.paged_prefill_attention(*args, workspace=ws), want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("n,c,row", [(30, 12, 5), (40, 17, 5), (40, 17, 0), (300, 100, 195), (300, 300, None), (290, 200, 89)])
+def test_queries_not_finite_of_rows_without_keys(pkv, n, c, row, split, e4m3):
+    """A row at a negative position sees nothing: out 0 and lse -inf, whatever its query holds."""
+    hq, hkv, d = 8, 2, 64
+    k, v, scales, tables = make_pool([c], hkv, d, e4m3, 11, junk=float("nan"))
+    g = torch.Generator().manual_seed(12)
+    q = torch.randn((n, hq, d), generator=g).to(torch.bfloat16).cuda()
+    for h, x in ((1, math.nan), (3, math.inf), (6, -math.inf)):
+        q[n - 1, h, 7] = x
+        if row is not None:
+            q[row, h, 7] = x
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    with split_tokens(split):
+        pkv.paged_prefill_attention(q, ints([0, n]), k, v, tables, ints([c]), 0.125, out, lse=lse, scales=scales)
+    assert pkv.check_device_status() == 0
+    blind = n - c
+    assert bool((out[:blind] == 0).all()) and bool((lse[:blind] == -math.inf).all())
+    bad = torch.isnan(out).any(-1)
+    want = torch.zeros_like(bad)
+    want[n - 1, [1, 3, 6]] = True
+    assert torch.equal(bad, want) and torch.equal(torch.isnan(lse), want)
+
+
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("which", [0, 1])
+def test_pool_scales_not_finite_and_rows_without_keys(pkv, which, split):
+    n, c, hq, hkv, d = 300, 200, 8, 2, 64
+    k, v, scales, tables = make_pool([c], hkv, d, True, 11)
+    scales[which, 1] = math.nan
+    g = torch.Generator().manual_seed(12)
+    q = torch.randn((n, hq, d), generator=g).to(torch.bfloat16).cuda()
+    lse = torch.full((n, hq), 7.0, device="cuda")
+    with split_tokens(split):
+        out = pkv.paged_prefill_attention(q, ints([0, n]), k, v, tables, ints([c]), 0.125, lse=lse, scales=scales)
+    assert bool((out[:n - c] == 0).all()) and bool((lse[:n - c] == -math.inf).all())
+    bad = torch.isnan(out)
+    assert bool(bad[n - c:, 4:].all()) and not bool(bad[:, :4].any())
