@@ -448,7 +448,8 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
  *   bf16 output).
  *   kv_indptr: [batch + 1] int32, not decreasing, at most num_rows.  Rows before kv_indptr[0]
  *     or from kv_indptr[batch] on are left as they were.  A bad range sets PKV_DEVFLAG_BAD_INDPTR
- *     and its rows are left as they were.
+ *     and its rows are left as they were; the other ranges are read all the same (offsets out of order
+ *     can give two of them a row: it is unspecified which writes it).
  *   starts: [batch] int32, or NULL for 0.
  *   A position outside [0, max_blocks_per_seq * 16) reads as zeros and sets
  *   PKV_DEVFLAG_BAD_CONTEXT_LEN; a block id outside the pool reads as zeros and sets

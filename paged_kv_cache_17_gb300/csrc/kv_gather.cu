@@ -47,24 +47,45 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherParams 
   const int ns = (p.batch + step - 1) / step;  // samples at 0, step, 2 step, ..
   for (int i = threadIdx.x; i < ns; i += kThreads) sample[i] = p.kv_indptr[i * step];
   __syncthreads();
+  int b = 0;
+  bool lost = false;  // this thread's row is of no range that the search finds
+  const int64_t row = row0 + threadIdx.x;
   if (threadIdx.x < nrows) {
-    const int64_t row = row0 + threadIdx.x;
-    int64_t slot = -2;
     int lo = 0, hi = ns;  // the answer's sample is in [lo, hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sample[mid] <= row) lo = mid;
       else hi = mid;
     }
-    int b = lo * step, e = min(p.batch, b + step);
+    b = lo * step;
+    int e = min(p.batch, b + step);
     while (e - b > 1) {
       const int mid = (b + e) >> 1;
       if (p.kv_indptr[mid] <= row) b = mid;
       else e = mid;
     }
     const int first = p.kv_indptr[b], last = p.kv_indptr[b + 1];
-    if (first >= 0 && row >= first && row < last && last <= p.num_rows) {
-      const int64_t n = (p.starts != nullptr ? static_cast<int64_t>(p.starts[b]) : 0) + (row - first);
+    lost = first < 0 || row < first || row >= last || last > p.num_rows;
+  }
+  // rows outside every range, or offsets out of order (a bad range), among which the search goes astray: all
+  // ranges are looked through, and the good ones say which rows are theirs
+  if (__syncthreads_or(lost)) {
+    int* range_of = sample;  // (the samples are done with)
+    if (threadIdx.x < nrows) range_of[threadIdx.x] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.batch; i += kThreads) {
+      const int64_t first = p.kv_indptr[i], last = p.kv_indptr[i + 1];
+      if (first < 0 || last > p.num_rows) continue;
+      const int64_t end = min(last, row0 + nrows);
+      for (int64_t r = max(first, row0); r < end; ++r) range_of[r - row0] = i;
+    }
+    __syncthreads();
+    if (lost) b = range_of[threadIdx.x];
+  }
+  if (threadIdx.x < nrows) {
+    int64_t slot = -2;
+    if (b >= 0) {
+      const int64_t n = (p.starts != nullptr ? static_cast<int64_t>(p.starts[b]) : 0) + (row - p.kv_indptr[b]);
       slot = -1;
       if (n < 0 || n >= static_cast<int64_t>(p.max_blocks) * kBlockSize) {
         set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);

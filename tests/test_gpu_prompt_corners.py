@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_helpers import split_tokens
-from prompt_helpers import make_pool
+from prompt_helpers import make_pool, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,46 @@ def test_pool_scales_not_finite_and_rows_without_keys(pkv, which, split):
     assert bool((out[:n - c] == 0).all()) and bool((lse[:n - c] == -math.inf).all())
     bad = torch.isnan(out)
     assert bool(bad[n - c:, 4:].all()) and not bool(bad[:, :4].any())
+
+
+def good_ranges(ip, rows):
+    return [(b, ip[b], ip[b + 1]) for b in range(len(ip) - 1) if 0 <= ip[b] <= ip[b + 1] <= rows]
+
+
+# offsets of four ranges of 40 rows of which one entry or two are bad; no good range shares a row with another
+DISORDER = [[0, 10, -5, 30, 40], [0, 10, 999, 30, 40], [0, -1, 12, 30, 40], [30, 40, 0, 10, 20], [5, 20, 3, 5, 5],
+            [-2, 10, 24, 30, 50], [20, 40, 0, 20, 19]]
+
+
+@pytest.mark.parametrize("ip", DISORDER, ids=str)
+def test_gather_good_ranges_beside_bad_ones(pkv, ip):
+    lens = [40, 40, 40, 40]
+    k, v, _, tables = make_pool(lens, 2, 64, False, 3)
+    ko, vo = (torch.full((40, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.check_device_status()
+    pkv.paged_kv_gather(k, v, tables, ints(ip), ko, vo)
+    assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+    for x, o in ((k, ko), (v, vo)):
+        want = torch.full_like(o, 7.0)
+        for b, first, last in good_ranges(ip, 40):
+            want[first:last] = x[tables[b].long()].flatten(0, 1)[:last - first]
+        assert torch.equal(o, want)
+
+
+def test_gather_good_ranges_beside_bad_ones_of_many(pkv):
+    """More ranges than a CTA keeps samples of."""
+    n = 700
+    k, v, _, tables = make_pool([3] * n, 1, 64, False, 5)
+    ip = offsets([3] * n)
+    for i, x in ((100, -5), (300, 1 << 20), (650, -1)):
+        ip[i] = x
+    rows = 3 * n
+    ko, vo = (torch.full((rows, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pkv.check_device_status()
+    pkv.paged_kv_gather(k, v, tables, ints(ip), ko, vo)
+    assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+    for x, o in ((k, ko), (v, vo)):
+        want = torch.full_like(o, 7.0)
+        for b, first, last in good_ranges(ip, rows):
+            want[first:last] = x[tables[b].long()].flatten(0, 1)[:last - first]
+        assert torch.equal(o, want)
