@@ -405,7 +405,8 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
  *     (a multiple of 8).  The rows of sequence b are q_indptr[b] .. q_indptr[b + 1] - 1.
  *   q_indptr: [batch + 1] int32, q_indptr[0] = 0, not decreasing, at most total_q; a sequence may
  *     have no rows.  Rows from q_indptr[batch] on are neither read into a result nor written.
- *     A bad range sets PKV_DEVFLAG_BAD_INDPTR and that sequence is skipped.
+ *     A bad range sets PKV_DEVFLAG_BAD_INDPTR and that sequence is skipped; the others are attended
+ *     all the same (offsets out of order can give two of them a row, whose result is then unspecified).
  *   block_tables, max_blocks_per_seq, context_lens, max_context_len, softmax_scale: as for the
  *     decode; context_lens[b] counts the chunk's tokens when causal.
  *   causal = 1: row i of a sequence with n rows and context c is at position c - n + i and

@@ -35,7 +35,18 @@ __global__ void __launch_bounds__(256) merge_prefill_kernel(const PrefillParams 
     else e = mid;
   }
   const int first = p.q_indptr[b], last = p.q_indptr[b + 1];
-  if (tok < first || tok >= last || first < 0 || last > p.total_q) return;
+  bool written = tok >= first && tok < last && first >= 0 && last <= p.total_q;
+  if (!written) {
+    // offsets out of order (a bad range) lead the search astray: the warp looks through all ranges
+    bool mine = false;
+#pragma unroll 4
+    for (int i = lane; i < p.batch; i += 32) {
+      const int from = p.q_indptr[i], to = p.q_indptr[i + 1];
+      mine |= from >= 0 && tok >= from && tok < to && to <= p.total_q;
+    }
+    written = __any_sync(kFull, mine);
+  }
+  if (!written) return;
 
   float M = -INFINITY;
   for (int j = lane; j < p.splits; j += 32) M = fmaxf(M, p.part_ml[j * rows + row].x);

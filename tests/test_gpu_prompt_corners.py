@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_helpers import split_tokens
-from prompt_helpers import make_pool, offsets
+from prompt_helpers import attention_64, attention_bounds, make_pool, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,61 @@ def test_gather_good_ranges_beside_bad_ones_of_many(pkv):
         for b, first, last in good_ranges(ip, rows):
             want[first:last] = x[tables[b].long()].flatten(0, 1)[:last - first]
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("times", [1, 8])  # 40 rows: a tile a work; 320: two
+@pytest.mark.parametrize("ip", DISORDER, ids=str)
+def test_attention_of_good_ranges_beside_bad_ones(pkv, ip, times, split, e4m3):
+    hq, hkv, d, rows = 8, 2, 64, 40 * times
+    ip = [x * times for x in ip]
+    ctx = [700, 400, 330, 900]
+    k, v, scales, tables = make_pool(ctx, hkv, d, e4m3, 6, junk=float("nan"))
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn((rows, hq, d), generator=g).to(torch.bfloat16).cuda()
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    pkv.check_device_status()
+    with split_tokens(split):
+        pkv.paged_prefill_attention(q, ints(ip), k, v, tables, ints(ctx), 0.125, out, lse=lse, scales=scales)
+    assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+    left = torch.ones(rows, dtype=torch.bool, device="cuda")
+    for b, first, last in good_ranges(ip, rows):
+        left[first:last] = False
+        if first == last:
+            continue
+        qs = q[first:last]
+        ref, ref_lse, mag, size = attention_64(qs, [last - first], k, v, scales, tables[b:b + 1], [ctx[b]], 0.125, True)
+        bound, lse_bound = attention_bounds(ref, mag, size, qs, e4m3, d)
+        assert bool(((out[first:last].double() - ref).abs() <= bound).all()), b
+        assert bool(((lse[first:last].double() - ref_lse).abs() <= lse_bound + ref_lse.abs() * 2.0 ** -22).all()), b
+    assert bool((out[left] == 7).all()) and bool((lse[left] == 7).all())
+
+
+def test_split_attention_of_many_ranges_beside_bad_ones(pkv):
+    """More ranges than a CTA of the merge has threads."""
+    n, hq, hkv, d = 700, 4, 2, 64
+    ctx = [150] * n
+    k, v, _, tables = make_pool([150], hkv, d, False, 6)
+    tables = tables.expand(n, -1).contiguous()
+    ip = offsets([2] * n)
+    for i, x in ((100, -5), (300, 1 << 20), (650, -1)):
+        ip[i] = x
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn((2 * n + 9, hq, d), generator=g).to(torch.bfloat16).cuda()
+    for split in (None, 128):
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        pkv.check_device_status()
+        with split_tokens(split):
+            pkv.paged_prefill_attention(q, ints(ip), k, v, tables, ints(ctx), 0.125, out)
+        assert pkv.check_device_status() == pkv.DEVFLAG_BAD_INDPTR
+        left = torch.ones(len(q), dtype=torch.bool, device="cuda")
+        for _, first, last in good_ranges(ip, len(q)):
+            left[first:last] = False
+        assert int(left.sum()) == 9 + 3 * 4 and bool((out[left] == 7).all())
+        lens = [2] * n
+        ref, _, mag, size = attention_64(q[:2 * n], lens, k, v, None, tables, ctx, 0.125, True)
+        bound, _ = attention_bounds(ref, mag, size, q, False, d)
+        off = (out[:2 * n].double() - ref).abs() - bound
+        assert float(off[~left[:2 * n]].max()) <= 0
