@@ -94,7 +94,8 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: Optional[s
       blended linearly in original_max_position / wavelength;
     * "yarn": blended linearly in the pair index between the pair that turns beta_fast times over
       original_max_position (kept from there down) and the one that turns beta_slow times (divided
-      by factor from there up); rope_scale = 0.1 ln(factor) + 1.
+      by factor from there up), the former's index rounded down, at least 0, the latter's up, at most
+      R - 1; rope_scale = 0.1 ln(factor) + 1.
     """
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be positive and even")
@@ -123,9 +124,10 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: Optional[s
         def pair_turning(times):  # index (not whole) of the pair that turns so often
             return half * math.log(original_max_position / (2 * math.pi * times)) / math.log(base)
 
+        # (the end may lie behind the last pair: the ramp then runs on to it)
         lo = max(0, math.floor(pair_turning(beta_fast)))
-        hi = min(half - 1, math.ceil(pair_turning(beta_slow)))
-        cut = ((p - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        hi = min(rotary_dim - 1, math.ceil(pair_turning(beta_slow)))
+        cut = ((p - lo) / max(hi - lo, 1e-3)).clamp(0, 1) if hi >= 0 else torch.ones_like(p)
         f = f * ((1 - cut) + cut / factor)
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
