@@ -774,7 +774,7 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
             n = __shfl_sync(kFull, n, src);
             w.seq = b0 + src;
             int ctx = __shfl_sync(kFull, len, src);
-            const int cap = min(p.max_context_len, p.max_blocks * kBlockSize);
+            const int cap = p.max_context_len;  // within the tables (checked on the host, in 64 bits)
             if (ctx < 0 || ctx > cap) {
               set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
               ctx = max(0, min(ctx, cap));

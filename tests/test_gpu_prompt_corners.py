@@ -190,3 +190,17 @@ def test_split_attention_of_many_ranges_beside_bad_ones(pkv):
         bound, _ = attention_bounds(ref, mag, size, q, False, d)
         off = (out[:2 * n].double() - ref).abs() - bound
         assert float(off[~left[:2 * n]].max()) <= 0
+
+
+def test_tables_wider_than_any_context(pkv):
+    """2^27 columns: columns times the block size passes 32 bits."""
+    n, c, hq, hkv, d = 5, 300, 8, 2, 64
+    k, v, _, tables = make_pool([c], hkv, d, False, 7)
+    q = torch.randn((n, hq, d), device="cuda").to(torch.bfloat16)
+    want = pkv.paged_prefill_attention(q, ints([0, n]), k, v, tables, ints([c]), 0.125, max_context_len=c)
+    wide = torch.zeros((1, 1 << 27), dtype=torch.int32, device="cuda")
+    wide[:, :tables.shape[1]] = tables
+    pkv.check_device_status()
+    got = pkv.paged_prefill_attention(q, ints([0, n]), k, v, wide, ints([c]), 0.125, max_context_len=c)
+    assert pkv.check_device_status() == 0
+    assert torch.equal(got, want)
