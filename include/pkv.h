@@ -368,7 +368,7 @@ pkv_status pkv_stage_copy(void* dst, const void* src, size_t bytes, pkv_stream_t
  *     pool is skipped and sets PKV_DEVFLAG_BAD_SLOT; two tokens with one slot: unspecified which
  *     lands.
  *   inv_freq: [rotary_dim / 2] fp64, radians per position (scaling for long contexts is in
- *     these values and rope_scale).  rotary_dim: a multiple of 16 in [0, head_dim]; 0 rotates
+ *     these values and rope_scale); the pair of one that is not finite comes out NaN.  rotary_dim: a multiple of 16 in [0, head_dim]; 0 rotates
  *     nothing, and positions and inv_freq may be NULL.
  *   q_weight, k_weight: [head_dim] bf16, 16-byte aligned, or NULL.
  *   q_out: may be q itself (same pointer and stride); any other overlap with the inputs is not

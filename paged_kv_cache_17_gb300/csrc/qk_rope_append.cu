@@ -205,8 +205,11 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads)
   const bool makes = static_cast<int>(threadIdx.x) < p.groups * half;
   const int etok = makes ? static_cast<int>(threadIdx.x) / half : 0, pair = threadIdx.x - etok * half;
   unsigned long long step = 0;
+  float amp = p.rope_scale;
   if (makes) {
     const double f = p.inv_freq[pair] * kInvTwoPi;
+    // not finite: no angle (the integer below would be 0; by its bits, fp64 comparisons are slow here)
+    if ((~__double2hiint(f) & 0x7ff00000) == 0) amp = __int_as_float(0x7fffffff);
     step = static_cast<unsigned long long>(static_cast<long long>((f - rint(f)) * kTwo64));
   }
   auto position = [&](int64_t t0) { return makes && t0 + etok < p.num_tokens ? p.positions[t0 + etok] : 0; };
@@ -217,10 +220,10 @@ __global__ void __launch_bounds__(kMaxThreads, kThreadsPerSm / kMaxThreads)
     float sn, cn;
     sincospif(r, &sn, &cn);
     if constexpr (INTER) {
-      reinterpret_cast<float2*>(table)[threadIdx.x] = make_float2(cn * p.rope_scale, sn * p.rope_scale);
+      reinterpret_cast<float2*>(table)[threadIdx.x] = make_float2(cn * amp, sn * amp);
     } else {
-      table[etok * p.rot + pair] = cn * p.rope_scale;
-      table[etok * p.rot + half + pair] = sn * p.rope_scale;
+      table[etok * p.rot + pair] = cn * amp;
+      table[etok * p.rot + half + pair] = sn * amp;
     }
   };
   uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;

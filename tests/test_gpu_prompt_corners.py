@@ -204,3 +204,25 @@ def test_tables_wider_than_any_context(pkv):
     got = pkv.paged_prefill_attention(q, ints([0, n]), k, v, wide, ints([c]), 0.125, max_context_len=c)
     assert pkv.check_device_status() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_frequencies_not_finite(pkv, bad, interleaved):
+    """The pair of a frequency that is not finite has no angle: NaN, at position 0 too; the others are turned."""
+    T, d, rot = 33, 64, 32
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn((T, h, d), generator=g).to(torch.bfloat16).cuda() for h in (4, 2, 2))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f, _ = pkv.rope_inv_freq(rot, device="cuda")
+    kc, vc, _, _ = make_pool([T], 2, d, False, 1)
+    slots = torch.arange(T, device="cuda")
+    want = pkv.qk_norm_rope_append(q, k, v, pos, slots, kc, vc, inv_freq=f, interleaved=interleaved)
+    k2, v2 = kc.clone(), vc.clone()
+    f2 = f.clone()
+    f2[5] = bad
+    got = pkv.qk_norm_rope_append(q, k, v, pos, slots, k2, v2, inv_freq=f2, interleaved=interleaved)
+    pair = [10, 11] if interleaved else [5, 21]
+    rest = [i for i in range(d) if i not in pair]
+    for a, b in ((got, want), (k2.view(-1, 2, d)[:T], kc.view(-1, 2, d)[:T])):
+        assert bool(torch.isnan(a[..., pair]).all()) and torch.equal(a[..., rest], b[..., rest])
