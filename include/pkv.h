@@ -423,8 +423,8 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
  *   Arithmetic: tensor-core products with fp32 accumulation and fp32 softmax statistics; the
  *   softmax weights enter the second product rounded to bf16 (bf16 pools) or fp16 (E4M3 pools: to
  *   half a step, or 2^-32 of the row's largest weight if that is more);
- *   q enters as it is (E4M3 pools: elements smaller than 2^-10 of their row's largest to within
- *   2^-18 of it).  Deterministic for given sizes and values; PKV_SPLIT_TOKENS fixes the partition
+ *   q enters as it is (E4M3 pools: elements smaller than 2^-9 of their row's largest to within
+ *   2^-17 of it).  Deterministic for given sizes and values; PKV_SPLIT_TOKENS fixes the partition
  *   length (rounded up to a multiple of 128; at most 65,536 where a sequence has 128 rows, tokens
  *   times query heads per kv head, or fewer on average, else 2^22).
  *   workspace: pkv_prefill_workspace_size(...) bytes, 256-byte aligned, any contents, NULL when

@@ -10,8 +10,9 @@
 // (the A operand of the second product): bf16 for bf16 pools (half a step 2^-8), fp16 times
 // 2^7 for E4M3 pools (2^-11; the factor keeps weights down to 2^-31 of the largest).
 //   E4M3 pools: K enters as its codes; q enters as two E4M3 terms, hi + lo with lo the rest,
-// after a power of two per row: a bf16 has 8 significant bits and each term 4, so the pair is
-// exact for elements down to 2^-10 of the row's largest and off by 2^-18 of that below.  The
+// after a power of two per row that takes its largest into [128, 256): a bf16 has 8 significant bits and
+// each term 4, and E4M3's smallest step is 2^-9, so the pair is exact for elements down to 2^-9 of the
+// row's largest and off by at most 2^-17 of the largest (half that step, of 128) below.  The
 // two products add up in the same accumulators and cost what one 16-bit product does.  V is
 // expanded to fp16 (exact) in shared memory.  The scales of K and V are applied in fp32.
 //

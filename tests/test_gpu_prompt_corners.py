@@ -226,3 +226,32 @@ def test_frequencies_not_finite(pkv, bad, interleaved):
     rest = [i for i in range(d) if i not in pair]
     for a, b in ((got, want), (k2.view(-1, 2, d)[:T], kc.view(-1, 2, d)[:T])):
         assert bool(torch.isnan(a[..., pair]).all()) and torch.equal(a[..., rest], b[..., rest])
+
+
+def test_small_elements_of_a_query_over_an_e4m3_pool(pkv):
+    """Two E4M3 terms after the row's largest is taken into [128, 256): what is left after the first is held to
+    half of E4M3's smallest step, 2^-10, so an element is exact from 2^-9 of the largest up and off by at most
+    2^-17 of the largest below.  One key that meets only the small element; lse is its score."""
+    d = 64
+    k = torch.zeros((1, 16, 1, d), device="cuda")
+    k[0, 0, 0, 1] = 448.0
+    k = k.to(torch.float8_e4m3fn)
+    scales = torch.tensor([[1.0], [1.0]], device="cuda")
+    mant = 1 + torch.arange(128, device="cuda") / 128  # every bf16 of an octave
+    for octave in range(0, 16):
+        q = torch.zeros((128, 1, d), device="cuda")
+        q[:, 0, 0] = 1.0
+        q[:, 0, 1] = mant * 2.0 ** -octave / 2
+        q = q.to(torch.bfloat16)
+        lse = torch.empty((128, 1), device="cuda")
+        pkv.paged_prefill_attention(q, ints([0, 128]), k, k, torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                                    ints([1]), 1.0, causal=False, lse=lse, scales=scales)
+        want = q[:, 0, 1].double() * 448
+        # the two terms' products and their sum are exact; relative: log2(e) rounded, its product with the score,
+        # two sums, ln 2 rounded and its product, below 8 roundings of 2^-24; absolute, at most 2^-19: the same two
+        # sums with the weights' factor 2^7 (2^-21 of 7 together), log2 of it (two units in 7: 2^-20) and the
+        # exponential (2^-22), times ln 2
+        off = (lse[:, 0].double() - want).abs() - 8 * 2.0 ** -24 * want - 2.0 ** -19
+        held = 0.0 if octave < 9 else 2.0 ** -17 * 448
+        assert float(off.max()) <= held, octave
+    assert pkv.check_device_status() == 0
