@@ -27,7 +27,7 @@
 //                   out over them as 16-bit pairs, rare rescale of the output, epilogue
 //   warps 8, 10     issue the MMAs, a warp per tile (narrow: warp 8 for both groups)
 //   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block at a time
-//   warp 11         looks for bad ranges (first CTA)
+//   warp 11         looks for bad ranges
 //   warps 12-15     V: zero the rows past the context in the last tile, so that what a page holds
 //                   there (NaN included) meets weight 0 as 0; E4M3: expand V to fp16
 // A value of V that is not finite at a position some rows see and others do not would reach
@@ -902,12 +902,12 @@ __global__ void __launch_bounds__((PrefillCfg<D, FP8>::kThreads), 1)
       }
       __syncwarp();
     } else if (warp < C::kFixWarp0) {
-      // the warp left over looks for bad ranges (whoever finds work stops at the sequence it belongs to)
-      if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int b = lane; b < p.batch; b += 32) {
-          const int first = p.q_indptr[b], last = p.q_indptr[b + 1];
-          if (first < 0 || last < first || last > p.total_q) set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
-        }
+      // the warp left over looks for bad ranges (whoever finds work stops at the sequence it belongs to); in
+      // every CTA that starts: any CTA's start may be cancelled, the first one's too
+      for (int b = lane; b < p.batch; b += 32) {
+        const int first = p.q_indptr[b], last = p.q_indptr[b + 1];
+        if (first < 0 || last < first || last > p.total_q) set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
+      }
     } else {
       // ======================================================================== V: cut tiles, expansion
       constexpr int kFix = C::kFixWarps * 32;
