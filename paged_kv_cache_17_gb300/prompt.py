@@ -6,8 +6,8 @@
 * ``paged_kv_gather`` reads cached positions back, dequantised;
 * ``rope_inv_freq`` makes the rotation's frequencies, scaled for long contexts or not.
 
-Arguments are checked and marshalled by ``_pkv_prompt.so`` (``csrc/prompt_bind.cpp``).  Tensors must be on
-the current device.
+Arguments are checked and marshalled by ``_pkv_prompt.so`` (``csrc/prompt_bind.cpp``); where it was not built,
+the three calls raise ImportError.  Tensors must be on the current device.
 """
 from __future__ import annotations
 
@@ -49,13 +49,27 @@ def bind(lib: ctypes.CDLL) -> None:
 bind(_pkv.lib)
 
 
+class _Missing:
+    """Stands in for the module of the marshalled calls where it cannot be loaded: they raise, what does not
+    need it works."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(self._why)
+
+
 def _marshal():
     path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_pkv_prompt.so")
     if not os.path.exists(path):
-        raise ImportError(f"_pkv_prompt.so is not built ({path}); run python -m paged_kv_cache_17_gb300._build")
+        return _Missing(f"_pkv_prompt.so is not built ({path}); run python -m paged_kv_cache_17_gb300._build")
     spec = importlib.util.spec_from_file_location("_pkv_prompt", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    try:
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError as e:  # built against another torch
+        return _Missing(f"{path} cannot be loaded ({e}); run python -m paged_kv_cache_17_gb300._build")
     return mod
 
 
