@@ -414,7 +414,8 @@ pkv_status pkv_qk_norm_rope_append(const pkv_cache_desc* cache, const pkv_rope_a
  *   causal = 0: every row attends all context_lens[b] keys (cross attention to states held in
  *     pages).
  *   Row with keys j: out = sum_j softmax_j(softmax_scale q . K_j) V_j (bf16, [total_q][num_q_heads]
- *     [head_dim] contiguous, 16-byte aligned), lse = ln sum_j exp(softmax_scale q . K_j) (fp32
+ *     [head_dim] contiguous, 16-byte aligned; it may be q itself where q is contiguous, any other overlap
+ *     with the inputs is not allowed, and with q refused), lse = ln sum_j exp(softmax_scale q . K_j) (fp32
  *     [total_q][num_q_heads], or NULL).  A row that sees no key: out 0, lse -inf.
  *   What the pages hold past a context or at positions a row does not see does not reach that
  *   row, NaN and infinities included.

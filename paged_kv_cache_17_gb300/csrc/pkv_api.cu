@@ -1086,6 +1086,12 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
     return fail(PKV_ERR_INVALID_ARG, "max_context_len %d exceeds max_blocks_per_seq * 16 = %lld", max_context_len,
                 static_cast<long long>(max_blocks_per_seq) * 16);
   if (causal != 0 && causal != 1) return fail(PKV_ERR_INVALID_ARG, "causal must be 0 or 1");
+  // in place, a row's query is read by the work that writes the row, and before; otherwise by others too
+  const int64_t row = static_cast<int64_t>(num_q_heads) * cache->head_dim;
+  const uintptr_t qi = reinterpret_cast<uintptr_t>(q), oi = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t qlen = (static_cast<uintptr_t>(total_q - 1) * q_stride + row) * 2, olen = total_q * row * 2;
+  if (!(qi == oi && (total_q == 1 || q_stride == row)) && qi < oi + olen && oi < qi + qlen)
+    return fail(PKV_ERR_INVALID_ARG, "out overlaps q (it may be q itself, contiguous)");
   if (!(std::fabs(softmax_scale) < 1e38f)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite, below 1e38");
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;

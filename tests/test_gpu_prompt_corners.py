@@ -255,3 +255,21 @@ def test_small_elements_of_a_query_over_an_e4m3_pool(pkv):
         held = 0.0 if octave < 9 else 2.0 ** -17 * 448
         assert float(off.max()) <= held, octave
     assert pkv.check_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("lens,ctx", [([3, 1, 8], [700, 300, 8]), ([300, 65, 700], [400, 65, 1500])])
+def test_attention_in_place(pkv, lens, ctx, split, e4m3):
+    hq, hkv, d = 16, 4, 128
+    k, v, scales, tables = make_pool(ctx, hkv, d, e4m3, 7, junk=math.nan)
+    q = torch.randn((sum(lens) + 5, hq, d), device="cuda").to(torch.bfloat16)
+    rest = (k, v, tables, ints(ctx), 0.09)
+    with split_tokens(split):
+        want = pkv.paged_prefill_attention(q, ints(offsets(lens)), *rest, scales=scales)
+        for _ in range(3):
+            x = q.clone()
+            got = pkv.paged_prefill_attention(x, ints(offsets(lens)), *rest, x, scales=scales)
+            assert got is x and torch.equal(got[:-5], want[:-5]) and torch.equal(got[-5:], q[-5:])
+        with pytest.raises(pkv.PkvError, match="overlaps"):
+            pkv.paged_prefill_attention(q[:-1], ints(offsets(lens)), *rest, q[1:], scales=scales)
