@@ -444,7 +444,7 @@ pkv_status pkv_paged_prefill_attention(const pkv_cache_desc* cache, const void* 
 
 /*
  * Read ranges of cached positions back into contiguous rows: row kv_indptr[b] + i of k_out and
- * v_out ([num_rows][num_kv_heads][head_dim], bf16 or fp32, 16-byte aligned) becomes position
+ * v_out ([num_rows][num_kv_heads][head_dim], bf16 or fp32, 16-byte aligned, apart) becomes position
  * starts[b] + i of sequence b, for i = 0 .. kv_indptr[b + 1] - kv_indptr[b] - 1.
  *   bf16 pools: the elements; E4M3 pools: code * scale (an fp32 product, rounded once more for
  *   bf16 output).

@@ -1249,6 +1249,10 @@ pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block
     return fail(PKV_ERR_INVALID_ARG, "block_tables, kv_indptr and starts must be 4-byte aligned");
   if (!aligned(k_out, 16) || !aligned(v_out, 16))
     return fail(PKV_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  const uintptr_t ki = reinterpret_cast<uintptr_t>(k_out), vi = reinterpret_cast<uintptr_t>(v_out);
+  const uintptr_t len = static_cast<uintptr_t>(num_rows) * cache->num_kv_heads * cache->head_dim *
+                        (out_dtype == PKV_OUT_FP32 ? 4 : 2);
+  if (ki < vi + len && vi < ki + len) return fail(PKV_ERR_INVALID_ARG, "k_out overlaps v_out");
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
   pkv::GatherParams p{};
