@@ -73,10 +73,11 @@ typedef enum { PKV_OUT_BF16 = 0, PKV_OUT_FP32 = 1 } pkv_out_dtype;
 
 /* Device status word bits (pkv_check_device_status). */
 #define PKV_DEVFLAG_BAD_SLOT 0x1u        /* append: slot >= num_blocks * block_size (skipped) */
-#define PKV_DEVFLAG_BAD_CONTEXT_LEN 0x2u /* decode: context length out of range (clamped) */
-#define PKV_DEVFLAG_BAD_BLOCK_ID 0x4u    /* decode: block id outside the pool (read as zeros);
+#define PKV_DEVFLAG_BAD_CONTEXT_LEN 0x2u /* decode, prefill: context length out of range (clamped);
+                                            gather: position outside the table (read as zeros) */
+#define PKV_DEVFLAG_BAD_BLOCK_ID 0x4u    /* decode, prefill, gather: block id outside the pool (read as zeros);
                                             copy: pair skipped */
-#define PKV_DEVFLAG_WAIT_TIMEOUT 0x8u    /* decode: a pipeline wait hit its iteration limit */
+#define PKV_DEVFLAG_WAIT_TIMEOUT 0x8u    /* decode, prefill: a pipeline wait hit its iteration limit */
 #define PKV_DEVFLAG_BAD_INDPTR 0x10u     /* prefill, gather: an entry of the row offsets is negative,
                                             decreasing or past the rows (that sequence is skipped) */
 
@@ -366,7 +367,7 @@ pkv_status pkv_stage_copy(void* dst, const void* src, size_t bytes, pkv_stream_t
  *   positions: [num_tokens] int32; slot_mapping: [num_tokens] int64 as for the append: a
  *     negative slot writes nothing to the pool (the token's q is still written), one past the
  *     pool is skipped and sets PKV_DEVFLAG_BAD_SLOT; two tokens with one slot: unspecified which
- *     lands.
+ *     lands, in each part of the row.
  *   inv_freq: [rotary_dim / 2] fp64, radians per position (scaling for long contexts is in
  *     these values and rope_scale); the pair of one that is not finite comes out NaN.  rotary_dim: a multiple of 16 in [0, head_dim]; 0 rotates
  *     nothing, and positions and inv_freq may be NULL.

@@ -8,11 +8,12 @@
 // and in the output, and so are the 16 rows of a block.
 //
 // Bound by memory: each row is read once and written once.  A CTA takes a run of rows of K or
-// of V: it finds their sequences once (a search of indptr, sampled into shared memory), keeps
-// the pool slot of each row there, and then moves 8 elements per thread at a time with four
+// of V: it finds their sequences once (a search of indptr, sampled into shared memory; a pass over all of
+// it when a row is not found), keeps the pool slot of each row there, and then moves 8 elements per thread
+// at a time with four
 // loads in flight.  Measured, 8 heads of 128: bf16, 64 ranges of 512 to 4096 tokens (1.19 GB moved),
 // 175 us, the time of a plain copy of as many bytes; E4M3 to fp32, four of 32 to 70 thousand
-// (1.73 GB), 264 us, 96 % of it; one range of 1000 tokens 4.0 us, launch and two dependent loads.
+// (1.73 GB), 262 us, 97 % of it; one range of 1000 tokens 3.7 us, launch and three dependent loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -42,16 +42,17 @@
 // order K0 K1 V0 K2 V1 .., E4M3 two fp16 V tiles.  TMEM (512 columns): scores, then weights, of
 // group w at 128 w; outputs at 256 + w D.
 //
-// What bounds it.  A wide step is 2048 cycles of products at D = 128; the tensor cores are kept fed
+// What bounds it.  (Times with the caches flushed between calls; in brackets, calls one after another in
+// a graph.)  A wide step is 2048 cycles of products at D = 128; the tensor cores are kept fed
 // but for the part of the chain scores -> weights -> products that the other tile does not cover:
-// 4096 tokens over 32,768, 32 + 8 heads, bf16: 1.29 ms = 1.60 PFLOP/s, 86 % of the measured cuBLAS
-// rate (1.08 ms with the softmax left out).  The exponentials, 32 a cycle and SM, take half of a
-// step; a polynomial on the FMA pipe for a share of them costs more than it saves, and two threads a
-// row, 16 softmax warps, slow the other roles down more than they gain (1.46 ms).  Prompts of 257 to
-// 2048 tokens: 115 us, 60 % of the rate: a work is a handful of steps there, and its start, masked
+// 4096 tokens over 32,768, 32 + 8 heads, bf16: 1.30 ms (1.26) = 1.58 PFLOP/s, 85 % of the measured cuBLAS
+// rate (1.08 ms with the softmax left out, when the whole took 1.29 in a graph).  The exponentials, 32 a cycle
+// and SM, take half of a step; a polynomial on the FMA pipe for a share of them costs more than it saves, and
+// two threads a row, 16 softmax warps, slow the other roles down more than they gain (1.46 ms).  Prompts of 257
+// to 2048 tokens: 117 us (112), 59 % of the rate: a work is a handful of steps there, and its start, masked
 // steps and epilogue weigh beside them.  24 x 3 to 8 tokens over 1800 to 12,000 (narrow, split in
-// 3): 114 us = 5.4 TB/s of K and V, 80 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
-// 3000 to 9000, 64 + 8 heads: 0.507 ms = 1.43 PFLOP/s; V's expansion takes shared-memory
+// 3): 116 us (115) = 5.3 TB/s of K and V, 78 % of the measured copy.  E4M3, 4 x 700 to 1100 tokens over
+// 3000 to 9000, 64 + 8 heads: 0.521 ms (0.500) = 1.39 PFLOP/s; V's expansion takes shared-memory
 // bandwidth and issue slots from the products and the softmax.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -193,8 +194,9 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
       : "memory");
 }
 
-// Wait for a phase; false when the CTA has aborted or after `tries` tries (2^23, each suspended by the
-// hardware for a time, so seconds; tests set fewer).  Shorter code than wait_or_abort, at 30 places: the roles together do not
+// Wait for a phase; false when the CTA has aborted or after `tries` tries (2^23, tests set fewer; the hardware
+// suspends each, for 3 to 10 us as measured, so half a minute or more, but promises no time, and works of 50 ms
+// are waited for).  Shorter code than wait_or_abort, at 30 places: the roles together do not
 // fit the SM's instruction cache, and the fetches beyond it were at 83 % of their peak rate.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                          int tries = kPrefillWaitTries) {

@@ -21,7 +21,7 @@
 // and go through the tokens in rounds: the next round's pieces are on their way and its table of
 // sines is made while this round's are worked on.  Measured for 8192 tokens of 32 + 8 + 8 heads of 128 into
 // an E4M3 pool (184 MB) and 20,011 of 8 + 2 + 2 heads of 64, a quarter rotated, into bf16 (62 MB):
-// 39 and 11 us = 4.7 and 5.5 TB/s; a CTA per token 46 and 14, with the product of the angle in fp64 and
+// 39 and 11.5 us one after another in a graph = 4.7 and 5.4 TB/s; a CTA per token 46 and 14, with the product of the angle in fp64 and
 // every E4M3 code by a division 58 and 19; more CTAs per SM at 64 registers spill (64 and 18).  A warp per
 // token, its rows in turns and its sines in registers, with no barrier: 51 and 17 (half of its life is
 // the start: sines, then the first rows).
