@@ -464,6 +464,68 @@ pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block
                                void* k_out, void* v_out, pkv_out_dtype out_dtype, pkv_stream_t stream);
 
 /*
+ * Differential attention over the pool: the difference of two softmax maps, in the three forms that the plain
+ * attention has above (a chunk of new tokens, one token per sequence, one token per sequence where sequences
+ * share prefixes).
+ *   Heads of head_dim = d elements come in pairs, in q and in the pool: output head p (of num_q_heads / 2) has
+ *   the query heads 2p and 2p + 1, reads the keys of kv heads 2n and 2n + 1 and, as one value 2d wide, the
+ *   values of both; n = p / G, G = num_q_heads / num_kv_heads.  A row with the keys j:
+ *     A_m[j] = softmax_j(softmax_scale q[2p + m] . K[2n + m][j]),  m = 0, 1
+ *     y = sum_j (A_0[j] - lambda A_1[j]) (V[2n][j], V[2n + 1][j])
+ *     out[p] = out_scale * y_i * w_i / sqrt(mean(y^2) + eps),  or out_scale * y where norm_weight is NULL.
+ *   The pool is an ordinary one: pkv_paged_kv_append, pkv_qk_norm_rope_append, pkv_paged_kv_gather,
+ *   pkv_copy_blocks and pkv_paged_kv_checksum serve it, E4M3 scales per kv head included.
+ *   lambda: fp32, 4-byte aligned: [num_q_heads / 2], or a row of them for every query token, lambda_stride
+ *     elements apart (0: one row for all tokens); of any sign.
+ *   norm_weight: [2 * head_dim] bf16, 16-byte aligned, or NULL.  eps: finite, >= 0.  out_scale: finite.
+ *   out: [tokens][num_q_heads / 2][2 * head_dim], contiguous, 16-byte aligned; it must not overlap the inputs
+ *     (with q refused).  A row that sees no key is 0.
+ *   head_dim must be 64, num_q_heads and num_kv_heads even.
+ * Everything else is as for the plain call of the same form.  Statistics, the difference and the norm are held
+ * in fp32 and rounded once, to out's type.
+ */
+typedef struct {
+  const float* lambda;
+  int64_t lambda_stride; /* elements */
+  const void* norm_weight;
+  float eps;
+  float out_scale;
+} pkv_diff_desc;
+
+/* Chunks of new tokens (pkv_paged_prefill_attention; out is bf16, and there is no lse). */
+size_t pkv_diff_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t max_context_len);
+
+pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const void* q, int64_t q_stride,
+                                            const int32_t* q_indptr, int32_t total_q, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                            int32_t num_q_heads, int32_t max_context_len, int32_t causal,
+                                            float softmax_scale, const pkv_diff_desc* diff, void* out, void* workspace,
+                                            size_t workspace_bytes, pkv_stream_t stream);
+
+/* One token per sequence (pkv_paged_decode_attention). */
+size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_context_len);
+
+pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                           int32_t num_q_heads, int32_t max_context_len, float softmax_scale,
+                                           const pkv_diff_desc* diff, void* out, pkv_out_dtype out_dtype,
+                                           void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* One token per sequence, prefixes shared (pkv_cascade_decode_attention). */
+size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t max_context_len, int32_t num_prefixes, int32_t max_members,
+                                       int32_t max_prefix_len);
+
+pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const void* q,
+                                             const pkv_prefix_desc* prefixes, const int32_t* block_tables,
+                                             int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                             int32_t num_q_heads, int32_t max_context_len, float softmax_scale,
+                                             const pkv_diff_desc* diff, void* out, pkv_out_dtype out_dtype,
+                                             void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
  * Read and clear the device status word of the current device after the work queued on
  * `stream` so far has finished (this call synchronises `stream`).  *flags receives the
  * PKV_DEVFLAG_* bits (may be NULL).  Returns PKV_ERR_DEVICE_CHECK if any bit was set,

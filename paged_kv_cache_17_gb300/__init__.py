@@ -48,6 +48,8 @@ EXPORTED_SYMBOLS = (
     "pkv_copy_blocks", "pkv_cascade_workspace_size", "pkv_cascade_decode_attention", "pkv_paged_kv_checksum",
     "pkv_paged_append_decode", "pkv_stage_copy", "pkv_qk_norm_rope_append", "pkv_prefill_workspace_size",
     "pkv_paged_prefill_attention", "pkv_paged_kv_gather",
+    "pkv_diff_prefill_workspace_size", "pkv_paged_diff_prefill_attention", "pkv_diff_decode_workspace_size",
+    "pkv_paged_diff_decode_attention", "pkv_cascade_diff_workspace_size", "pkv_cascade_diff_decode_attention",
 )
 
 
@@ -409,3 +411,8 @@ def version() -> int:
 # the prompt side: norm + rotation + append, chunk attention, reading pages back
 from .prompt import (paged_kv_gather, paged_prefill_attention, prefill_workspace_size,  # noqa: E402,F401
                      qk_norm_rope_append, rope_inv_freq)
+
+# differential attention: chunks, one token per sequence, one token per sequence over shared prefixes
+from .diff import (cascade_diff_decode_attention, cascade_diff_workspace_size, diff_decode_workspace_size,  # noqa: E402,F401
+                   diff_lambda, diff_prefill_workspace_size, paged_diff_decode_attention,
+                   paged_diff_prefill_attention)

@@ -1,0 +1,45 @@
+// diff.cuh -- parameters and launchers of differential attention over the paged cache (launched from
+// pkv_api.cu): chunks of new tokens, one token per sequence, and one token per sequence over shared prefixes.
+//
+// Two kv heads 2n and 2n + 1 of 64 elements are side by side in a row of the pool, so the kernels see a pool of
+// hkv / 2 heads of 128: its K row holds the keys of both maps, its V row is the pair's value.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace pkv {
+
+constexpr int kDiffD = 64;            // elements of a head
+constexpr int kDiffW = 2 * kDiffD;    // of a pair's value
+
+struct DiffParams {
+  const uint16_t* q;        // [rows][2 heads][64] bf16, rows q_stride apart
+  int64_t q_stride;
+  const int32_t* q_indptr;  // rows of the sequences, or NULL: row b is sequence b's
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const float* scales;      // E4M3: [2][2 pairs]
+  const float* lambda;      // [heads] per row, lambda_stride apart
+  int64_t lambda_stride;
+  const uint16_t* norm_weight;  // [128] bf16, or NULL
+  void* out;                // [rows][heads][128]
+  uint32_t* status;
+  // shared prefixes (cascade): sequence b's keys are those of prefix seq_prefix[b], then its own
+  const int32_t* prefix_tables;
+  const int32_t* prefix_lens;
+  const int32_t* seq_prefix;
+  int max_prefix_blocks, max_prefix_len, num_prefixes;
+  int batch, rows;
+  int heads, pairs, group;  // output heads, pairs of kv heads, heads / pairs
+  int max_blocks, num_blocks, max_context_len;
+  int causal, out_fp32;
+  float score_scale;        // softmax_scale * log2(e)
+  float eps, out_scale;
+};
+
+cudaError_t launch_diff_simple(bool fp8, const DiffParams& p, const void* k, const void* v, cudaStream_t stream);
+
+}  // namespace pkv

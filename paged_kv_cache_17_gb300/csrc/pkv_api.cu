@@ -16,6 +16,7 @@
 #include "../../include/pkv.h"
 #include "cascade.cuh"
 #include "decode_launch.cuh"
+#include "diff.cuh"
 #include "prompt.cuh"
 
 namespace {
@@ -1274,6 +1275,239 @@ pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block
   const cudaError_t e = pkv::launch_kv_gather(cache->kv_dtype == PKV_KV_FP8_E4M3, out_dtype == PKV_OUT_FP32, p,
                                               dev->sm_count, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gather launch");
+  return PKV_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- differential attention
+
+namespace {
+
+pkv_status check_diff_heads(int32_t hq, int32_t hkv, int32_t d) {
+  if (d != pkv::kDiffD) return fail(PKV_ERR_UNSUPPORTED, "head_dim must be 64 for differential attention (got %d)", d);
+  if (hq <= 0 || hkv <= 0 || hq % 2 != 0 || hkv % 2 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "heads come in pairs: num_q_heads (%d) and num_kv_heads (%d) must be even", hq, hkv);
+  return PKV_OK;
+}
+
+// lambda, norm and output; out holds out_bytes, q q_bytes
+pkv_status check_diff(const pkv_diff_desc* f, int64_t heads, const void* q, int64_t q_bytes, const void* out,
+                      int64_t out_bytes) {
+  if (!f) return fail(PKV_ERR_INVALID_ARG, "the differential's descriptor is NULL");
+  if (!f->lambda || !aligned(f->lambda, 4)) return fail(PKV_ERR_INVALID_ARG, "lambda must be non-NULL and 4-byte aligned");
+  if (f->lambda_stride != 0 && (f->lambda_stride < heads || f->lambda_stride > (1LL << 38)))
+    return fail(PKV_ERR_INVALID_ARG, "lambda_stride (%lld) must be 0 or at least num_q_heads / 2",
+                static_cast<long long>(f->lambda_stride));
+  if (!aligned(f->norm_weight, 16)) return fail(PKV_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
+  if (f->norm_weight && !(f->eps >= 0.f && std::isfinite(f->eps)))
+    return fail(PKV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!std::isfinite(f->out_scale)) return fail(PKV_ERR_INVALID_ARG, "out_scale must be finite");
+  if (!out || !aligned(out, 16)) return fail(PKV_ERR_INVALID_ARG, "out must be non-NULL and 16-byte aligned");
+  const uintptr_t qi = reinterpret_cast<uintptr_t>(q), oi = reinterpret_cast<uintptr_t>(out);
+  if (qi < oi + out_bytes && oi < qi + q_bytes) return fail(PKV_ERR_INVALID_ARG, "out overlaps q");
+  return PKV_OK;
+}
+
+// what the three forms have in common
+pkv::DiffParams diff_params(const pkv_cache_desc* cache, const pkv_diff_desc* f, const void* q, int64_t q_stride,
+                            const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                            int32_t rows, int32_t hq, int32_t max_context_len, float softmax_scale, void* out,
+                            bool out_fp32, DeviceInfo* dev) {
+  pkv::DiffParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.scales = cache->scales;
+  p.lambda = f->lambda;
+  p.lambda_stride = f->lambda_stride;
+  p.norm_weight = static_cast<const uint16_t*>(f->norm_weight);
+  p.out = out;
+  p.status = dev->status;
+  p.batch = batch;
+  p.rows = rows;
+  p.heads = hq / 2;
+  p.pairs = cache->num_kv_heads / 2;
+  p.group = p.heads / p.pairs;
+  p.max_blocks = max_blocks;
+  p.num_blocks = static_cast<int>(cache->num_blocks);
+  p.max_context_len = max_context_len;
+  p.out_fp32 = out_fp32;
+  p.score_scale = softmax_scale * 1.4426950408889634f;  // log2(e)
+  p.eps = f->eps;
+  p.out_scale = f->out_scale;
+  return p;
+}
+
+// checks shared by the two calls of one token per sequence
+pkv_status check_diff_decode(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
+                             int32_t max_blocks, const int32_t* context_lens, int32_t batch, int32_t hq,
+                             int32_t max_context_len, float softmax_scale, const pkv_diff_desc* diff, const void* out,
+                             pkv_out_dtype out_dtype) {
+  if (!q || !block_tables || !context_lens)
+    return fail(PKV_ERR_INVALID_ARG, "q, block_tables and context_lens must be non-NULL");
+  if (!aligned(q, 16)) return fail(PKV_ERR_INVALID_ARG, "q must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return fail(PKV_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
+  if (out_dtype != PKV_OUT_BF16 && out_dtype != PKV_OUT_FP32)
+    return fail(PKV_ERR_INVALID_ARG, "unknown out_dtype %d", static_cast<int>(out_dtype));
+  if (max_blocks <= 0) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks) * 16)
+    return fail(PKV_ERR_INVALID_ARG, "max_context_len %d exceeds max_blocks_per_seq * 16 = %lld", max_context_len,
+                static_cast<long long>(max_blocks) * 16);
+  if (!(std::fabs(softmax_scale) < 1e38f)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite, below 1e38");
+  const int64_t row = static_cast<int64_t>(hq) * cache->head_dim;
+  return check_diff(diff, hq / 2, q, batch * row * 2, out, batch * row * (out_dtype == PKV_OUT_FP32 ? 4 : 2));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_diff_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t max_context_len) {
+  t_last_error.clear();
+  if (check_prefill_sizes(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
+      check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
+    return 0;
+  return 0;
+}
+
+pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const void* q, int64_t q_stride,
+                                            const int32_t* q_indptr, int32_t total_q, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                            int32_t num_q_heads, int32_t max_context_len, int32_t causal,
+                                            float softmax_scale, const pkv_diff_desc* diff, void* out, void* workspace,
+                                            size_t workspace_bytes, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  const int d = cache->head_dim, hkv = cache->num_kv_heads;
+  if ((st = check_prefill_sizes(batch, total_q, num_q_heads, hkv, d, max_context_len)) != PKV_OK) return st;
+  if ((st = check_diff_heads(num_q_heads, hkv, d)) != PKV_OK) return st;
+  if (batch == 0 || total_q == 0) return PKV_OK;
+  if ((st = check_rows("q", q, q_stride, num_q_heads, d)) != PKV_OK) return st;
+  if (!q_indptr || !block_tables || !context_lens)
+    return fail(PKV_ERR_INVALID_ARG, "q_indptr, block_tables and context_lens must be non-NULL");
+  if (!aligned(q_indptr, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return fail(PKV_ERR_INVALID_ARG, "q_indptr, block_tables and context_lens must be 4-byte aligned");
+  if (max_blocks_per_seq <= 0) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * 16)
+    return fail(PKV_ERR_INVALID_ARG, "max_context_len %d exceeds max_blocks_per_seq * 16 = %lld", max_context_len,
+                static_cast<long long>(max_blocks_per_seq) * 16);
+  if (causal != 0 && causal != 1) return fail(PKV_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!(std::fabs(softmax_scale) < 1e38f)) return fail(PKV_ERR_INVALID_ARG, "softmax_scale must be finite, below 1e38");
+  const int64_t row = static_cast<int64_t>(num_q_heads) * d;
+  if ((st = check_diff(diff, num_q_heads / 2, q, ((total_q - 1) * q_stride + row) * 2, out, total_q * row * 2)) != PKV_OK)
+    return st;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  pkv::DiffParams p = diff_params(cache, diff, q, q_stride, block_tables, max_blocks_per_seq, context_lens, batch,
+                                  total_q, num_q_heads, max_context_len, softmax_scale, out, false, dev);
+  p.q_indptr = q_indptr;
+  p.causal = causal;
+  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+  return PKV_OK;
+}
+
+size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_context_len) {
+  t_last_error.clear();
+  if (check_prefill_sizes(batch, batch, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
+      check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
+    return 0;
+  return 0;
+}
+
+pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                           int32_t num_q_heads, int32_t max_context_len, float softmax_scale,
+                                           const pkv_diff_desc* diff, void* out, pkv_out_dtype out_dtype,
+                                           void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  const int d = cache->head_dim, hkv = cache->num_kv_heads;
+  if ((st = check_prefill_sizes(batch, batch, num_q_heads, hkv, d, max_context_len)) != PKV_OK) return st;
+  if ((st = check_diff_heads(num_q_heads, hkv, d)) != PKV_OK) return st;
+  if (batch == 0) return PKV_OK;
+  if ((st = check_diff_decode(cache, q, block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads,
+                              max_context_len, softmax_scale, diff, out, out_dtype)) != PKV_OK)
+    return st;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  const pkv::DiffParams p =
+      diff_params(cache, diff, q, static_cast<int64_t>(num_q_heads) * d, block_tables, max_blocks_per_seq, context_lens,
+                  batch, batch, num_q_heads, max_context_len, softmax_scale, out, out_dtype == PKV_OUT_FP32, dev);
+  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+  return PKV_OK;
+}
+
+size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t max_context_len, int32_t num_prefixes, int32_t max_members,
+                                       int32_t max_prefix_len) {
+  t_last_error.clear();
+  if (num_prefixes < 0 || max_members < 0 || max_prefix_len < 0) {
+    fail(PKV_ERR_INVALID_ARG, "prefix sizes must be non-negative");
+    return 0;
+  }
+  if (check_prefill_sizes(batch, batch, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
+      check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
+    return 0;
+  return 0;
+}
+
+pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const pkv_prefix_desc* px,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                                             int32_t max_context_len, float softmax_scale, const pkv_diff_desc* diff,
+                                             void* out, pkv_out_dtype out_dtype, void* workspace,
+                                             size_t workspace_bytes, pkv_stream_t stream) {
+  t_last_error.clear();
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (!px) return fail(PKV_ERR_INVALID_ARG, "prefixes must be non-NULL");
+  if (px->num_prefixes < 0 || px->max_members < 0 || px->max_prefix_len < 0 || px->max_prefix_blocks < 0)
+    return fail(PKV_ERR_INVALID_ARG, "prefix sizes must be non-negative");
+  if (px->num_prefixes == 0 || px->max_members == 0 || px->max_prefix_len == 0)
+    return pkv_paged_diff_decode_attention(cache, q, block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads,
+                                           max_context_len, softmax_scale, diff, out, out_dtype, workspace,
+                                           workspace_bytes, stream);
+  const int d = cache->head_dim, hkv = cache->num_kv_heads;
+  if ((st = check_prefill_sizes(batch, batch, num_q_heads, hkv, d, max_context_len)) != PKV_OK) return st;
+  if ((st = check_diff_heads(num_q_heads, hkv, d)) != PKV_OK) return st;
+  if (batch == 0) return PKV_OK;
+  if (!px->prefix_tables || !px->prefix_lens || !px->member_indptr || !px->member_seqs || !px->seq_prefix)
+    return fail(PKV_ERR_INVALID_ARG, "prefix tables, lengths, member lists and seq_prefix must be non-NULL");
+  if (!aligned(px->prefix_tables, 4) || !aligned(px->prefix_lens, 4) || !aligned(px->member_indptr, 4) ||
+      !aligned(px->member_seqs, 4) || !aligned(px->seq_prefix, 4))
+    return fail(PKV_ERR_INVALID_ARG, "prefix arrays must be 4-byte aligned");
+  if (px->max_prefix_len % 16 != 0) return fail(PKV_ERR_INVALID_ARG, "max_prefix_len must be a multiple of 16");
+  if (px->max_prefix_len > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "max_prefix_len above 2^30");
+  if (static_cast<int64_t>(px->max_prefix_blocks) * 16 < px->max_prefix_len)
+    return fail(PKV_ERR_INVALID_ARG, "max_prefix_len exceeds max_prefix_blocks * 16");
+  if ((st = check_diff_decode(cache, q, block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads,
+                              max_context_len, softmax_scale, diff, out, out_dtype)) != PKV_OK)
+    return st;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PKV_OK) return st;
+  pkv::DiffParams p =
+      diff_params(cache, diff, q, static_cast<int64_t>(num_q_heads) * d, block_tables, max_blocks_per_seq, context_lens,
+                  batch, batch, num_q_heads, max_context_len, softmax_scale, out, out_dtype == PKV_OUT_FP32, dev);
+  p.prefix_tables = px->prefix_tables;
+  p.prefix_lens = px->prefix_lens;
+  p.seq_prefix = px->seq_prefix;
+  p.max_prefix_blocks = px->max_prefix_blocks;
+  p.max_prefix_len = px->max_prefix_len;
+  p.num_prefixes = px->num_prefixes;
+  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "differential cascade launch");
   return PKV_OK;
 }
 

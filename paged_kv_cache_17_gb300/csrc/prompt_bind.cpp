@@ -1,5 +1,5 @@
-// prompt_bind.cpp -- marshalling of the prompt side's three calls from torch tensors to the C ABI of
-// include/pkv.h (the functions of prompt.py, which documents them): checks of types, shapes,
+// prompt_bind.cpp -- marshalling of the prompt side's and the differential attention's calls from torch tensors to
+// the C ABI of include/pkv.h (the functions of prompt.py and diff.py, which document them): checks of types, shapes,
 // strides and devices, addresses, the output's and the workspace's memory, and nothing of the
 // computation.  In C++ because the calls last a few microseconds for one token on the GPU and
 // the same checks in Python with ctypes took 16 to 22 on the host.
@@ -282,6 +282,178 @@ PyObject* gather(PyObject* const* a) {
   return PyLong_FromLong(st);
 }
 
+// lambda ([heads] or [rows, heads] float32), norm_weight, eps and out_scale of a differential call
+pkv_diff_desc diff_of(PyObject* lam, PyObject* weight, PyObject* eps, PyObject* out_scale, int64_t rows, int64_t heads,
+                      int64_t d, int64_t dev) {
+  pkv_diff_desc f{};
+  const at::Tensor& l = needed(lam, "lam", dev);
+  if (l.scalar_type() != at::kFloat) type_error("lam must be float32");
+  const bool per_row = l.dim() == 2;
+  if ((!per_row && l.dim() != 1) || l.size(-1) != heads || (per_row && l.size(0) != rows))
+    value_error("lam must be [" + std::to_string(heads) + "] or [" + std::to_string(rows) + ", " +
+                std::to_string(heads) + "]");
+  if (heads > 1 && l.stride(-1) != 1) value_error("lam's heads must be contiguous (only the tokens may be strided)");
+  // (an expanded row, stride 0, is one row for all tokens)
+  f.lambda = static_cast<const float*>(l.data_ptr());
+  f.lambda_stride = per_row && rows > 1 ? l.stride(0) : 0;
+  f.norm_weight = vector<const void>(beside(weight, "norm_weight", dev), "norm_weight", at::kBFloat16, 2 * d);
+  f.eps = number(eps, "eps");
+  f.out_scale = number(out_scale, "out_scale");
+  return f;
+}
+
+// the output given, or a new bfloat16 one: [rows, heads, 2 d]
+at::Tensor diff_out(PyObject* o, int64_t rows, int64_t heads, int64_t d, bool fp32_too, int64_t dev) {
+  const at::Tensor* given = beside(o, "out", dev);
+  at::Tensor out = given ? *given : fresh({rows, heads, 2 * d}, at::kBFloat16, dev);
+  if (given && ((out.scalar_type() != at::kBFloat16 && !(fp32_too && out.scalar_type() == at::kFloat)) ||
+                out.dim() != 3 || out.size(0) != rows || out.size(1) != heads || out.size(2) != 2 * d ||
+                !out.is_contiguous()))
+    value_error(std::string("out must be a contiguous bfloat16 ") + (fp32_too ? "or float32 " : "") + "tensor [" +
+                std::to_string(rows) + ", " + std::to_string(heads) + ", " + std::to_string(2 * d) + "]");
+  return out;
+}
+
+// the workspace given, or one of the call's own: calls on several streams and captured graphs share none
+struct Workspace {
+  at::Tensor own;
+  void* at = nullptr;
+  size_t bytes = 0;
+  Workspace(PyObject* o, size_t need, int64_t dev) {
+    const at::Tensor* ws = beside(o, "workspace", dev);
+    if (ws && !ws->is_contiguous()) value_error("workspace must be contiguous");
+    if (need == 0) return;
+    if (!ws) {
+      own = fresh({static_cast<int64_t>(need)}, at::kByte, dev);
+      ws = &own;
+    }
+    at = ws->data_ptr();
+    bytes = ws->numel() * ws->element_size();
+  }
+};
+
+// q, q_indptr, k_cache, v_cache, block_tables, context_lens, softmax_scale, lam, out, norm_weight, eps, out_scale,
+// causal, scales, max_context_len, workspace
+PyObject* diff_prefill(PyObject* const* a) {
+  int64_t dev;
+  const pkv_cache_desc cache = pool_of(a[2], a[3], a[13], &dev);
+  const int64_t d = cache.head_dim;
+  const at::Tensor& q = needed(a[0], "q", dev);
+  const int64_t q_stride = token_rows(q, "q", -1, d);
+  const int64_t tokens = q.size(0), hq = q.size(1);
+  if (tokens > 0x7fffffff || hq > 0x7fffffff) value_error("q is too large");
+  int32_t batch, blocks;
+  const int32_t* tables = tables_of(needed(a[4], "block_tables", dev), &batch, &blocks);
+  const int32_t* lens =
+      vector<const int32_t>(&needed(a[5], "context_lens", dev), "context_lens", at::kInt, batch);
+  const int32_t* indptr =
+      vector<const int32_t>(&needed(a[1], "q_indptr", dev), "q_indptr", at::kInt, static_cast<int64_t>(batch) + 1);
+  const int64_t most = static_cast<int64_t>(blocks) * cache.block_size;
+  const int32_t max_len =
+      a[14] == Py_None ? static_cast<int32_t>(std::min<int64_t>(most, INT32_MAX)) : int32(a[14], "max_context_len");
+  const float scale = number(a[6], "softmax_scale");
+  const pkv_diff_desc f = diff_of(a[7], a[9], a[10], a[11], tokens, hq / 2, d, dev);
+  at::Tensor out = diff_out(a[8], tokens, hq / 2, d, false, dev);
+  const int32_t t32 = static_cast<int32_t>(tokens), hq32 = static_cast<int32_t>(hq);
+  const int32_t causal = truth(a[12], "causal");
+  const Workspace ws(a[15],
+                     batch > 0 && tokens > 0
+                         ? pkv_diff_prefill_workspace_size(batch, t32, hq32, cache.num_kv_heads, cache.head_dim, max_len)
+                         : 0,
+                     dev);
+  void *const qp = q.data_ptr(), *const op = out.data_ptr();
+  pkv_status st;
+  const pkv_stream_t stream = current_stream(dev);
+  Py_BEGIN_ALLOW_THREADS;
+  st = pkv_paged_diff_prefill_attention(&cache, qp, q_stride, indptr, t32, tables, blocks, lens, batch, hq32, max_len,
+                                        causal, scale, &f, op, ws.at, ws.bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return st == PKV_OK ? THPVariable_Wrap(std::move(out)) : PyLong_FromLong(st);
+}
+
+// q [B, Hq, d], contiguous, and what goes with it
+struct DiffStep {
+  const void* q;
+  int32_t batch, hq, blocks, max_len;
+  const int32_t *tables, *lens;
+  DiffStep(PyObject* qo, PyObject* to, PyObject* lo, PyObject* max, const pkv_cache_desc& cache, int64_t dev) {
+    const at::Tensor& t = needed(qo, "q", dev);
+    token_rows(t, "q", -1, cache.head_dim);
+    if (!t.is_contiguous()) value_error("q must be contiguous");
+    if (t.size(1) > 0x7fffffff) value_error("q is too large");
+    tables = tables_of(needed(to, "block_tables", dev), &batch, &blocks);
+    if (t.size(0) != batch) value_error("block_tables must have a row for every row of q");
+    lens = vector<const int32_t>(&needed(lo, "context_lens", dev), "context_lens", at::kInt, batch);
+    hq = static_cast<int32_t>(t.size(1));
+    q = t.data_ptr();
+    const int64_t most = static_cast<int64_t>(blocks) * cache.block_size;
+    max_len = max == Py_None ? static_cast<int32_t>(std::min<int64_t>(most, INT32_MAX)) : int32(max, "max_context_len");
+  }
+};
+
+// q, k_cache, v_cache, block_tables, context_lens, softmax_scale, lam, out, norm_weight, eps, out_scale, scales,
+// max_context_len, workspace
+PyObject* diff_decode(PyObject* const* a) {
+  int64_t dev;
+  const pkv_cache_desc cache = pool_of(a[1], a[2], a[11], &dev);
+  const int64_t d = cache.head_dim;
+  const DiffStep s(a[0], a[3], a[4], a[12], cache, dev);
+  const float scale = number(a[5], "softmax_scale");
+  const pkv_diff_desc f = diff_of(a[6], a[8], a[9], a[10], s.batch, s.hq / 2, d, dev);
+  at::Tensor out = diff_out(a[7], s.batch, s.hq / 2, d, true, dev);
+  const Workspace ws(
+      a[13],
+      s.batch > 0 ? pkv_diff_decode_workspace_size(s.batch, s.hq, cache.num_kv_heads, cache.head_dim, s.max_len) : 0, dev);
+  void* const op = out.data_ptr();
+  const pkv_out_dtype type = out.scalar_type() == at::kFloat ? PKV_OUT_FP32 : PKV_OUT_BF16;
+  pkv_status st;
+  const pkv_stream_t stream = current_stream(dev);
+  Py_BEGIN_ALLOW_THREADS;
+  st = pkv_paged_diff_decode_attention(&cache, s.q, s.tables, s.blocks, s.lens, s.batch, s.hq, s.max_len, scale, &f, op,
+                                       type, ws.at, ws.bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return st == PKV_OK ? THPVariable_Wrap(std::move(out)) : PyLong_FromLong(st);
+}
+
+// q, k_cache, v_cache, prefix_tables, prefix_lens, member_indptr, member_seqs, seq_prefix, block_tables, context_lens,
+// softmax_scale, lam, out, norm_weight, eps, out_scale, max_members, max_prefix_len, max_context_len, scales, workspace
+PyObject* diff_cascade(PyObject* const* a) {
+  int64_t dev;
+  const pkv_cache_desc cache = pool_of(a[1], a[2], a[19], &dev);
+  const int64_t d = cache.head_dim;
+  const DiffStep s(a[0], a[8], a[9], a[18], cache, dev);
+  pkv_prefix_desc x{};
+  x.prefix_tables = tables_of(needed(a[3], "prefix_tables", dev), &x.num_prefixes, &x.max_prefix_blocks);
+  x.prefix_lens = vector<const int32_t>(&needed(a[4], "prefix_lens", dev), "prefix_lens", at::kInt, x.num_prefixes);
+  x.member_indptr = vector<const int32_t>(&needed(a[5], "member_indptr", dev), "member_indptr", at::kInt,
+                                          static_cast<int64_t>(x.num_prefixes) + 1);
+  const at::Tensor& seqs = needed(a[6], "member_seqs", dev);
+  x.member_seqs = vector<const int32_t>(&seqs, "member_seqs", at::kInt, seqs.dim() == 1 ? seqs.size(0) : 0);
+  x.seq_prefix = vector<const int32_t>(&needed(a[7], "seq_prefix", dev), "seq_prefix", at::kInt, s.batch);
+  x.max_members = seqs.numel() > 0 ? int32(a[16], "max_members") : 0;
+  const int64_t most = static_cast<int64_t>(x.max_prefix_blocks) * cache.block_size;
+  x.max_prefix_len =
+      a[17] == Py_None ? static_cast<int32_t>(std::min<int64_t>(most, INT32_MAX)) : int32(a[17], "max_prefix_len");
+  const float scale = number(a[10], "softmax_scale");
+  const pkv_diff_desc f = diff_of(a[11], a[13], a[14], a[15], s.batch, s.hq / 2, d, dev);
+  at::Tensor out = diff_out(a[12], s.batch, s.hq / 2, d, true, dev);
+  const Workspace ws(a[20],
+                     s.batch > 0 ? pkv_cascade_diff_workspace_size(s.batch, s.hq, cache.num_kv_heads, cache.head_dim,
+                                                                   s.max_len, x.num_prefixes, x.max_members,
+                                                                   x.max_prefix_len)
+                                 : 0,
+                     dev);
+  void* const op = out.data_ptr();
+  const pkv_out_dtype type = out.scalar_type() == at::kFloat ? PKV_OUT_FP32 : PKV_OUT_BF16;
+  pkv_status st;
+  const pkv_stream_t stream = current_stream(dev);
+  Py_BEGIN_ALLOW_THREADS;
+  st = pkv_cascade_diff_decode_attention(&cache, s.q, &x, s.tables, s.blocks, s.lens, s.batch, s.hq, s.max_len, scale,
+                                         &f, op, type, ws.at, ws.bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return st == PKV_OK ? THPVariable_Wrap(std::move(out)) : PyLong_FromLong(st);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -301,7 +473,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<append, 15>("append"), method<prefill, 13>("prefill"), method<gather, 8>("gather"),
-                         {nullptr, nullptr, 0, nullptr}};
+                         method<diff_prefill, 16>("diff_prefill"), method<diff_decode, 14>("diff_decode"),
+                         method<diff_cascade, 21>("diff_cascade"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_prompt", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
