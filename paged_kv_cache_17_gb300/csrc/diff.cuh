@@ -32,6 +32,13 @@ struct DiffParams {
   const int32_t* prefix_lens;
   const int32_t* seq_prefix;
   int max_prefix_blocks, max_prefix_len, num_prefixes;
+  // partial records, where a row's keys are split: of (slot, map, row, head) at index
+  // ((slot * 2 + map) * rows + row) * heads + head; a shared prefix's slots first, then the row's own
+  float2* part_ml;   // reference maximum (log2 units) and sum
+  float* part_acc;   // [128], unnormalised, without V's scale
+  int pre_slots;     // slots of a shared prefix (0: none)
+  int split_blocks;  // 16-token blocks of one of a row's own slots
+  int max_splits;    // own slots
   int batch, rows;
   int heads, pairs, group;  // output heads, pairs of kv heads, heads / pairs
   int max_blocks, num_blocks, max_context_len;
@@ -39,6 +46,11 @@ struct DiffParams {
   float score_scale;        // softmax_scale * log2(e)
   float eps, out_scale;
 };
+
+// One token per sequence on mma.sync, and the merge of records that follows where there are any
+cudaError_t launch_diff_decode(bool fp8, const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p,
+                               cudaStream_t stream);
+cudaError_t launch_diff_merge(bool fp8, const DiffParams& p, cudaStream_t stream);
 
 cudaError_t launch_diff_simple(bool fp8, const DiffParams& p, const void* k, const void* v, cudaStream_t stream);
 

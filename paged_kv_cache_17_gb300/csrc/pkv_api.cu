@@ -1340,6 +1340,59 @@ pkv::DiffParams diff_params(const pkv_cache_desc* cache, const pkv_diff_desc* f,
   return p;
 }
 
+// Records of split contexts and shared prefixes: (m, l), then the outputs, of both maps
+struct DiffPlan {
+  Split split;
+  int pre_slots;
+  size_t ml_bytes, ws_bytes;
+};
+
+void size_records(DiffPlan* d, int64_t rows, int64_t heads) {
+  if (d->split.max_splits <= 1 && d->pre_slots == 0) return;
+  const size_t records = static_cast<size_t>(d->pre_slots + d->split.max_splits) * 2 * rows * heads;
+  d->ml_bytes = round256(records * 2 * sizeof(float));
+  d->ws_bytes = d->ml_bytes + round256(records * pkv::kDiffW * sizeof(float));
+}
+
+DiffPlan plan_diff_decode(int batch, int hq, int hkv, int max_context_len, int sm_count) {
+  DiffPlan d{};
+  d.split = choose_split(batch, hkv / 2, max_context_len, sm_count);
+  const int blocks = (max_context_len + 15) / 16;
+  while (d.split.max_splits > 65535) {  // the grid
+    d.split.split_blocks *= 2;
+    d.split.max_splits = (blocks + d.split.split_blocks - 1) / d.split.split_blocks;
+  }
+  size_records(&d, batch, hq / 2);
+  return d;
+}
+
+pkv_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return PKV_OK;
+  if (!workspace) return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes required", need);
+  if (!aligned(workspace, 256)) return fail(PKV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (bytes < need) return fail(PKV_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", bytes, need);
+  return PKV_OK;
+}
+
+void set_records(pkv::DiffParams* p, const DiffPlan& d, void* workspace) {
+  p->pre_slots = d.pre_slots;
+  p->split_blocks = d.split.split_blocks;
+  p->max_splits = d.split.max_splits;
+  if (d.ws_bytes > 0) {
+    p->part_ml = static_cast<float2*>(workspace);
+    p->part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.ml_bytes);
+  }
+}
+
+// the pool as the kernels of one token see it: a pair of heads of 64 as one of 128
+bool encode_pairs(CUtensorMap* tk, CUtensorMap* tv, const pkv_cache_desc* c) {
+  const int pairs = c->num_kv_heads / 2, w = pkv::kDiffW;
+  return c->kv_dtype == PKV_KV_FP8_E4M3 ? encode_kv_map_e4m3_swz(tk, c->k_cache, c->num_blocks, pairs, w) &&
+                                              encode_kv_map_e4m3_swz(tv, c->v_cache, c->num_blocks, pairs, w)
+                                        : encode_kv_map_groups(tk, c->k_cache, c->num_blocks, pairs, w) &&
+                                              encode_kv_map_groups(tv, c->v_cache, c->num_blocks, pairs, w);
+}
+
 // checks shared by the two calls of one token per sequence
 pkv_status check_diff_decode(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
                              int32_t max_blocks, const int32_t* context_lens, int32_t batch, int32_t hq,
@@ -1419,7 +1472,9 @@ size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_
   if (check_prefill_sizes(batch, batch, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
       check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
     return 0;
-  return 0;
+  DeviceInfo* dev = nullptr;
+  if (batch == 0 || device_info(&dev) != PKV_OK) return 0;
+  return plan_diff_decode(batch, num_q_heads, num_kv_heads, max_context_len, dev->sm_count).ws_bytes;
 }
 
 pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
@@ -1439,12 +1494,22 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
     return st;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
-  const pkv::DiffParams p =
+  const DiffPlan plan = plan_diff_decode(batch, num_q_heads, hkv, max_context_len, dev->sm_count);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) != PKV_OK) return st;
+  pkv::DiffParams p =
       diff_params(cache, diff, q, static_cast<int64_t>(num_q_heads) * d, block_tables, max_blocks_per_seq, context_lens,
                   batch, batch, num_q_heads, max_context_len, softmax_scale, out, out_dtype == PKV_OUT_FP32, dev);
-  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
-                                                reinterpret_cast<cudaStream_t>(stream));
+  set_records(&p, plan, workspace);
+  CUtensorMap tk, tv;
+  if (!encode_pairs(&tk, &tv, cache)) return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
+  const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+  if (p.max_splits > 1) {
+    e = pkv::launch_diff_merge(fp8, p, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "differential merge launch");
+  }
   return PKV_OK;
 }
 
