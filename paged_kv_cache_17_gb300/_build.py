@@ -27,7 +27,7 @@ SOURCES = ["pkv_api.cu", "append.cu", "decode_bf16.cu", "decode_e4m3.cu", "pkv_n
            "block_manager.cpp", "cascade_bf16.cu", "cascade_e4m3.cu",
            "decode_mma.cu", "decode_mma_e4m3.cu",
            "merge_partitions.cu", "cascade_prefix_tc.cu", "cascade_prefix_mma.cu", "kv_checksum.cu", "stage_copy.cu",
-           "qk_rope_append.cu", "prefill_tc.cu", "merge_prefill.cu", "kv_gather.cu", "diff_simple.cu", "diff_decode.cu",
+           "qk_rope_append.cu", "prefill_tc.cu", "merge_prefill.cu", "kv_gather.cu", "diff_chunk.cu", "diff_decode.cu",
            "diff_merge.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

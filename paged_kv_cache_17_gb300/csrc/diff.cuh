@@ -27,11 +27,7 @@ struct DiffParams {
   const uint16_t* norm_weight;  // [128] bf16, or NULL
   void* out;                // [rows][heads][128]
   uint32_t* status;
-  // shared prefixes (cascade): sequence b's keys are those of prefix seq_prefix[b], then its own
-  const int32_t* prefix_tables;
-  const int32_t* prefix_lens;
-  const int32_t* seq_prefix;
-  int max_prefix_blocks, max_prefix_len, num_prefixes;
+  const int32_t* seq_prefix;  // shared prefixes: >= 0 for the sequences that have one, or NULL
   // partial records, where a row's keys are split: of (slot, map, row, head) at index
   // ((slot * 2 + map) * rows + row) * heads + head; a shared prefix's slots first, then the row's own
   float2* part_ml;   // reference maximum (log2 units) and sum
@@ -44,6 +40,14 @@ struct DiffParams {
   int max_blocks, num_blocks, max_context_len;
   int causal, out_fp32;
   float score_scale;        // softmax_scale * log2(e)
+  // chunks and prefix passes (diff_chunk.cu)
+  const int32_t* member_seqs;  // prefix pass: rows of the members, q_indptr their ranges; max_members of one prefix
+  int max_members;
+  int split_tiles;          // 128-key steps of a slot
+  int negate;               // softmax_scale is negative
+  float score_size;         // |softmax_scale| * log2(e), positive
+  int wait_tries;           // of a wait for work or scores: kPrefillWaitTries, or fewer (tests)
+  long long test_post_delay_cycles;  // tests: the loading warp holds every work back so long
   float eps, out_scale;
 };
 
@@ -52,6 +56,11 @@ cudaError_t launch_diff_decode(bool fp8, const CUtensorMap& tk, const CUtensorMa
                                cudaStream_t stream);
 cudaError_t launch_diff_merge(bool fp8, const DiffParams& p, cudaStream_t stream);
 
-cudaError_t launch_diff_simple(bool fp8, const DiffParams& p, const void* k, const void* v, cudaStream_t stream);
+// Chunks (rows ended, or records where contexts are split) and prefix passes (records) on tcgen05; prefix passes
+// take their tables, lengths, ranges and sequences' count from p's q_indptr, block_tables, context_lens and batch
+enum DiffForm { kDiffChunk, kDiffChunkSplit, kDiffPrefix };
+cudaError_t launch_diff_chunk(bool fp8, DiffForm form, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const DiffParams& p, int tile_slots, int splits,
+                              cudaStream_t stream);
 
 }  // namespace pkv

@@ -1335,6 +1335,9 @@ pkv::DiffParams diff_params(const pkv_cache_desc* cache, const pkv_diff_desc* f,
   p.max_context_len = max_context_len;
   p.out_fp32 = out_fp32;
   p.score_scale = softmax_scale * 1.4426950408889634f;  // log2(e)
+  p.negate = softmax_scale < 0.f;
+  // a zero scale becomes a factor that leaves every score at 0 while masked ones stay -inf
+  p.score_size = std::max(std::fabs(softmax_scale) * 1.4426950408889634f, 1e-37f);
   p.eps = f->eps;
   p.out_scale = f->out_scale;
   return p;
@@ -1354,8 +1357,9 @@ void size_records(DiffPlan* d, int64_t rows, int64_t heads) {
   d->ws_bytes = d->ml_bytes + round256(records * pkv::kDiffW * sizeof(float));
 }
 
-DiffPlan plan_diff_decode(int batch, int hq, int hkv, int max_context_len, int sm_count) {
+DiffPlan plan_diff_decode(int batch, int hq, int hkv, int max_context_len, int pre_slots, int sm_count) {
   DiffPlan d{};
+  d.pre_slots = pre_slots;
   d.split = choose_split(batch, hkv / 2, max_context_len, sm_count);
   const int blocks = (max_context_len + 15) / 16;
   while (d.split.max_splits > 65535) {  // the grid
@@ -1381,6 +1385,118 @@ void set_records(pkv::DiffParams* p, const DiffPlan& d, void* workspace) {
   if (d.ws_bytes > 0) {
     p->part_ml = static_cast<float2*>(workspace);
     p->part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.ml_bytes);
+  }
+}
+
+// How the tiles of 128 rows (tokens x the heads of a group) and their contexts are laid out over the SMs, one CTA
+// each: `works` tiles' works over `steps` 128-key steps of step_us each, cut into n runs.  CTAs take works as they
+// finish, so the time is modelled as the larger of one work's and an SM's share of all of them plus half a work for
+// the uneven end; records, their writing and reading and the merge on top.  At most `most` steps a run: the tensor
+// cores add to an accumulator by truncation, up to 2^-23 of the sum for each of a step's 8 additions, all towards
+// zero.  PKV_SPLIT_TOKENS fixes the run.
+struct DiffRuns {
+  int splits, split_tiles;
+};
+
+constexpr double kDiffWorkUs = 3.0;  // a work's start and end
+
+DiffRuns plan_diff_runs(long long works, int steps, int most, double step_us, double record_us, double merge_us,
+                        long long max_splits, int forced, int sm_count) {
+  most = std::min(most, steps);
+  if (forced > 0) {
+    forced = std::min(forced, most);
+    return DiffRuns{(steps + forced - 1) / forced, forced};
+  }
+  DiffRuns r{1, steps};
+  double best = -1;
+  const int least = (steps + most - 1) / most;
+  for (int n = least; n <= std::max<long long>(least, std::min<long long>(steps, max_splits)); ++n) {
+    const int run = (steps + n - 1) / n;
+    if ((steps + run - 1) / run != n) continue;  // the same runs as a smaller count
+    const double one = run * step_us + kDiffWorkUs, share = static_cast<double>(works) * n / sm_count;
+    double us = std::max(one, share * one + run * step_us / 2);
+    if (n > 1) us += merge_us + record_us * n;
+    if (best < 0 || us < best) {
+      best = us;
+      r = DiffRuns{n, run};
+    }
+  }
+  return r;
+}
+
+int forced_steps(const char* name, int tokens) {
+  if (const char* env = std::getenv(name)) {
+    const long v = std::strtol(env, nullptr, 10);
+    if (v * tokens >= 16) return static_cast<int>(std::min<long>((v * tokens + 127) / 128, 1 << 23));
+  }
+  return 0;
+}
+
+struct DiffChunkPlan {
+  int tile_slots;
+  DiffRuns runs;
+  DiffPlan records;
+};
+
+DiffChunkPlan plan_diff_chunk(int batch, int total_q, int hq, int hkv, bool fp8, int max_context_len, int sm_count) {
+  DiffChunkPlan c{};
+  const int heads = hq / 2, pairs = hkv / 2, tok = 128 / (hq / hkv);
+  const long long seqs = std::min(batch, total_q);
+  c.tile_slots = static_cast<int>((total_q + seqs * (tok - 1)) / tok);
+  const long long tiles = std::max<long long>(seqs, (total_q + tok - 1) / tok);
+  // K and V of a step are 64 KiB (E4M3: 32): 1.5 us of an SM's share of the memory, by as many tiles as share them
+  const double step_us = std::max(1.0, (fp8 ? 0.75 : 1.5) * static_cast<double>(seqs) / tiles);
+  const double record_us = 2.0 * total_q * heads * 2 * (pkv::kDiffW + 2) * 4 / kPrefillRecordBytesPerUs;
+  c.runs = plan_diff_runs(tiles * pairs, std::max(1, (max_context_len + 127) / 128), pkv::kPrefillMaxRun, step_us,
+                          record_us, kPrefillMergeUs, 48, forced_steps("PKV_SPLIT_TOKENS", 1), sm_count);
+  c.records.split.max_splits = c.runs.splits;
+  size_records(&c.records, total_q, heads);
+  return c;
+}
+
+// Shared prefixes: a prefix's members are the rows of its tiles.  The softmax weights enter in two terms, so a step's
+// products take 2560 cycles.  At most 64 steps a run (8192 keys), so that truncated sums stay within 2^-14.
+constexpr double kDiffPrefixStepUs = 1.5;
+constexpr int kDiffPrefixMaxRun = 64;
+
+struct DiffPrefixPlan {
+  int tile_slots;
+  DiffRuns runs;
+};
+
+DiffPrefixPlan plan_diff_prefix(int batch, int num_prefixes, int max_members, int hq, int hkv, int max_prefix_len,
+                                int sm_count) {
+  const int tok = 128 / (hq / hkv);
+  const long long per = (static_cast<long long>(max_members) + tok - 1) / tok;
+  // every sequence has one prefix at most
+  const long long slots = std::min(per * num_prefixes, (batch + static_cast<long long>(num_prefixes) * (tok - 1)) / tok);
+  DiffPrefixPlan x{static_cast<int>(std::min<long long>(slots, 0x7fffffff)), {}};
+  const double record_us = 2.0 * batch * (hq / 2) * 2 * (pkv::kDiffW + 2) * 4 / kPrefillRecordBytesPerUs;
+  x.runs = plan_diff_runs(slots * (hkv / 2), (max_prefix_len + 127) / 128, kDiffPrefixMaxRun, kDiffPrefixStepUs, record_us,
+                          0.0, 16, forced_steps("PKV_PREFIX_SPLIT_BLOCKS", 16), sm_count);
+  return x;
+}
+
+// the pool as the chunk kernel sees it: bf16 a box per block; E4M3 K rows swizzled for the tensor cores, V rows as
+// they are (its expansion reads them)
+bool encode_pairs_chunk(CUtensorMap* tk, CUtensorMap* tv, const pkv_cache_desc* c) {
+  const int pairs = c->num_kv_heads / 2, w = pkv::kDiffW;
+  return c->kv_dtype == PKV_KV_FP8_E4M3 ? encode_kv_map_e4m3_swz(tk, c->k_cache, c->num_blocks, pairs, w) &&
+                                              encode_kv_map(tv, c->v_cache, c->num_blocks, pairs, w, true)
+                                        : encode_kv_map_groups(tk, c->k_cache, c->num_blocks, pairs, w) &&
+                                              encode_kv_map_groups(tv, c->v_cache, c->num_blocks, pairs, w);
+}
+
+// tests only: waits for work and scores that run out (fewer tries, works held back)
+void set_waits(pkv::DiffParams* p) {
+  p->wait_tries = pkv::kPrefillWaitTries;
+  if (const char* env = std::getenv("PKV_TEST_PREFILL_WAIT_TRIES")) {
+    const long v = std::strtol(env, nullptr, 10);
+    if (v > 0) p->wait_tries = static_cast<int>(std::min<long>(v, pkv::kPrefillWaitTries));
+  }
+  if (const char* env = std::getenv("PKV_TEST_PREFILL_POST_DELAY_CYCLES")) {
+    const long long v = std::strtoll(env, nullptr, 10);
+    p->test_post_delay_cycles = v > 0 ? std::min(v, 100000000LL) : 0;  // at most about 50 ms
   }
 }
 
@@ -1424,7 +1540,14 @@ size_t pkv_diff_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t n
   if (check_prefill_sizes(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
       check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
     return 0;
-  return 0;
+  DeviceInfo* dev = nullptr;
+  if (batch == 0 || total_q == 0 || device_info(&dev) != PKV_OK) return 0;
+  // (the runs' lengths differ between the pool types: room for either)
+  size_t most = 0;
+  for (const bool fp8 : {false, true})
+    most = std::max(most, plan_diff_chunk(batch, total_q, num_q_heads, num_kv_heads, fp8, max_context_len, dev->sm_count)
+                              .records.ws_bytes);
+  return most;
 }
 
 pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const void* q, int64_t q_stride,
@@ -1456,13 +1579,30 @@ pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const v
     return st;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
+  const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
+  const DiffChunkPlan plan = plan_diff_chunk(batch, total_q, num_q_heads, hkv, fp8, max_context_len, dev->sm_count);
+  if (plan.runs.splits > 65535) return fail(PKV_ERR_UNSUPPORTED, "context too long for the partition grid");
+  if ((st = check_workspace(workspace, workspace_bytes, plan.records.ws_bytes)) != PKV_OK) return st;
   pkv::DiffParams p = diff_params(cache, diff, q, q_stride, block_tables, max_blocks_per_seq, context_lens, batch,
                                   total_q, num_q_heads, max_context_len, softmax_scale, out, false, dev);
+  set_records(&p, plan.records, workspace);
+  set_waits(&p);
   p.q_indptr = q_indptr;
   p.causal = causal;
-  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
-                                                reinterpret_cast<cudaStream_t>(stream));
+  p.split_tiles = plan.runs.split_tiles;
+  CUtensorMap tq{}, tk, tv;
+  if (!(fp8 || encode_q_map(&tq, q, q_stride, total_q, p.heads, p.group, pkv::kDiffW)) ||
+      !encode_pairs_chunk(&tk, &tv, cache))
+    return fail(PKV_ERR_INVALID_ARG, "cannot describe q or the KV pool as a TMA tensor map");
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool records = plan.runs.splits > 1;
+  cudaError_t e = pkv::launch_diff_chunk(fp8, records ? pkv::kDiffChunkSplit : pkv::kDiffChunk, tq, tk, tv, p,
+                                         plan.tile_slots, plan.runs.splits, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+  if (records) {
+    e = pkv::launch_diff_merge(fp8, p, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "differential merge launch");
+  }
   return PKV_OK;
 }
 
@@ -1474,7 +1614,7 @@ size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_
     return 0;
   DeviceInfo* dev = nullptr;
   if (batch == 0 || device_info(&dev) != PKV_OK) return 0;
-  return plan_diff_decode(batch, num_q_heads, num_kv_heads, max_context_len, dev->sm_count).ws_bytes;
+  return plan_diff_decode(batch, num_q_heads, num_kv_heads, max_context_len, 0, dev->sm_count).ws_bytes;
 }
 
 pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const int32_t* block_tables,
@@ -1494,7 +1634,7 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
     return st;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
-  const DiffPlan plan = plan_diff_decode(batch, num_q_heads, hkv, max_context_len, dev->sm_count);
+  const DiffPlan plan = plan_diff_decode(batch, num_q_heads, hkv, max_context_len, 0, dev->sm_count);
   if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) != PKV_OK) return st;
   pkv::DiffParams p =
       diff_params(cache, diff, q, static_cast<int64_t>(num_q_heads) * d, block_tables, max_blocks_per_seq, context_lens,
@@ -1524,7 +1664,13 @@ size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32
   if (check_prefill_sizes(batch, batch, num_q_heads, num_kv_heads, head_dim, max_context_len) != PKV_OK ||
       check_diff_heads(num_q_heads, num_kv_heads, head_dim) != PKV_OK)
     return 0;
-  return 0;
+  DeviceInfo* dev = nullptr;
+  if (batch == 0 || device_info(&dev) != PKV_OK) return 0;
+  if (num_prefixes == 0 || max_members == 0 || max_prefix_len == 0)
+    return plan_diff_decode(batch, num_q_heads, num_kv_heads, max_context_len, 0, dev->sm_count).ws_bytes;
+  const DiffPrefixPlan x = plan_diff_prefix(batch, num_prefixes, max_members, num_q_heads, num_kv_heads, max_prefix_len,
+                                            dev->sm_count);
+  return plan_diff_decode(batch, num_q_heads, num_kv_heads, max_context_len, x.runs.splits, dev->sm_count).ws_bytes;
 }
 
 pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const void* q, const pkv_prefix_desc* px,
@@ -1561,18 +1707,40 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
     return st;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PKV_OK) return st;
+  const DiffPrefixPlan x = plan_diff_prefix(batch, px->num_prefixes, px->max_members, num_q_heads, hkv,
+                                            px->max_prefix_len, dev->sm_count);
+  if (static_cast<long long>(x.tile_slots) * (hkv / 2) > 0x7fffffffLL || x.runs.splits > 65535)
+    return fail(PKV_ERR_UNSUPPORTED, "too many prefixes for the prefix-pass grid");
+  const DiffPlan plan = plan_diff_decode(batch, num_q_heads, hkv, max_context_len, x.runs.splits, dev->sm_count);
+  if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) != PKV_OK) return st;
   pkv::DiffParams p =
       diff_params(cache, diff, q, static_cast<int64_t>(num_q_heads) * d, block_tables, max_blocks_per_seq, context_lens,
                   batch, batch, num_q_heads, max_context_len, softmax_scale, out, out_dtype == PKV_OUT_FP32, dev);
-  p.prefix_tables = px->prefix_tables;
-  p.prefix_lens = px->prefix_lens;
+  set_records(&p, plan, workspace);
   p.seq_prefix = px->seq_prefix;
-  p.max_prefix_blocks = px->max_prefix_blocks;
-  p.max_prefix_len = px->max_prefix_len;
-  p.num_prefixes = px->num_prefixes;
-  const cudaError_t e = pkv::launch_diff_simple(cache->kv_dtype == PKV_KV_FP8_E4M3, p, cache->k_cache, cache->v_cache,
-                                                reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "differential cascade launch");
+  // the prefix pass: the members of a prefix are rows over its tables
+  pkv::DiffParams pass = p;
+  set_waits(&pass);
+  pass.q_indptr = px->member_indptr;
+  pass.member_seqs = px->member_seqs;
+  pass.max_members = px->max_members;
+  pass.block_tables = px->prefix_tables;
+  pass.max_blocks = px->max_prefix_blocks;
+  pass.context_lens = px->prefix_lens;
+  pass.max_context_len = px->max_prefix_len;
+  pass.batch = px->num_prefixes;
+  pass.split_tiles = x.runs.split_tiles;
+  CUtensorMap none{}, ck, cv, tk, tv;
+  if (!encode_pairs_chunk(&ck, &cv, cache) || !encode_pairs(&tk, &tv, cache))
+    return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
+  const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = pkv::launch_diff_chunk(fp8, pkv::kDiffPrefix, none, ck, cv, pass, x.tile_slots, x.runs.splits, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "differential prefix-pass launch");
+  e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+  e = pkv::launch_diff_merge(fp8, p, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "differential merge launch");
   return PKV_OK;
 }
 
