@@ -17,13 +17,12 @@
 // holds both maps' halves side by side, V's tile is the pair's value; each is loaded once for both maps.  The two
 // softmax groups are the two maps of the same rows: while one map's softmax runs, the tensor cores work on the
 // other's products.  So a row's two outputs lie in the same tensor-memory lane, and its end needs no more
-// than two exchanges between two threads.  Scores and weights go by half steps of 64 keys, in two buffers a map:
-// the scores of the half step after the next follow P V in its buffer, and a map's softmax finds the next ones
-// done.
+// than two exchanges between two threads.
 //
 //   warps 0-3, 4-7  softmax of map 0 and 1: thread r owns row r (TMEM lane r): scores in, weights out over them as
 //                   16-bit pairs, rare rescale of the output, epilogue (each group 64 columns of both outputs)
-//   warps 8, 10     issue the MMAs of map 0 and 1: per half step P V, then the scores two half steps on
+//   warps 8, 10     issue the MMAs of map 0 and 1, in turns: per step P V, then the next scores (one warp for both
+//                   took 1.4 times as long to issue as the tensor cores to execute)
 //   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block at a time
 //   warp 11         looks for bad ranges
 //   warps 12-15     V: zero the rows past the context in the last tile, so that what a page holds there (NaN
@@ -35,7 +34,7 @@
 // the last.
 //
 // Shared memory: Q (both halves; E4M3 hi and lo), a ring of K and V tiles in the order K0 K1 V0 K2 V1 .., E4M3 two
-// fp16 V tiles.  TMEM (512 columns): scores, then weights, of map m at 128 m and 128 m + 64; outputs at 256 + 128 m.
+// fp16 V tiles.  TMEM (512 columns): scores, then weights, of map m at 128 m; outputs at 256 + 128 m.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -90,10 +89,10 @@ namespace {
 // barriers and small shared state, at kOffBar
 struct DiffShared {
   uint64_t full[6], empty[6];  // ring: tile landed, tile consumed
-  uint64_t s_full[2][2];       // [map][buffer] scores of a half step done
-  uint64_t p_full[2][2];       // its weights written, the output rescaled (an arrival per warp)
-  uint64_t pv_done[2];         // products of a map's half step with V done (one phase is told from the one before
-                               // where the one before that is known to be over: at a half step's scores)
+  uint64_t s_full[2];          // scores of a step done (and every product issued before)
+  uint64_t p_half[2];          // weights of a step's first 64 keys written, the output rescaled (an arrival per warp),
+                               // and the other map's turn over
+  uint64_t p_full[2];          // all weights of a step written (an arrival per warp)
   uint64_t o_full[2];          // every product of the map's work done
   uint64_t fixed[8];           // bf16: V tile of a cut step fixed; E4M3 (two in use): V tile expanded
   uint64_t exp_free[2];        // E4M3: expanded V tile consumed
@@ -123,7 +122,6 @@ struct DiffWork {
 
 struct DiffSteps {
   int k0, nstep;  // first 128-key step, steps
-  int nhalf;      // half steps of 64 keys
   int lim_min;    // keys that every row sees
   int first_cut;  // first step whose V needs care: some row does not see all of its keys
   __device__ __forceinline__ static int lim(const DiffWork& w, const DiffParams& p, int i) {
@@ -131,14 +129,10 @@ struct DiffSteps {
   }
   __device__ __forceinline__ DiffSteps(const DiffWork& w, const DiffParams& p) {
     k0 = w.split * p.split_tiles;
-    const int keys = min(lim(w, p, w.ntok - 1) - k0 * 128, p.split_tiles * 128);
-    nhalf = (max(0, keys) + 63) / 64;
-    nstep = (nhalf + 1) / 2;
+    nstep = max(0, min((lim(w, p, w.ntok - 1) + 127) / 128, k0 + p.split_tiles) - k0);
     lim_min = lim(w, p, 0);
     first_cut = max(0, min(nstep, lim_min / 128 - k0));
   }
-  // half steps that go through buffer b
-  __device__ __forceinline__ int through(int b) const { return (nhalf + 1 - b) / 2; }
   // position of V of step j in the ring's order K0 K1 V0 K2 V1 ..
   __device__ __forceinline__ int v_item(int j) const { return min(2 * j + 2, 2 * nstep - 1); }
 };
@@ -181,11 +175,9 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       sh.epilogues[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.s_full[i][b], 1);
-        mbar_init(&sh.p_full[i][b], 4);
-      }
-      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 5);
+      mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.exp_free[i], 2);
       mbar_init(&sh.work_full[i], 1);
@@ -240,52 +232,47 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       auto same = [](uint32_t x) { return __shfl_sync(kFull, x, 0); };  // a value of the warp
       constexpr uint32_t kIdO = idesc_f16(C::kRows, W, !FP8, true);
       // scores: A = Q with its sign turned (bit 13) for a negative scale; E4M3 formats are 0
-      const uint32_t id_s = idesc_f16(C::kRows, 64, !FP8, false) | (p.negate ? 1u << 13 : 0u);
+      const uint32_t id_s = idesc_f16(C::kRows, C::kKeys, !FP8, false) | (p.negate ? 1u << 13 : 0u);
       const uint32_t ring_lo = same(desc_lo(ring, 16)), ring_v_lo = same(desc_lo(ring, 1024));
       const uint32_t exp_v_lo = same(desc_lo(smem_u32(smem + C::kOffExp), C::kHalf16));
       // this map's half of Q's and K's columns
       const uint32_t q_lo = same(desc_lo(q_base, 16) + g * (FP8 ? 64 : C::kHalf16) / 16);
-      const uint32_t k_half = same(g * (FP8 ? 64 : 1024) / 16);
+      const uint32_t k0_lo = same(ring_lo + g * (FP8 ? 64 : 1024) / 16);
       const uint32_t s_col = same(tmem + C::kColS + 128 * g), o_col = same(tmem + C::kColO + W * g);
-      // keys 64 half .. of the tile in this slot
-      auto issue_s = [&](int half, unsigned slot) {
-        const uint32_t k_lo = same(ring_lo + k_half + slot * (C::kSlot / 16) + half * (C::kSlot / 32));
-        const uint32_t d = same(s_col + 64 * half);
+      auto issue_s = [&](unsigned slot) {
+        const uint32_t k_lo = same(k0_lo + slot * (C::kSlot / 16));
         if constexpr (FP8) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              mma_ss<true>(d, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, kDescK128, kDescK128, id_s,
+              mma_ss<true>(s_col, q_lo + (part * C::kCodes + kk * 32) / 16, k_lo + kk * 2, kDescK128, kDescK128, id_s,
                            part > 0 || kk > 0, leader);
         } else {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss<false>(d, q_lo + kk * 2, k_lo + kk * 2, kDescK128, kDesc128<C::kGroup>, id_s, kk > 0, leader);
+            mma_ss<false>(s_col, q_lo + kk * 2, k_lo + kk * 2, kDescK128, kDesc128<C::kGroup>, id_s, kk > 0, leader);
         }
-        commit(&sh.s_full[g][half], leader);
+        commit(&sh.s_full[g], leader);
       };
-      auto issue_o = [&](int half, bool first, uint32_t v_lo0) {
+      // keys 64 half .. of a step
+      auto issue_o = [&](int half, bool first, uint32_t v_lo) {
         constexpr uint32_t kVGroup = FP8 ? 1024 : C::kGroup;  // eight keys
-        const uint32_t pt = same(s_col + 64 * half);
-        const uint32_t v_lo = same(v_lo0 + half * (8 * kVGroup / 16));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          mma_ts(o_col, pt + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, !first || kk > 0, leader);
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
+          mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, !first || kk > 0, leader);
           if constexpr (PREFIX)
-            mma_ts(o_col, pt + 32 + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, true, leader);
+            mma_ts(o_col, s_col + 64 + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, true, leader);
         }
-        commit(&sh.pv_done[g], leader);
       };
 
       Cursor<C::kSlots> base{0, 0};  // ring position of the work's first tile
       unsigned steps_done = 0, cuts = 0, q_count = 0;
-      unsigned c0 = 0, c1 = 0;  // half steps through the buffers so far
       bool ok = true;
       DiffWork w;
       for (unsigned n = 0; ok && next_work(n, w); ++n) {
         const DiffSteps st(w, p);
-        const int nstep = st.nstep, nhalf = st.nhalf;
+        const int nstep = st.nstep;
         if (nstep == 0) continue;
         Cursor<C::kSlots> kc = base, vc = base;
         vc.advance(nstep == 1 ? 1 : 2);
@@ -303,50 +290,50 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
             return wait(&sh.full[vc.slot], vc.phase);
           }
         };
+        // The maps take turns, so that one's products run under the other's softmax.  The fifth arrival on p_half is
+        // the other issuer's, once its turn before is over: on map 0's for a work's first step when issuer 1 is
+        // through with the work before, then after map 1's step before; on map 1's after map 0's same step.  So no
+        // arrival comes before the phase it belongs to.
+        if (g == 1 && leader) mbar_arrive(&sh.p_half[0]);
         ok = wait(&sh.q_full, q_count & 1);
         ++q_count;
         ok = ok && wait_k();
         if (!ok) break;
         tc_fence_after();
-        for (int h = 0; h < min(2, nhalf); ++h) {
-          issue_s(h, kc.slot);
-        }
+        issue_s(kc.slot);
         commit(&sh.empty[kc.slot], leader);
         if (nstep == 1) commit(&sh.q_empty, leader);
-#pragma unroll 1
-        for (int h = 0; h < nhalf; ++h) {
-          const int j = h >> 1, half = h & 1;
-          const unsigned parity = ((half ? c1 : c0) + j) & 1;
-          const bool more = h + 2 < nhalf;
-          if (half == 0) {
-            ok = wait_v(j);
-            if (more) kc.advance(j == 0 ? 1 : 2);
-            if (!FP8 && more && ok) ok = wait_k();  // before the weights, where waiting costs nothing
-            if (!ok) break;
-          }
-          const uint32_t v_lo = FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16)
-                                    : ring_v_lo + vc.slot * (C::kSlot / 16);
-          ok = wait(&sh.p_full[g][half], parity);
+        for (int j = 0; j < nstep; ++j) {
+          const bool more = j + 1 < nstep;
+          const unsigned parity = (steps_done + j) & 1;
+          ok = wait_v(j);
+          if (more) kc.advance(j == 0 ? 1 : 2);
+          if (!FP8 && more && ok) ok = wait_k();  // before the weights, where waiting costs nothing
+          if (!ok) break;
+          const uint32_t v_lo = same(FP8 ? exp_v_lo + ((steps_done + j) & 1) * (C::kTile16 / 16)
+                                         : ring_v_lo + vc.slot * (C::kSlot / 16));
+          ok = wait(&sh.p_half[g], parity);
           if (!ok) break;
           tc_fence_after();
-          issue_o(half, h == 0, v_lo);
-          if (FP8 && half == 0 && more) {  // K may come later than the weights: V's expansion holds up the ring
+          issue_o(0, j == 0, v_lo);
+          ok = wait(&sh.p_full[g], parity);
+          if (!ok) break;
+          tc_fence_after();
+          issue_o(1, false, v_lo);
+          if (FP8 && more) {  // K may come later than the weights: V's expansion holds up the ring
             ok = wait_k();
             if (!ok) break;
             tc_fence_after();
           }
-          // the scores two half steps on follow P V in the same columns, in issue order
-          if (more) issue_s(half, kc.slot);
-          if (h + 1 == nhalf) commit(&sh.o_full[g], leader);
-          if (half == 1 || h + 1 == nhalf) {
-            commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader);
-            vc.advance(j + 2 == nstep ? 1 : 2);
-          }
-          if (more && (half == 1 || h + 3 == nhalf)) commit(&sh.empty[kc.slot], leader);
-          if (h + 3 == nhalf) commit(&sh.q_empty, leader);
+          // the next scores follow P V in the same columns, in issue order
+          if (more) issue_s(kc.slot);
+          else commit(&sh.o_full[g], leader);
+          if ((g == 0 || more) && leader) mbar_arrive(&sh.p_half[g ^ 1]);
+          commit(FP8 ? &sh.exp_free[(steps_done + j) & 1] : &sh.empty[vc.slot], leader);
+          vc.advance(j + 2 == nstep ? 1 : 2);
+          if (more) commit(&sh.empty[kc.slot], leader);
+          if (j + 2 == nstep) commit(&sh.q_empty, leader);
         }
-        c0 += st.through(0);
-        c1 += st.through(1);
         base.advance_by(2 * nstep);
         steps_done += nstep;
         cuts += nstep - st.first_cut;
@@ -703,7 +690,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
     const int r = threadIdx.x & 127;   // row of the tile, TMEM lane
     const int my_i = r >> log_g;       // token within the work
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t scol0 = tmem + lane_base + C::kColS + 128 * g;
+    const uint32_t scol = tmem + lane_base + C::kColS + 128 * g;
     const uint32_t ocol = tmem + lane_base + C::kColO;  // map 0's output
     const uint32_t mine = ocol + W * g;
     float* join = reinterpret_cast<float*>(smem + C::kOffJoin);  // [factors, squares][group][row]
@@ -713,8 +700,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       __syncwarp();
       named_sync(2, 256);
     }
-    unsigned c0 = 0, c1 = 0, c_pv = 0;  // half steps so far, through the buffers and in all
-    unsigned c_o = 0;                   // works with steps so far
+    unsigned c_s = 0, c_o = 0;  // steps and works with steps so far
     bool dead = false;
     DiffWork w;
     for (unsigned n = 0; !dead; ++n) {
@@ -727,7 +713,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       }
       if (none) break;
       const DiffSteps st(w, p);
-      const int nhalf = st.nhalf;
+      const int nstep = st.nstep;
       const int head = w.h * G + (r & (G - 1));
       bool rv = my_i < w.ntok;
       int row = w.tok0 + my_i;  // of q and the output
@@ -741,7 +727,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       }
       const int64_t unit = static_cast<int64_t>(row) * p.heads + head;
       const int64_t rec = static_cast<int64_t>(w.split * 2 + g) * p.rows * p.heads + unit;
-      if (nhalf == 0) {  // rows that see nothing (of this split)
+      if (nstep == 0) {  // rows that see nothing (of this split)
         if (rv) {
           if constexpr (RECORDS) {
             p.part_ml[rec] = make_float2(-INFINITY, 0.f);
@@ -754,6 +740,9 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
         continue;
       }
       float sscale = p.score_size;
+      // lambda, asked for long before its use
+      float sign = 1.f;
+      if (!RECORDS && g == 1 && rv) sign = -__ldg(p.lambda + row * p.lambda_stride + head);
 
       if constexpr (kQByThreads) {
         // this map's half of the row of Q; the tile is free: the map's last scores of the work before are done
@@ -816,11 +805,9 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       const int warp_lim = __reduce_min_sync(kFull, rv ? my_lim : 0x7fffffff);
       const bool idle = !__any_sync(kFull, rv);  // no row of the warp exists: its products go nowhere
       float m_used = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (int h = 0; h < nhalf; ++h) {
-        const int key0 = st.k0 * C::kKeys + 64 * h, half = h & 1;
-        const uint32_t scol = scol0 + 64 * half;
-        const bool ok = wait_for(&sh.s_full[g][half], ((half ? c1 : c0) + (h >> 1)) & 1, abort, p.wait_tries);
+      for (int t = 0; t < nstep; ++t) {
+        const int key0 = (st.k0 + t) * C::kKeys;
+        const bool ok = wait_for(&sh.s_full[g], (c_s + t) & 1, abort, p.wait_tries);
         if (!__all_sync(kFull, ok)) {  // tensor-memory loads are warp-collective: leave as a warp
           if (!*abort) fail();
           dead = true;
@@ -828,14 +815,24 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
         }
         tc_fence_after();
         if (!idle) {
-          float s[64];
-          tmem_ld64(scol, s);
-          if (key0 + 64 > warp_lim) {  // keys that a row does not see
+          // keys that a row does not see: -inf over their scores, in the columns (a loop of 32: this is for a
+          // work's last steps, and straight code for 128 is slow to fetch)
+          if (key0 + C::kKeys > warp_lim) {
             const int left = my_lim - key0;
+#pragma unroll 1
+            for (int c = max(0, warp_lim - key0) & ~31; c < C::kKeys; c += 32) {
+              float x[32];
+              tmem_ld32(scol + c, x);
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= left) s[i] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (i >= left - c) x[i] = -INFINITY;
+              tmem_st32(scol + c, x);
+            }
           }
+          float s[128];
+          // (one load of 128 columns wants more registers than 512 threads start with)
+          tmem_ld64(scol, *reinterpret_cast<float(*)[64]>(s));
+          tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
           // 32 weights from their scores, as 16-bit pairs into the columns of the scores
           float2 sum[2] = {};
           uint32_t pw[16], pl[PREFIX ? 16 : 1];
@@ -853,7 +850,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
           };
           auto put = [&](int q) {
             tmem_st16u(scol + 16 * q, pw);
-            if constexpr (PREFIX) tmem_st16u(scol + 32 + 16 * q, pl);
+            if constexpr (PREFIX) tmem_st16u(scol + 64 + 16 * q, pl);
           };
           // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
           auto minus_m = [&]() { return (m_used == -INFINITY ? 0.f : -m_used) + C::kBias; };
@@ -863,12 +860,12 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
           do {
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int i = 4; i < 60; i += 8) {
+            for (int i = 4; i < 124; i += 8) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
             }
             const float top =
-                max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[60], s[61], s[61]), s[62], s[63])) * sscale;
+                max3(max3(mx[0], mx[1], mx[2]), mx[3], max3(max3(s[124], s[125], s[125]), s[126], s[127])) * sscale;
             if (!(top < INFINITY)) l = __int_as_float(0x7fffffff);  // a NaN or an infinity among the scores
             const bool grow = top > m_used + C::kLazy;
             if (!__any_sync(kFull, grow)) break;
@@ -879,14 +876,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
               m_used = top;
             }
             __syncwarp();
-            if (h > 0) {  // once P V of the half step before is done
-              const bool done = wait_for(&sh.pv_done[g], (c_pv + h - 1) & 1, abort);
-              if (!__all_sync(kFull, done)) {
-                if (!*abort) fail();
-                dead = true;
-                break;
-              }
-              tc_fence_after();
+            if (t > 0) {  // P V of the previous step was issued before these scores: it is done
 #pragma unroll 1
               for (int ch = 0; ch < W / 16; ++ch) {
                 float o[16];
@@ -899,21 +889,30 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
             sum[0] = sum[1] = make_float2(0.f, 0.f);
             weights(0, minus_m());
           } while (false);
-          if (dead) break;
+          const float negm = minus_m();
           put(0);
-          weights(1, minus_m());
+          weights(1, negm);
           put(1);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          arrive_by(&sh.p_half[g], lane == 0);
+          weights(2, negm);
+          put(2);
+          weights(3, negm);
+          put(3);
           sum[0] = fadd2(sum[0], sum[1]);
           l += sum[0].x + sum[0].y;
           tmem_wait_st();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[g]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[g][half]);
+        if (lane == 0) mbar_arrive(&sh.p_full[g]);
       }
-      c0 += st.through(0);
-      c1 += st.through(1);
-      c_pv += nhalf;
+      c_s += nstep;
 
       // ---- epilogue: the map's record, or the output row
       if (!dead) {
@@ -966,7 +965,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       } else {
         // this map's factor; then each group has both outputs' 64 columns of one value head
         float a = 0.f;  // of a row without keys
-        if (rv && (l > 0.f || l != l)) a = (g == 0 ? 1.f : -p.lambda[row * p.lambda_stride + head]) / l;
+        if (rv && (l > 0.f || l != l)) a = sign / l;
         join[g * 128 + r] = a;
         const bool empty = l == 0.f;  // (of both maps alike: they see the same keys)
         tc_fence_before();
@@ -977,25 +976,29 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
         if (!dead && !idle) {
           add_odd(0, col0, col0 + kDiffD);
           add_odd(1, col0, col0 + kDiffD);
-          float a0 = join[r], a1 = join[128 + r], square = 0.f;
+          float a0 = join[r], a1 = join[128 + r];
           if constexpr (FP8) {
             const float vs = p.scales[2 * (p.pairs + w.h) + g];
             a0 *= vs;
             a1 *= vs;
           }
+          float2 square = make_float2(0.f, 0.f);
+          const float2 f0 = make_float2(a0, a0), f1 = make_float2(a1, a1);
 #pragma unroll 1
           for (int c = col0; c < col0 + kDiffD; c += 32) {  // the difference goes over this map's columns
             float y[32], o[32];
             tmem_ld32(ocol + c, y);
             tmem_ld32(ocol + W + c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              y[i] = fmaf(y[i], a0, o[i] * a1);
-              square = fmaf(y[i], y[i], square);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 d = ffma2(make_float2(y[i], y[i + 1]), f0, fmul2(make_float2(o[i], o[i + 1]), f1));
+              square = ffma2(d, d, square);
+              y[i] = d.x;
+              y[i + 1] = d.y;
             }
             tmem_st32(mine + c, y);
           }
-          join[256 + g * 128 + r] = square;
+          join[256 + g * 128 + r] = square.x + square.y;
         }
         tc_fence_before();
         __syncwarp();
@@ -1020,24 +1023,23 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
             turn_put(mine + 16 * c, words);
           }
           tmem_wait_st();
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[16];
-            turn_get(mine + (static_cast<uint32_t>(16 * half) << 16), v);
+          uint32_t v[2][16];
+          turn_get(mine, v[0]);
+          turn_get(mine + (16u << 16), v[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int rr = (r & ~31) + 16 * half + 8 * k + (lane >> 2);
-              const int i = rr >> log_g;
-              if (i >= w.ntok) continue;
-              uint4* dst = reinterpret_cast<uint4*>(
-                               static_cast<uint16_t*>(p.out) +
-                               (static_cast<int64_t>(w.tok0 + i) * p.heads + w.h * G + (rr & (G - 1))) * W) +
-                           8 * g + (lane & 3);
-              dst[0] = make_uint4(v[k], v[2 + k], v[4 + k], v[6 + k]);
-              dst[4] = make_uint4(v[8 + k], v[10 + k], v[12 + k], v[14 + k]);
+          for (int k = 0; k < 4; ++k) {
+            const int rr = (r & ~31) + 8 * k + (lane >> 2);
+            const int i = rr >> log_g;
+            const uint32_t* x = v[k >> 1] + (k & 1);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                  (static_cast<int64_t>(w.tok0 + i) * p.heads + w.h * G + (rr & (G - 1))) * W) +
+                         8 * g + (lane & 3);
+            if (i < w.ntok) {
+              dst[0] = make_uint4(x[0], x[2], x[4], x[6]);
+              dst[4] = make_uint4(x[8], x[10], x[12], x[14]);
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
       }
       tc_fence_before();
