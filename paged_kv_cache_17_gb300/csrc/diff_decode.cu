@@ -31,10 +31,10 @@ namespace pkv {
 
 template <int NT, bool FP8>
 struct DiffDecodeCfg {
-  static constexpr int kWarps = 2;  // consumers
+  static constexpr int kWarps = NT == 2 ? 3 : 2;  // consumers
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kTile = kBlockSize * kDiffW * (FP8 ? 1 : 2);
-  static constexpr int kStages = 32768 / (2 * kTile);
+  static constexpr int kStages = (NT == 2 ? 49152 : 32768) / (2 * kTile);
   static constexpr int kRing = 2 * kStages * kTile;
   static constexpr int kCols = 8 * NT;
   static constexpr int kBytes = 1008 + kRing + 2 * kStages * 8;  // 1008: alignment slack
@@ -91,6 +91,22 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
   const int32_t* table = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + blk0;
   // the first 32 ids, asked for beside the length (valid entries of the row; past the context they are not used)
   int ids = warp == NW && blk0 + lane < p.max_blocks ? table[lane] : 0;
+  // Q^T: column gid (of each tile), k-step kk: 16 of the 128 elements, the first map's for kk < 4.  E4M3: in
+  // the order of the codes that a lane reads, 16 consecutive ones of each half.  (Asked for beside the length too, and
+  // waited for by the warps that use it alone, so that K and V are asked for one round trip after the length is.)
+  uint32_t qb[KS][2];
+  if (warp < NW) {
+    const int g = NT == 2 ? gid : gid & 3;
+    const uint32_t* qr =
+        reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + static_cast<int64_t>(pair * G + (g < G ? g : 0)) * kDiffW);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      const bool live = g < G && (NT == 2 || (gid >> 2) == kk / 4);
+      const int w0 = FP8 ? (kk / 4) * 32 + tig * 8 + (kk & 3) * 2 : kk * 8 + tig;
+      qb[kk][0] = live ? qr[w0] : 0u;
+      qb[kk][1] = live ? qr[w0 + (FP8 ? 1 : 4)] : 0u;
+    }
+  }
   if (len < 0 || len > p.max_context_len) {
     if (threadIdx.x == 0 && s == 0) set_flag(p.status, PKV_DEVFLAG_BAD_CONTEXT_LEN);
     len = max(0, min(len, p.max_context_len));
@@ -110,20 +126,18 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
   }
   const int nloc = min(nblk - blk0, p.split_blocks);
 
-  // Q^T: column gid (of each tile), k-step kk: 16 of the 128 elements, the first map's for kk < 4.  E4M3: in
-  // the order of the codes that a lane reads, 16 consecutive ones of each half.
-  uint32_t qb[KS][2];
-  int qexp[NT];
-  if (warp < NW) {
-    const int g = NT == 2 ? gid : gid & 3;
-    const uint32_t* qr = reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + static_cast<int64_t>(head0 + g) * kDiffW);
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      const bool live = g < G && (NT == 2 || (gid >> 2) == kk / 4);
-      const int w0 = FP8 ? (kk / 4) * 32 + tig * 8 + (kk & 3) * 2 : kk * 8 + tig;
-      qb[kk][0] = live ? qr[w0] : 0u;
-      qb[kk][1] = live ? qr[w0 + (FP8 ? 1 : 4)] : 0u;
+  if (threadIdx.x == NW * 32) tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  int qexp[NT] = {};
+  if (warp < NW) {
     if constexpr (FP8) {  // the column's largest goes to 2^13 .. 2^14
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -145,16 +159,6 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
       }
     }
   }
-  if (threadIdx.x == NW * 32) tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    fence_mbar_init();
-  }
-  __syncthreads();
-
   // factors of this thread's columns 2 tig and 2 tig + 1 of each tile
   float factor[NT][2];
 #pragma unroll

@@ -1357,10 +1357,34 @@ void size_records(DiffPlan* d, int64_t rows, int64_t heads) {
   d->ws_bytes = d->ml_bytes + round256(records * pkv::kDiffW * sizeof(float));
 }
 
+// steps of 128 keys that an environment variable fixes (a count of `tokens` tokens each), or 0
+int forced_steps(const char* name, int tokens) {
+  if (const char* env = std::getenv(name)) {
+    const long v = std::strtol(env, nullptr, 10);
+    if (v * tokens >= 16) return static_cast<int>(std::min<long>((v * tokens + 127) / 128, 1 << 23));
+  }
+  return 0;
+}
+
+// One token: runs of choose_split's length where the contexts fill the SMs with runs of 512 tokens or more; below that
+// shorter ones, down to 64, for about 3.3 CTAs an SM, since a CTA alone takes 0.3 us a block.  Contexts of up to 12
+// blocks stay whole (the merge would cost more).  One request of 777 tokens, 64 query heads: 64 tokens a run 13.0 us, 128
+// 15.0, 512 21.2; one of 16,000: 256 27.3, 64 36.5, 512 29.3; 8 of 500: 64 15.0, 256 17.1, 512 19.1; 32 of 1000: 512 37.6,
+// 256 41.7, 64 46.8; one of 100: whole 10.9, in two 13.0 (launch and cold caches included).
+Split choose_diff_split(int batch, int pairs, int max_context_len, int sm_count) {
+  Split s = choose_split(batch, pairs, max_context_len, sm_count);
+  const long long blocks = (max_context_len + 15) / 16, all = blocks * batch * pairs;
+  if (forced_steps("PKV_SPLIT_TOKENS", 1) > 0 || blocks <= 12 || all >= 9LL * sm_count * kMinSplitBlocks) return s;
+  const long long want = (all * 3 / 10 + sm_count - 1) / sm_count;
+  s.split_blocks = static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks, (std::max(want, 4LL) + 3) / 4 * 4}));
+  s.max_splits = static_cast<int>((blocks + s.split_blocks - 1) / s.split_blocks);
+  return s;
+}
+
 DiffPlan plan_diff_decode(int batch, int hq, int hkv, int max_context_len, int pre_slots, int sm_count) {
   DiffPlan d{};
   d.pre_slots = pre_slots;
-  d.split = choose_split(batch, hkv / 2, max_context_len, sm_count);
+  d.split = choose_diff_split(batch, hkv / 2, max_context_len, sm_count);
   const int blocks = (max_context_len + 15) / 16;
   while (d.split.max_splits > 65535) {  // the grid
     d.split.split_blocks *= 2;
@@ -1422,14 +1446,6 @@ DiffRuns plan_diff_runs(long long works, int steps, int most, double step_us, do
     }
   }
   return r;
-}
-
-int forced_steps(const char* name, int tokens) {
-  if (const char* env = std::getenv(name)) {
-    const long v = std::strtol(env, nullptr, 10);
-    if (v * tokens >= 16) return static_cast<int>(std::min<long>((v * tokens + 127) / 128, 1 << 23));
-  }
-  return 0;
 }
 
 struct DiffChunkPlan {
