@@ -8,8 +8,7 @@
 // accumulators are rescaled rarely; then  y = o_0 / l_0 - lam o_1 / l_1, its norm and the scale.  Statistics, both
 // products, difference and norm are held in fp32.  Rounded to 16 bits are the weights alone, the A operand of the
 // second product: bf16 for bf16 pools (half a step 2^-8), fp16 times 2^7 for E4M3 pools (2^-11; the factor keeps
-// weights down to 2^-31 of the largest); in prefix passes as two such terms, hi + lo, since the output of one
-// token may be fp32.  E4M3 pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per
+// weights down to 2^-31 of the largest); in prefix passes whose output is fp32 as two such terms, hi + lo.  E4M3 pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per
 // row and map that takes its largest into [128, 256), exact for elements down to 2^-9 of the largest and off by
 // at most 2^-17 of it below; V is expanded to fp16 (exact).
 //
@@ -145,7 +144,8 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
                       const __grid_constant__ CUtensorMap tm_v, const DiffParams p) {
   using C = DiffChunkCfg<FP8>;
   constexpr int W = kDiffW;
-  constexpr bool RECORDS = FORM != kDiffChunk, PREFIX = FORM == kDiffPrefix;
+  constexpr bool RECORDS = FORM != kDiffChunk, PREFIX = FORM == kDiffPrefix || FORM == kDiffPrefixFine;
+  constexpr bool FINE = FORM == kDiffPrefixFine;  // weights in two terms
   constexpr bool kQByThreads = FP8 || PREFIX;  // Q written by the softmax threads: converted, or gathered
   constexpr unsigned NS = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {
           mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, !first || kk > 0, leader);
-          if constexpr (PREFIX)
+          if constexpr (FINE)
             mma_ts(o_col, s_col + 64 + 8 * kk, v_lo + kk * (2 * kVGroup / 16), kDesc128<kVGroup>, kIdO, true, leader);
         }
       };
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
           tmem_ld64(scol + 64, *reinterpret_cast<float(*)[64]>(s + 64));
           // 32 weights from their scores, as 16-bit pairs into the columns of the scores
           float2 sum[2] = {};
-          uint32_t pw[16], pl[PREFIX ? 16 : 1];
+          uint32_t pw[16], pl[FINE ? 16 : 1];
           auto weights = [&](int q, float negm) {
             const float2 sc2 = make_float2(sscale, sscale), nm2 = make_float2(negm, negm);
 #pragma unroll
@@ -844,13 +844,13 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
               x.x = exp2_ftz(x.x);
               x.y = exp2_ftz(x.y);
               sum[i & 1] = fadd2(sum[i & 1], x);
-              if constexpr (PREFIX) split16<FP8>(x.x, x.y, pw[i], pl[i]);
+              if constexpr (FINE) split16<FP8>(x.x, x.y, pw[i], pl[i]);
               else pw[i] = pack16<FP8>(x.x, x.y);
             }
           };
           auto put = [&](int q) {
             tmem_st16u(scol + 16 * q, pw);
-            if constexpr (PREFIX) tmem_st16u(scol + 64 + 16 * q, pl);
+            if constexpr (FINE) tmem_st16u(scol + 64 + 16 * q, pl);
           };
           // a row that has seen nothing yet keeps reference 0: its weights are 2^-inf = 0
           auto minus_m = [&]() { return (m_used == -INFINITY ? 0.f : -m_used) + C::kBias; };
@@ -950,16 +950,36 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
           if (rv) p.part_ml[rec] = make_float2(m_used - C::kBias, l);
           __syncwarp();
           add_odd(g, 0, W);
+          // turned, through the columns that are read, so that four lanes store 64 bytes of a row together (lanes
+          // storing their own rows touch 32 lines an instruction)
 #pragma unroll 1
           for (int col = 0; col < W; col += 32) {
             float o[32];
             tmem_ld32(mine + col, o);
-            if (rv) {
-              float4* dst = reinterpret_cast<float4*>(p.part_acc + rec * W + col);
+            uint32_t words[16];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) words[i] = __float_as_uint(o[16 * c + i]);
+              turn_put(mine + col + 16 * c, words);
             }
-            __syncwarp();
+            tmem_wait_st();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[16];
+              turn_get(mine + col + (static_cast<uint32_t>(16 * half) << 16), v);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int src = 16 * half + 8 * k + (lane >> 2);
+                const int64_t to = __shfl_sync(kFull, rv ? rec : -1, src);
+                if (to >= 0) {
+                  uint4* dst = reinterpret_cast<uint4*>(p.part_acc + to * W + col) + (lane & 3);
+                  dst[0] = make_uint4(v[k], v[2 + k], v[4 + k], v[6 + k]);
+                  dst[4] = make_uint4(v[8 + k], v[10 + k], v[12 + k], v[14 + k]);
+                }
+                __syncwarp();
+              }
+            }
           }
         }
       } else {
@@ -1091,6 +1111,7 @@ static cudaError_t launch_form(DiffForm form, const CUtensorMap& tq, const CUten
   switch (form) {
     case kDiffChunk: return launch<FP8, kDiffChunk>(tq, tk, tv, p, tile_slots, splits, stream);
     case kDiffChunkSplit: return launch<FP8, kDiffChunkSplit>(tq, tk, tv, p, tile_slots, splits, stream);
+    case kDiffPrefixFine: return launch<FP8, kDiffPrefixFine>(tq, tk, tv, p, tile_slots, splits, stream);
     case kDiffPrefix: return launch<FP8, kDiffPrefix>(tq, tk, tv, p, tile_slots, splits, stream);
   }
   return cudaErrorInvalidValue;

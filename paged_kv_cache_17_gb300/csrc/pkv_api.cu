@@ -1751,7 +1751,7 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
     return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
   const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_diff_chunk(fp8, pkv::kDiffPrefix, none, ck, cv, pass, x.tile_slots, x.runs.splits, cs);
+  cudaError_t e = pkv::launch_diff_chunk(fp8, p.out_fp32 ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, ck, cv, pass, x.tile_slots, x.runs.splits, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefix-pass launch");
   e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
