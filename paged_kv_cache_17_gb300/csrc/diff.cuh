@@ -14,6 +14,7 @@ namespace pkv {
 
 constexpr int kDiffD = 64;            // elements of a head
 constexpr int kDiffW = 2 * kDiffD;    // of a pair's value
+constexpr int kDiffCluster = 8;       // the largest cluster that every launch may ask for
 
 struct DiffParams {
   const uint16_t* q;        // [rows][2 heads][64] bf16, rows q_stride apart
@@ -35,6 +36,7 @@ struct DiffParams {
   int pre_slots;     // slots of a shared prefix (0: none)
   int split_blocks;  // 16-token blocks of one of a row's own slots
   int max_splits;    // own slots
+  int cluster;       // one token: a sequence's runs (at most kDiffCluster) are a cluster and end its rows, no records
   int batch, rows;
   int heads, pairs, group;  // output heads, pairs of kv heads, heads / pairs
   int max_blocks, num_blocks, max_context_len;

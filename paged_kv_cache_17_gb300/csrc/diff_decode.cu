@@ -15,6 +15,8 @@
 // Contexts are cut into runs of blocks, one CTA each: a producer warp that streams K and V by TMA, a block's pair
 // as one box each, and two consumer warps that take the blocks in turn, each with its own statistics.  A sequence
 // of one run ends here (difference, norm, store); others leave a record per map and the merge kernel ends them.
+// Where few requests leave most SMs idle, a sequence's runs, at most eight, are a thread-block cluster instead: they
+// read each other's states through distributed shared memory and end the rows themselves, without a second kernel.
 //
 // What bounds it: reading K and V once.
 #include <cuda.h>
@@ -62,7 +64,32 @@ __device__ __forceinline__ uint32_t diff_at(uint32_t base, int r, int c) {
   return base + (r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int NT, bool FP8>
+// Every CTA of the cluster has come here; what it wrote to shared memory before is seen
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address in CTA `rank` of the cluster of what is at addr here
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_rank(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+
+template <int NT, bool FP8, bool CLUSTER>
 __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
     diff_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DiffParams p) {
@@ -83,6 +110,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
   const bool beside = p.pre_slots > 0;
   if (!beside) pdl_wait();
   auto leave = [&]() {
+    if constexpr (CLUSTER) cluster_sync();  // nobody reads this CTA's shared memory any more
     if (beside && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) pdl_wait();
   };
 
@@ -121,6 +149,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
       const float zero[4] = {};
       for (int g = warp; g < G; g += NW + 1) diff_store(p, b, head0 + g, true, zero, zero, lane);
     }
+    if constexpr (CLUSTER) cluster_sync();
     leave();
     return;
   }
@@ -374,6 +403,46 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
         }
       }
   }
+  if constexpr (CLUSTER) {
+    // Head g of the group is ended by the cluster's CTA g mod nsplit.  Lane i holds state i (run i / NW, warp i mod NW).
+    cluster_sync();
+    const int states = nsplit * NW;
+    const float vs = FP8 ? p.scales[2 * (p.pairs + pair) + lane / 16] : 1.f;
+    for (int g = s + warp * nsplit; g < G; g += (NW + 1) * nsplit) {
+      float y[2][4];
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        const int c = NT == 2 ? 8 * map + g : 4 * map + g;
+        const int i = min(lane, states - 1), at = i % NW * NC + c;
+        float top = ld_rank(map_rank(smem_u32(ms + at), i / NW)), den = ld_rank(map_rank(smem_u32(ls + at), i / NW));
+        const float own = top;
+        if (lane >= states) den = 0.f;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, shfl_xor(top, k));
+        // (a state without blocks has maximum -inf and sum 0, and so has one whose scores were all NaN, sum NaN)
+        const float f = own == -INFINITY ? 1.f : fast_exp2(own - top);
+        den *= f;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) den += shfl_xor(den, k);
+        float num[4] = {};
+#pragma unroll 4
+        for (int j = 0; j < states; ++j) {
+          const float w = __shfl_sync(kFull, f, j);
+          const float4 x = ld_rank4(map_rank(smem_u32(os + (j % NW * NC + c) * kDiffW + 4 * lane), j / NW));
+          num[0] = fmaf(w, x.x, num[0]);
+          num[1] = fmaf(w, x.y, num[1]);
+          num[2] = fmaf(w, x.z, num[2]);
+          num[3] = fmaf(w, x.w, num[3]);
+        }
+        const float by = vs / den;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[map][k] = num[k] * by;
+      }
+      diff_store(p, b, head0 + g, false, y[0], y[1], lane);
+    }
+    leave();
+    return;
+  }
   __syncthreads();
   const bool ends = nsplit == 1 && !with_prefix;
   const float vs = FP8 ? p.scales[2 * (p.pairs + pair) + lane / 16] : 1.f;
@@ -412,10 +481,10 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
   leave();
 }
 
-template <int NT, bool FP8>
+template <int NT, bool FP8, bool CLUSTER>
 static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p, cudaStream_t stream) {
   using C = DiffDecodeCfg<NT, FP8>;
-  auto kern = diff_decode_kernel<NT, FP8>;
+  auto kern = diff_decode_kernel<NT, FP8, CLUSTER>;
   static std::atomic<bool> configured[64] = {};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -430,18 +499,31 @@ static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Di
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if constexpr (CLUSTER) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = static_cast<unsigned>(p.max_splits);
+    cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
+}
+
+template <bool CLUSTER>
+static cudaError_t launch_form(bool fp8, const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p,
+                               cudaStream_t stream) {
+  if (p.group <= 4) return fp8 ? launch<1, true, CLUSTER>(tk, tv, p, stream) : launch<1, false, CLUSTER>(tk, tv, p, stream);
+  return fp8 ? launch<2, true, CLUSTER>(tk, tv, p, stream) : launch<2, false, CLUSTER>(tk, tv, p, stream);
 }
 
 cudaError_t launch_diff_decode(bool fp8, const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p,
                                cudaStream_t stream) {
-  if (p.group <= 4) return fp8 ? launch<1, true>(tk, tv, p, stream) : launch<1, false>(tk, tv, p, stream);
-  return fp8 ? launch<2, true>(tk, tv, p, stream) : launch<2, false>(tk, tv, p, stream);
+  return p.cluster ? launch_form<true>(fp8, tk, tv, p, stream) : launch_form<false>(fp8, tk, tv, p, stream);
 }
 
 }  // namespace pkv

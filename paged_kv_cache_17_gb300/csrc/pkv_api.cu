@@ -1347,11 +1347,12 @@ pkv::DiffParams diff_params(const pkv_cache_desc* cache, const pkv_diff_desc* f,
 struct DiffPlan {
   Split split;
   int pre_slots;
+  bool cluster;  // one token: the runs of a sequence are a cluster, and leave no records
   size_t ml_bytes, ws_bytes;
 };
 
 void size_records(DiffPlan* d, int64_t rows, int64_t heads) {
-  if (d->split.max_splits <= 1 && d->pre_slots == 0) return;
+  if ((d->split.max_splits <= 1 || d->cluster) && d->pre_slots == 0) return;
   const size_t records = static_cast<size_t>(d->pre_slots + d->split.max_splits) * 2 * rows * heads;
   d->ml_bytes = round256(records * 2 * sizeof(float));
   d->ws_bytes = d->ml_bytes + round256(records * pkv::kDiffW * sizeof(float));
@@ -1366,25 +1367,36 @@ int forced_steps(const char* name, int tokens) {
   return 0;
 }
 
-// One token: runs of choose_split's length where the contexts fill the SMs with runs of 512 tokens or more; below that
-// shorter ones, down to 64, for about 3.3 CTAs an SM, since a CTA alone takes 0.3 us a block.  Contexts of up to 12
-// blocks stay whole (the merge would cost more).  One request of 777 tokens, 64 query heads: 64 tokens a run 13.0 us, 128
-// 15.0, 512 21.2; one of 16,000: 256 27.3, 64 36.5, 512 29.3; 8 of 500: 64 15.0, 256 17.1, 512 19.1; 32 of 1000: 512 37.6,
-// 256 41.7, 64 46.8; one of 100: whole 10.9, in two 13.0 (launch and cold caches included).
-Split choose_diff_split(int batch, int pairs, int max_context_len, int sm_count) {
-  Split s = choose_split(batch, pairs, max_context_len, sm_count);
+// One token: runs of choose_split's length where the contexts fill the SMs with runs of 512 tokens or more.  Below that
+// shorter ones, down to 64, for about 3.3 CTAs an SM, since a CTA alone takes 0.3 us a block; and where eight runs, up to
+// eight blocks longer than that, are enough, a cluster, which saves the merge kernel.  Contexts of up to 12 blocks stay
+// whole.  (FIGURES)
+struct DiffSplit {
+  Split split;
+  bool cluster;
+};
+
+DiffSplit choose_diff_split(int batch, int pairs, int max_context_len, bool records, int sm_count) {
+  DiffSplit s{choose_split(batch, pairs, max_context_len, sm_count), false};
   const long long blocks = (max_context_len + 15) / 16, all = blocks * batch * pairs;
-  if (forced_steps("PKV_SPLIT_TOKENS", 1) > 0 || blocks <= 12 || all >= 9LL * sm_count * kMinSplitBlocks) return s;
-  const long long want = (all * 3 / 10 + sm_count - 1) / sm_count;
-  s.split_blocks = static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks, (std::max(want, 4LL) + 3) / 4 * 4}));
-  s.max_splits = static_cast<int>((blocks + s.split_blocks - 1) / s.split_blocks);
+  const bool forced = std::getenv("PKV_SPLIT_TOKENS") != nullptr;
+  if (!forced && blocks > 12 && all < 9LL * sm_count * kMinSplitBlocks) {
+    const long long want = std::max((all * 3 / 10 + sm_count - 1) / sm_count, 4LL), eighth = (blocks + 7) / 8;
+    const bool cluster = !records && eighth <= want + 8;
+    s.split.split_blocks =
+        static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks, cluster ? std::max(want, eighth) : (want + 3) / 4 * 4}));
+    s.split.max_splits = static_cast<int>((blocks + s.split.split_blocks - 1) / s.split.split_blocks);
+    s.cluster = cluster && s.split.max_splits > 1 && s.split.max_splits <= pkv::kDiffCluster;
+  }
   return s;
 }
 
 DiffPlan plan_diff_decode(int batch, int hq, int hkv, int max_context_len, int pre_slots, int sm_count) {
   DiffPlan d{};
   d.pre_slots = pre_slots;
-  d.split = choose_diff_split(batch, hkv / 2, max_context_len, sm_count);
+  const DiffSplit c = choose_diff_split(batch, hkv / 2, max_context_len, pre_slots > 0, sm_count);
+  d.split = c.split;
+  d.cluster = c.cluster;
   const int blocks = (max_context_len + 15) / 16;
   while (d.split.max_splits > 65535) {  // the grid
     d.split.split_blocks *= 2;
@@ -1406,6 +1418,7 @@ void set_records(pkv::DiffParams* p, const DiffPlan& d, void* workspace) {
   p->pre_slots = d.pre_slots;
   p->split_blocks = d.split.split_blocks;
   p->max_splits = d.split.max_splits;
+  p->cluster = d.cluster;
   if (d.ws_bytes > 0) {
     p->part_ml = static_cast<float2*>(workspace);
     p->part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.ml_bytes);
@@ -1662,7 +1675,7 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
-  if (p.max_splits > 1) {
+  if (p.max_splits > 1 && !p.cluster) {
     e = pkv::launch_diff_merge(fp8, p, cs);
     if (e != cudaSuccess) return cuda_fail(e, "differential merge launch");
   }
