@@ -31,12 +31,12 @@
 
 namespace pkv {
 
-template <int NT, bool FP8>
+template <int NT, bool FP8, bool CLUSTER>
 struct DiffDecodeCfg {
-  static constexpr int kWarps = NT == 2 ? 3 : 2;  // consumers
+  static constexpr int kWarps = CLUSTER ? 4 : NT == 2 ? 3 : 2;  // consumers
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kTile = kBlockSize * kDiffW * (FP8 ? 1 : 2);
-  static constexpr int kStages = (NT == 2 ? 49152 : 32768) / (2 * kTile);
+  static constexpr int kStages = (CLUSTER ? 65536 : NT == 2 ? 49152 : 32768) / (2 * kTile);
   static constexpr int kRing = 2 * kStages * kTile;
   static constexpr int kCols = 8 * NT;
   static constexpr int kBytes = 1008 + kRing + 2 * kStages * 8;  // 1008: alignment slack
@@ -90,10 +90,10 @@ __device__ __forceinline__ float4 ld_rank4(uint32_t addr) {
 }
 
 template <int NT, bool FP8, bool CLUSTER>
-__global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
+__global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
     diff_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DiffParams p) {
-  using C = DiffDecodeCfg<NT, FP8>;
+  using C = DiffDecodeCfg<NT, FP8, CLUSTER>;
   constexpr int NW = C::kWarps, ST = C::kStages, KS = kDiffW / 16, MT = kDiffW / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -403,46 +403,6 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
         }
       }
   }
-  if constexpr (CLUSTER) {
-    // Head g of the group is ended by the cluster's CTA g mod nsplit.  Lane i holds state i (run i / NW, warp i mod NW).
-    cluster_sync();
-    const int states = nsplit * NW;
-    const float vs = FP8 ? p.scales[2 * (p.pairs + pair) + lane / 16] : 1.f;
-    for (int g = s + warp * nsplit; g < G; g += (NW + 1) * nsplit) {
-      float y[2][4];
-#pragma unroll
-      for (int map = 0; map < 2; ++map) {
-        const int c = NT == 2 ? 8 * map + g : 4 * map + g;
-        const int i = min(lane, states - 1), at = i % NW * NC + c;
-        float top = ld_rank(map_rank(smem_u32(ms + at), i / NW)), den = ld_rank(map_rank(smem_u32(ls + at), i / NW));
-        const float own = top;
-        if (lane >= states) den = 0.f;
-#pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, shfl_xor(top, k));
-        // (a state without blocks has maximum -inf and sum 0, and so has one whose scores were all NaN, sum NaN)
-        const float f = own == -INFINITY ? 1.f : fast_exp2(own - top);
-        den *= f;
-#pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) den += shfl_xor(den, k);
-        float num[4] = {};
-#pragma unroll 4
-        for (int j = 0; j < states; ++j) {
-          const float w = __shfl_sync(kFull, f, j);
-          const float4 x = ld_rank4(map_rank(smem_u32(os + (j % NW * NC + c) * kDiffW + 4 * lane), j / NW));
-          num[0] = fmaf(w, x.x, num[0]);
-          num[1] = fmaf(w, x.y, num[1]);
-          num[2] = fmaf(w, x.z, num[2]);
-          num[3] = fmaf(w, x.w, num[3]);
-        }
-        const float by = vs / den;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[map][k] = num[k] * by;
-      }
-      diff_store(p, b, head0 + g, false, y[0], y[1], lane);
-    }
-    leave();
-    return;
-  }
   __syncthreads();
   const bool ends = nsplit == 1 && !with_prefix;
   const float vs = FP8 ? p.scales[2 * (p.pairs + pair) + lane / 16] : 1.f;
@@ -470,6 +430,13 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
         const float by = vs / den;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[map][i] = num[i] * by;
+      } else if constexpr (CLUSTER) {  // the run's state, in the place of the first warp's
+        __syncwarp();
+        *reinterpret_cast<float4*>(os + c * kDiffW + 4 * lane) = make_float4(num[0], num[1], num[2], num[3]);
+        if (lane == 0) {
+          ms[c] = top;
+          ls[c] = den;
+        }
       } else {
         const int64_t rec = (static_cast<int64_t>((p.pre_slots + s) * 2 + map) * p.rows + b) * p.heads + head0 + g;
         *reinterpret_cast<float4*>(p.part_acc + rec * kDiffW + 4 * lane) = make_float4(num[0], num[1], num[2], num[3]);
@@ -478,12 +445,58 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8>::kThreads))
     }
     if (ends) diff_store(p, b, head0 + g, false, y[0], y[1], lane);
   }
+  if constexpr (CLUSTER) {
+    cluster_sync();
+    // head g of the group is ended by the cluster's CTA g mod nsplit; lane j holds run j's maximum and sum
+    for (int g = s + warp * nsplit; !ends && g < G; g += (NW + 1) * nsplit) {
+      float y[2][4];
+      float4 x[2][kDiffCluster];
+      float top[2], den[2];
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        const int c = NT == 2 ? 8 * map + g : 4 * map + g, j = min(lane, nsplit - 1);
+        top[map] = ld_rank(map_rank(smem_u32(ms + c), j));
+        den[map] = ld_rank(map_rank(smem_u32(ls + c), j));
+#pragma unroll
+        for (int i = 0; i < kDiffCluster; ++i)
+          if (i < nsplit) x[map][i] = ld_rank4(map_rank(smem_u32(os + c * kDiffW + 4 * lane), i));
+      }
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        const float own = top[map];
+        float all = own, sum = lane < nsplit ? den[map] : 0.f;
+#pragma unroll
+        for (int k = 4; k >= 1; k >>= 1) all = fmaxf(all, shfl_xor(all, k));  // (lanes 0-7; the others repeat the last)
+        all = __shfl_sync(kFull, all, 0);
+        const float f = own == -INFINITY ? 1.f : fast_exp2(own - all);
+        sum *= f;
+#pragma unroll
+        for (int k = 4; k >= 1; k >>= 1) sum += shfl_xor(sum, k);
+        sum = __shfl_sync(kFull, sum, 0);
+        float num[4] = {};
+#pragma unroll
+        for (int i = 0; i < kDiffCluster; ++i) {
+          const float w = __shfl_sync(kFull, f, i);
+          if (i < nsplit) {
+            num[0] = fmaf(w, x[map][i].x, num[0]);
+            num[1] = fmaf(w, x[map][i].y, num[1]);
+            num[2] = fmaf(w, x[map][i].z, num[2]);
+            num[3] = fmaf(w, x[map][i].w, num[3]);
+          }
+        }
+        const float by = vs / sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[map][k] = num[k] * by;
+      }
+      diff_store(p, b, head0 + g, false, y[0], y[1], lane);
+    }
+  }
   leave();
 }
 
 template <int NT, bool FP8, bool CLUSTER>
 static cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const DiffParams& p, cudaStream_t stream) {
-  using C = DiffDecodeCfg<NT, FP8>;
+  using C = DiffDecodeCfg<NT, FP8, CLUSTER>;
   auto kern = diff_decode_kernel<NT, FP8, CLUSTER>;
   static std::atomic<bool> configured[64] = {};
   int device = 0;

@@ -1382,7 +1382,8 @@ DiffSplit choose_diff_split(int batch, int pairs, int max_context_len, bool reco
   const bool forced = std::getenv("PKV_SPLIT_TOKENS") != nullptr;
   if (!forced && blocks > 12 && all < 9LL * sm_count * kMinSplitBlocks) {
     const long long want = std::max((all * 3 / 10 + sm_count - 1) / sm_count, 4LL), eighth = (blocks + 7) / 8;
-    const bool cluster = !records && eighth <= want + 8;
+    const bool cluster =
+        !records && eighth <= want + 8 && static_cast<long long>(batch) * pairs * std::min(blocks, 8LL) <= 3LL * sm_count;
     s.split.split_blocks =
         static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks, cluster ? std::max(want, eighth) : (want + 3) / 4 * 4}));
     s.split.max_splits = static_cast<int>((blocks + s.split.split_blocks - 1) / s.split.split_blocks);
