@@ -492,7 +492,9 @@ typedef struct {
   float out_scale;
 } pkv_diff_desc;
 
-/* Chunks of new tokens (pkv_paged_prefill_attention; out is bf16, and there is no lse). */
+/* Chunks of new tokens (pkv_paged_prefill_attention; out is bf16, and there is no lse).
+ *   The softmax weights enter the second product as in the plain call: rounded to bf16 (bf16 pools) or fp16 (E4M3).
+ *   PKV_SPLIT_TOKENS fixes the partition length (rounded up to a multiple of 128, at most 65,536). */
 size_t pkv_diff_prefill_workspace_size(int32_t batch, int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
                                        int32_t head_dim, int32_t max_context_len);
 
@@ -503,7 +505,9 @@ pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const v
                                             float softmax_scale, const pkv_diff_desc* diff, void* out, void* workspace,
                                             size_t workspace_bytes, pkv_stream_t stream);
 
-/* One token per sequence (pkv_paged_decode_attention). */
+/* One token per sequence (pkv_paged_decode_attention, with no CUDA-core form).
+ *   The weights enter as a 16-bit hi + lo pair; E4M3 pools: q times a power of two per head, in fp16.  What the pages
+ *   hold past a context does not reach the result, NaN and infinities included. */
 size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t max_context_len);
 
@@ -513,7 +517,12 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
                                            const pkv_diff_desc* diff, void* out, pkv_out_dtype out_dtype,
                                            void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
-/* One token per sequence, prefixes shared (pkv_cascade_decode_attention). */
+/* One token per sequence, prefixes shared (pkv_cascade_decode_attention).
+ *   The prefix part runs as a chunk does, its weights rounded as there; for an fp32 output they enter as a hi + lo
+ *   pair.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong or longer than
+ *   max_members, or a member outside the batch, sets PKV_DEVFLAG_BAD_INDPTR: the results of the sequences that it
+ *   would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the blocks per run of
+ *   the prefix part (rounded up to a multiple of 8, at most 512). */
 size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t max_context_len, int32_t num_prefixes, int32_t max_members,
                                        int32_t max_prefix_len);

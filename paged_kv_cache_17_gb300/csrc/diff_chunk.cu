@@ -20,8 +20,7 @@
 //
 //   warps 0-3, 4-7  softmax of map 0 and 1: thread r owns row r (TMEM lane r): scores in, weights out over them as
 //                   16-bit pairs, rare rescale of the output, epilogue (each group 64 columns of both outputs)
-//   warps 8, 10     issue the MMAs of map 0 and 1, in turns: per step P V, then the next scores (one warp for both
-//                   took 1.4 times as long to issue as the tensor cores to execute)
+//   warps 8, 10     issue the MMAs of map 0 and 1, in turns: per step P V, then the next scores
 //   warp 9          finds the work and passes it on; TMA of Q, K and V, a 16-token block at a time
 //   warp 11         looks for bad ranges
 //   warps 12-15     V: zero the rows past the context in the last tile, so that what a page holds there (NaN
@@ -34,6 +33,21 @@
 //
 // Shared memory: Q (both halves; E4M3 hi and lo), a ring of K and V tiles in the order K0 K1 V0 K2 V1 .., E4M3 two
 // fp16 V tiles.  TMEM (512 columns): scores, then weights, of map m at 128 m; outputs at 256 + 128 m.
+//
+// What bounds it.  A step of 128 keys is 1536 cycles of products for both maps and takes about 2500: the chain of a map,
+// scores -> weights -> products, is 1250 cycles of softmax (220 to load the scores, 650 for the first 32 weights beside
+// the maximum, 380 to the first half's arrival) and about 1000 from there to the next scores, and the other map covers
+// as much of it as the turns allow.  Exponentials left out: 6 % less; softmax left out: 1.65 ms of 2.09, the measured
+// cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.1 ms = 1.47 PFLOP/s, 78 % of the measured burst rate and 86 %
+// of the sustained one (the power limit holds the clock at 1.9 GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96
+// PFLOP/s: 6.4 steps a work, and 6000 cycles of start, join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split:
+// 142 us, 64 % of the copy rate: a step's chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to
+// 9000, 128 + 16 heads: 0.90 ms = 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 29 us alone, 16 steps and 8 us.
+//   Measured and left out: one issuing warp for both maps (2256 us against 2092 for the long chunk); half steps of 64 keys
+// in two score buffers a map, so that scores do not wait for weights (2363; products of 64 keys and every change between
+// operand forms cost about 100 cycles a piece, 3060 when pieces of the two are interleaved); the weights of a step
+// checked against the reference in two halves (2160); no turns (2430); a row's 64 columns of the output kept in
+// registers through the epilogue (2250: spills in the softmax).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -18,7 +18,12 @@
 // Where few requests leave most SMs idle, a sequence's runs, at most eight, are a thread-block cluster instead: they
 // read each other's states through distributed shared memory and end the rows themselves, without a second kernel.
 //
-// What bounds it: reading K and V once.
+// What bounds it.  Reading K and V once, for bf16 pools: 64 requests of 512 to 4096 tokens, 64 + 16 heads: 97 us = 6.2
+// TB/s of all bytes, 91 % of the measured copy; 8 of 32 to 128 thousand, 128 + 16 heads: 374 us = 6.55 TB/s, 97 % (three
+// consumer warps and a 48 KiB ring for two tiles; two and 32 KiB: 395).  E4M3, 33 of 1000 to 9001, 16 heads of their own: 71
+// us = 4.8 TB/s: 380 instructions a block from two warps a CTA, 48 % of the issue slots, and a wave of uneven CTAs (an
+// SM is busy 80 % of the time); two blocks at a time in a warp need more registers than they hide latency (79), four warps
+// a CTA the same.  One request of 777 tokens: 7.2 us in a graph, launch and five dependent round trips.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -3,7 +3,9 @@
 //   y_m = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j,  then the difference, the norm and the store.
 // One to eight warps per (row, output head), which take runs of slots, both maps each; records in order within a
 // warp, warps in order, so the result does not depend on timing.  Bound by reading the records once, which the
-// kernels before it leave in L2.
+// kernels before it leave in L2: 256 rows of 32 heads, two or three records a map (20 MB): 10 us by itself with cold
+// caches, its launch under the end of the kernel before; one row of 32 heads, 13 records: 4 us, the chain row -> length
+// -> records -> norm.
 #include <cuda_runtime.h>
 
 #include "diff.cuh"

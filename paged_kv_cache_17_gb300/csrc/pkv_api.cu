@@ -1370,7 +1370,10 @@ int forced_steps(const char* name, int tokens) {
 // One token: runs of choose_split's length where the contexts fill the SMs with runs of 512 tokens or more.  Below that
 // shorter ones, down to 64, for about 3.3 CTAs an SM, since a CTA alone takes 0.3 us a block; and where eight runs, up to
 // eight blocks longer than that, are enough, a cluster, which saves the merge kernel.  Contexts of up to 12 blocks stay
-// whole.  (FIGURES)
+// whole.  With cold caches: one request of 16,000 tokens, 64 query heads: runs of 256 tokens 27.3 us, 64 37.5, 512 29.3;
+// four of 9000, E4M3: 320 21.2, 64 31.4, 512 25.2; 32 of 1000: 512 37.5, 256 41.6, 64 46.7; one of 100: whole 10.9, in two
+// 12.9.  Clusters, in a graph: one request of 777 tokens 7.2 us (runs of 64 and a merge 7.3, of 128 8.2, of 512 13.3),
+// four of 2000 9.7 (10.7 at the best run), one of 250 6.2 (7.2).
 struct DiffSplit {
   Split split;
   bool cluster;
@@ -1484,9 +1487,11 @@ DiffChunkPlan plan_diff_chunk(int batch, int total_q, int hq, int hkv, bool fp8,
   return c;
 }
 
-// Shared prefixes: a prefix's members are the rows of its tiles.  The softmax weights enter in two terms, so a step's
-// products take 2560 cycles.  At most 64 steps a run (8192 keys), so that truncated sums stay within 2^-14.
-constexpr double kDiffPrefixStepUs = 1.5;
+// Shared prefixes: a prefix's members are the rows of its tiles.  At most 64 steps a run (8192 keys), so that truncated
+// sums stay within 2^-14.  256 sequences over 2048 tokens: one run of 16 steps 81 us in all (cold), two 90, four 112;
+// sixteen prompts of 2000, eight sequences each, E4M3: 55, 59, 72; two of 784, three each: seven runs of one step 17, four
+// 18, two 22.
+constexpr double kDiffPrefixStepUs = 1.5;  // (two-term weights, for fp32 outputs: 2.6)
 constexpr int kDiffPrefixMaxRun = 64;
 
 struct DiffPrefixPlan {
@@ -1760,12 +1765,14 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
   pass.max_context_len = px->max_prefix_len;
   pass.batch = px->num_prefixes;
   pass.split_tiles = x.runs.split_tiles;
-  CUtensorMap none{}, ck, cv, tk, tv;
-  if (!encode_pairs_chunk(&ck, &cv, cache) || !encode_pairs(&tk, &tv, cache))
-    return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
   const bool fp8 = cache->kv_dtype == PKV_KV_FP8_E4M3;
+  // (the maps of pass and decode differ in E4M3's V alone)
+  CUtensorMap none{}, tk, tv, pass_v;
+  if (!encode_pairs(&tk, &tv, cache) ||
+      (fp8 && !encode_kv_map(&pass_v, cache->v_cache, cache->num_blocks, hkv / 2, pkv::kDiffW, true)))
+    return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_diff_chunk(fp8, p.out_fp32 ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, ck, cv, pass, x.tile_slots, x.runs.splits, cs);
+  cudaError_t e = pkv::launch_diff_chunk(fp8, p.out_fp32 ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, tk, fp8 ? pass_v : tv, pass, x.tile_slots, x.runs.splits, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefix-pass launch");
   e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
