@@ -8,9 +8,10 @@
 // accumulators are rescaled rarely; then  y = o_0 / l_0 - lam o_1 / l_1, its norm and the scale.  Statistics, both
 // products, difference and norm are held in fp32.  Rounded to 16 bits are the weights alone, the A operand of the
 // second product: bf16 for bf16 pools (half a step 2^-8), fp16 times 2^7 for E4M3 pools (2^-11; the factor keeps
-// weights down to 2^-31 of the largest); in prefix passes whose output is fp32 as two such terms, hi + lo.  E4M3 pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per
-// row and map that takes its largest into [128, 256), exact for elements down to 2^-9 of the largest and off by
-// at most 2^-17 of it below; V is expanded to fp16 (exact).
+// weights down to 2^-31 of the largest); in prefix passes whose output is fp32 as two such terms, hi + lo.  E4M3
+// pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per row and map that takes its
+// largest into [128, 256), exact for elements down to 2^-9 of the largest and off by at most 2^-17 of it below; V is
+// expanded to fp16 (exact).
 //
 // Layout.  A work is 128 rows (128 / G tokens of the G heads of a pair) over one run of keys.  K's tile of 128 keys
 // holds both maps' halves side by side, V's tile is the pair's value; each is loaded once for both maps.  The two
@@ -34,20 +35,21 @@
 // Shared memory: Q (both halves; E4M3 hi and lo), a ring of K and V tiles in the order K0 K1 V0 K2 V1 .., E4M3 two
 // fp16 V tiles.  TMEM (512 columns): scores, then weights, of map m at 128 m; outputs at 256 + 128 m.
 //
-// What bounds it.  A step of 128 keys is 1536 cycles of products for both maps and takes about 2500: the chain of a map,
-// scores -> weights -> products, is 1250 cycles of softmax (220 to load the scores, 650 for the first 32 weights beside
-// the maximum, 380 to the first half's arrival) and about 1000 from there to the next scores, and the other map covers
-// as much of it as the turns allow.  Exponentials left out: 6 % less; softmax left out: 1.65 ms of 2.09, the measured
-// cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.1 ms = 1.47 PFLOP/s, 78 % of the measured burst rate and 86 %
-// of the sustained one (the power limit holds the clock at 1.9 GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96
-// PFLOP/s: 6.4 steps a work, and 6000 cycles of start, join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split:
-// 142 us, 64 % of the copy rate: a step's chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to
-// 9000, 128 + 16 heads: 0.90 ms = 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 29 us alone, 16 steps and 8 us.
-//   Measured and left out: one issuing warp for both maps (2256 us against 2092 for the long chunk); half steps of 64 keys
-// in two score buffers a map, so that scores do not wait for weights (2363; products of 64 keys and every change between
-// operand forms cost about 100 cycles a piece, 3060 when pieces of the two are interleaved); the weights of a step
-// checked against the reference in two halves (2160); no turns (2430); a row's 64 columns of the output kept in
-// registers through the epilogue (2250: spills in the softmax).
+// What bounds it.  A step of 128 keys is 1536 cycles of products for both maps and takes 2250 (2500 traced): the
+// chain of a map, scores -> weights -> products, is 1250 cycles of softmax (220 to load the scores, 650 for the
+// first 32 weights beside the maximum, 380 to the first half's arrival) and about 1000 from there to the next
+// scores, and the other map covers as much of it as the turns allow.  Exponentials left out: 6 % less; softmax left
+// out: 1.65 ms of 2.09, the measured cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.1 ms = 1.47
+// PFLOP/s, 78 % of the measured burst rate and 86 % of the sustained one (the power limit holds the clock at 1.9
+// GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96 PFLOP/s: 6.4 steps a work, and 6000 cycles of start,
+// join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split: 142 us, 64 % of the copy rate: a step's
+// chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to 9000, 128 + 16 heads: 0.90 ms =
+// 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 29 us alone, 16 steps and 8 us.
+//   Measured and left out: one issuing warp for both maps (2256 us against 2092 for the long chunk); half steps of 64
+// keys in two score buffers a map, so that scores do not wait for weights (2363; products of 64 keys and every
+// change between operand forms cost about 100 cycles a piece, 3060 when pieces of the two are interleaved); the
+// weights of a step checked against the reference in two halves (2160); no turns (2430); a row's 64 columns of the
+// output kept in registers through the epilogue (2250: spills in the softmax).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -86,7 +88,8 @@ struct DiffChunkCfg {
   static constexpr int kKinds = FP8 ? 1 : 3;                // NaN, +inf, -inf (E4M3 has no infinity)
   static constexpr int kBytes = 1008 + kOffPoison + kKinds * kDiffW * 4;  // 1008: alignment slack
   static constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
-  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kIssuer2Warp = 10, kRangeWarp = 11, kFixWarp0 = 12, kFixWarps = 4;
+  static constexpr int kIssuerWarp = 8, kProducerWarp = 9, kIssuer2Warp = 10, kRangeWarp = 11;
+  static constexpr int kFixWarp0 = 12, kFixWarps = 4;
   static constexpr int kThreads = (kFixWarp0 + kFixWarps) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;  // per thread
   static constexpr int kSoftRegs = 184;

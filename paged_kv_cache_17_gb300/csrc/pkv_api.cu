@@ -1361,8 +1361,8 @@ void size_records(DiffPlan* d, int64_t rows, int64_t heads) {
 // steps of 128 keys that an environment variable fixes (a count of `tokens` tokens each), or 0
 int forced_steps(const char* name, int tokens) {
   if (const char* env = std::getenv(name)) {
-    const long v = std::strtol(env, nullptr, 10);
-    if (v * tokens >= 16) return static_cast<int>(std::min<long>((v * tokens + 127) / 128, 1 << 23));
+    const long v = std::min(std::strtol(env, nullptr, 10), 1L << 30);
+    if (v * tokens >= 16) return static_cast<int>(std::min((v * tokens + 127) / 128, 1L << 23));
   }
   return 0;
 }

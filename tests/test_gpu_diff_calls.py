@@ -334,6 +334,36 @@ def test_blocks_far_into_a_large_pool(pkv, e4m3):
     assert pkv.check_device_status() == 0
 
 
+def test_scales_of_any_sign(pkv):
+    """E4M3 pools whose scales are negative or, of a key head, zero."""
+    ctx = [200, 33, 1000]
+    for flip in ((0, 0), (0, 1), (1, 1), None):
+        j = Job(3, ctx, 8, 4, True, 4)
+        if flip is None:
+            j.scales[0, 2] = 0.0
+        else:
+            j.scales[flip] *= -1
+        check_step(pkv, ctx, 8, 4, True, job=j)
+        check_chunk(pkv, [1, 1, 1], ctx, 8, 4, True, job=j)
+        check_shared(pkv, [96], [[1, 0]], [5, 0, 40], 8, 4, True, job=shared_job(flip))
+
+
+def shared_job(flip):
+    j = Job(3, [96, 5, 0, 40], 8, 4, True, 5)
+    if flip is None:
+        j.scales[0, 2] = 0.0
+    else:
+        j.scales[flip] *= -1
+    return j
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_one_pair(pkv, e4m3):
+    check_step(pkv, [300, 0, 7], 2, 2, e4m3)
+    check_chunk(pkv, [140, 3], [200, 7], 2, 2, e4m3, per_token=True)
+    check_shared(pkv, [64], [[1, 0]], [5, 0, 40], 2, 2, e4m3)
+
+
 def test_codes_as_bytes_and_lambda_layouts(pkv):
     ctx = [100, 33]
     j = Job(2, ctx, 8, 2, True, 2)
