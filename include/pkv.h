@@ -518,8 +518,8 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
                                            void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /* One token per sequence, prefixes shared (pkv_cascade_decode_attention).
- *   The prefix part runs as a chunk does, its weights rounded as there; for an fp32 output they enter as a hi + lo
- *   pair.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong or longer than
+ *   The prefix part's weights enter as a 16-bit hi + lo pair too, but for an E4M3 pool with a bf16 output: rounded to
+ *   fp16.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong or longer than
  *   max_members, or a member outside the batch, sets PKV_DEVFLAG_BAD_INDPTR: the results of the sequences that it
  *   would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the blocks per run of
  *   the prefix part (rounded up to a multiple of 8, at most 512). */

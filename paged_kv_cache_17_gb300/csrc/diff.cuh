@@ -60,7 +60,7 @@ cudaError_t launch_diff_merge(bool fp8, const DiffParams& p, cudaStream_t stream
 
 // Chunks (rows ended, or records where contexts are split) and prefix passes (records) on tcgen05; prefix passes
 // take their tables, lengths, ranges and sequences' count from p's q_indptr, block_tables, context_lens and batch
-// (fine: with softmax weights in two 16-bit terms, for fp32 outputs)
+// (fine: with softmax weights in two 16-bit terms; else E4M3 pools only)
 enum DiffForm { kDiffChunk, kDiffChunkSplit, kDiffPrefix, kDiffPrefixFine };
 cudaError_t launch_diff_chunk(bool fp8, DiffForm form, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const DiffParams& p, int tile_slots, int splits,

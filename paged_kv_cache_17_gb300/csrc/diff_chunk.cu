@@ -8,10 +8,10 @@
 // accumulators are rescaled rarely; then  y = o_0 / l_0 - lam o_1 / l_1, its norm and the scale.  Statistics, both
 // products, difference and norm are held in fp32.  Rounded to 16 bits are the weights alone, the A operand of the
 // second product: bf16 for bf16 pools (half a step 2^-8), fp16 times 2^7 for E4M3 pools (2^-11; the factor keeps
-// weights down to 2^-31 of the largest); in prefix passes whose output is fp32 as two such terms, hi + lo.  E4M3
-// pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per row and map that takes its
-// largest into [128, 256), exact for elements down to 2^-9 of the largest and off by at most 2^-17 of it below; V is
-// expanded to fp16 (exact).
+// weights down to 2^-31 of the largest); in prefix passes as two such terms, hi + lo, but for E4M3 pools with a bf16
+// output.  E4M3 pools: K enters as its codes, q as two E4M3 terms, hi + lo, after a power of two per row and map that
+// takes its largest into [128, 256), exact for elements down to 2^-9 of the largest and off by at most 2^-17 of it
+// below; V is expanded to fp16 (exact).
 //
 // Layout.  A work is 128 rows (128 / G tokens of the G heads of a pair) over one run of keys.  K's tile of 128 keys
 // holds both maps' halves side by side, V's tile is the pair's value; each is loaded once for both maps.  The two
@@ -44,7 +44,7 @@
 // GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96 PFLOP/s: 6.4 steps a work, and 6000 cycles of start,
 // join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split: 142 us, 64 % of the copy rate: a step's
 // chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to 9000, 128 + 16 heads: 0.90 ms =
-// 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 29 us alone, 16 steps and 8 us.
+// 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 42 us alone, 16 steps (29 us with one weight term).
 //   Measured and left out: one issuing warp for both maps (2256 us against 2092 for the long chunk); half steps of 64
 // keys in two score buffers a map, so that scores do not wait for weights (2363; products of 64 keys and every
 // change between operand forms cost about 100 cycles a piece, 3060 when pieces of the two are interleaved); the
@@ -1129,7 +1129,9 @@ static cudaError_t launch_form(DiffForm form, const CUtensorMap& tq, const CUten
     case kDiffChunk: return launch<FP8, kDiffChunk>(tq, tk, tv, p, tile_slots, splits, stream);
     case kDiffChunkSplit: return launch<FP8, kDiffChunkSplit>(tq, tk, tv, p, tile_slots, splits, stream);
     case kDiffPrefixFine: return launch<FP8, kDiffPrefixFine>(tq, tk, tv, p, tile_slots, splits, stream);
-    case kDiffPrefix: return launch<FP8, kDiffPrefix>(tq, tk, tv, p, tile_slots, splits, stream);
+    case kDiffPrefix:
+      if constexpr (FP8) return launch<FP8, kDiffPrefix>(tq, tk, tv, p, tile_slots, splits, stream);
+      break;
   }
   return cudaErrorInvalidValue;
 }

@@ -1488,10 +1488,10 @@ DiffChunkPlan plan_diff_chunk(int batch, int total_q, int hq, int hkv, bool fp8,
 }
 
 // Shared prefixes: a prefix's members are the rows of its tiles.  At most 64 steps a run (8192 keys), so that truncated
-// sums stay within 2^-14.  256 sequences over 2048 tokens: one run of 16 steps 81 us in all (cold), two 90, four 112;
+// sums stay within 2^-14.  256 sequences over 2048 tokens: one run of 16 steps 83 us in all (cold), two 95, four 121;
 // sixteen prompts of 2000, eight sequences each, E4M3: 55, 59, 72; two of 784, three each: seven runs of one step 17, four
 // 18, two 22.
-constexpr double kDiffPrefixStepUs = 1.5;  // (two-term weights, for fp32 outputs: 2.6)
+constexpr double kDiffPrefixStepUs = 1.5;  // (2.3 with two-term weights; the runs that it leads to are the best either way)
 constexpr int kDiffPrefixMaxRun = 64;
 
 struct DiffPrefixPlan {
@@ -1772,7 +1772,10 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
       (fp8 && !encode_kv_map(&pass_v, cache->v_cache, cache->num_blocks, hkv / 2, pkv::kDiffW, true)))
     return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = pkv::launch_diff_chunk(fp8, p.out_fp32 ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, tk, fp8 ? pass_v : tv, pass, x.tile_slots, x.runs.splits, cs);
+  // One term of a weight, fp16, is far below a bf16 output's rounding; one bf16 term is as large as it (256 sequences over
+  // one prompt: 68 us against 71, error 0.0025 against 0.0017)
+  const bool fine = !fp8 || p.out_fp32;
+  cudaError_t e = pkv::launch_diff_chunk(fp8, fine ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, tk, fp8 ? pass_v : tv, pass, x.tile_slots, x.runs.splits, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefix-pass launch");
   e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");

@@ -256,8 +256,8 @@ def check_shared(pkv, prefixes, members, tails, hq, hkv, e4m3, seed=0, scale=0.1
     keys = [([(front[prefix_of[i]], prefixes[prefix_of[i]])] if prefix_of[i] >= 0 else []) + [(own[i], t)]
             for i, t in enumerate(tails)]
     m = maps_64(j.q, [1] * b, (j.k, j.v), j.scales, keys, scale, j.lam, False)
-    # a prefix's weights are rounded as a chunk's are, but for fp32 outputs: two terms
-    weight = STEP_WEIGHT if dtype == torch.float32 else CHUNK_WEIGHT[e4m3]
+    # a prefix's weights are two terms, but for E4M3 pools with a bf16 output: one, fp16
+    weight = CHUNK_WEIGHT[True] if e4m3 and dtype == torch.bfloat16 else STEP_WEIGHT
     compare(out, finish_64(m, j.w, j.eps, j.out_scale), bounds(m, j.w, j.eps, j.out_scale, weight, e4m3, halves(dtype)))
     return out
 
@@ -349,7 +349,7 @@ def test_a_served_layer(pkv, e4m3):
                                                    **keys)
         key = [[(whole[b], at + 1)] for b in range(2)]
         check(plain, q, [1, 1], key, False, STEP_WEIGHT)
-        check(shared, q, [1, 1], key, False, CHUNK_WEIGHT[e4m3])
+        check(shared, q, [1, 1], key, False, CHUNK_WEIGHT[True] if e4m3 else STEP_WEIGHT)
     assert pkv.check_device_status() == 0
 
 
