@@ -42,7 +42,7 @@
 // out: 1.65 ms of 2.09, the measured cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.1 ms = 1.47
 // PFLOP/s, 78 % of the measured burst rate and 86 % of the sustained one (the power limit holds the clock at 1.9
 // GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96 PFLOP/s: 6.4 steps a work, and 6000 cycles of start,
-// join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split: 142 us, 64 % of the copy rate: a step's
+// join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split: 136 us, 67 % of the copy rate: a step's
 // chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to 9000, 128 + 16 heads: 0.90 ms =
 // 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 42 us alone, 16 steps (29 us with one weight term).
 //   Measured and left out: one issuing warp for both maps (2256 us against 2092 for the long chunk); half steps of 64
