@@ -1,7 +1,8 @@
 // diff_decode.cu -- differential attention of one token per sequence over the paged cache.
 //
 // Mathematics.  Per (sequence, pair of kv heads) and 16-token block, as two small products on the tensor cores
-// (mma.sync m16n8k16, fp32 accumulation), with an online softmax per column between them:
+// (mma.sync m16n8k16, fp32 accumulation), with an online softmax per column between them, by a reference that moves
+// when a score passes it by more than 2^8:
 //   S^T [16 tokens x C] = K [16 x 128] . Q^T [128 x C],    O^T [128 x C] += V^T [128 x 16] . P^T [16 x C]
 // A row of K holds the pair's two key heads side by side, a row of V is the pair's value.  The columns are (map,
 // query head of the group): a column's query fills its map's half of the 128, the other half is zero, so one
@@ -20,10 +21,11 @@
 //
 // What bounds it.  Reading K and V once, for bf16 pools: 64 requests of 512 to 4096 tokens, 64 + 16 heads: 97 us = 6.2
 // TB/s of all bytes, 91 % of the measured copy; 8 of 32 to 128 thousand, 128 + 16 heads: 374 us = 6.55 TB/s, 97 % (three
-// consumer warps and a 48 KiB ring for two tiles; two and 32 KiB: 395).  E4M3, 33 of 1000 to 9001, 16 heads of their own: 71
-// us = 4.8 TB/s: 380 instructions a block from two warps a CTA, 48 % of the issue slots, and a wave of uneven CTAs (an
-// SM is busy 80 % of the time); two blocks at a time in a warp need more registers than they hide latency (79), four warps
-// a CTA the same.  One request of 777 tokens: 7.2 us in a graph, launch and five dependent round trips.
+// consumer warps and a 48 KiB ring for two tiles; two and 32 KiB: 395).  E4M3, 33 of 1000 to 9001, 16 heads of their own: 68
+// us = 5.0 TB/s (71 with a maximum over the lanes for every block; 128 heads: 90, 100): some 360 instructions a block from
+// two warps a CTA, half of the issue slots, and a wave of uneven CTAs (an SM is busy 80 % of the time); two blocks at a
+// time in a warp, or the next block's scores under this one's softmax, need more than the 96 registers that let six CTAs
+// share an SM (79, 91), four warps a CTA the same; 80 registers for eight CTAs spill (81).  One request of 777 tokens: 7.2 us in a graph, launch and five dependent round trips.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
     }
   }
 
+  constexpr float kLazy = 8.f;
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -311,15 +314,18 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           sc[t][e] = gid + 8 * (e >> 1) < valid ? sc[t][e] * factor[t][e & 1] : -INFINITY;
-        // ---- online softmax: the block's maximum over the lanes of equal tig
-        float b0 = fmaxf(sc[t][0], sc[t][2]), b1 = fmaxf(sc[t][1], sc[t][3]);
+        // ---- online softmax: the reference moves, to the block's maximum over the lanes of equal tig, when a score
+        // passes it by more than 2^8 (any reference gives the same quotient): rarely, and only then the lanes are asked
+        const float b0 = fmaxf(sc[t][0], sc[t][2]), b1 = fmaxf(sc[t][1], sc[t][3]);
+        if (__any_sync(kFull, b0 > m[t][0] + kLazy || b1 > m[t][1] + kLazy)) {
+          float n0 = b0, n1 = b1;
 #pragma unroll
-        for (int i = 4; i <= 16; i <<= 1) {
-          b0 = fmaxf(b0, shfl_xor(b0, i));
-          b1 = fmaxf(b1, shfl_xor(b1, i));
-        }
-        const float n0 = fmaxf(m[t][0], b0), n1 = fmaxf(m[t][1], b1);
-        if (__any_sync(kFull, n0 > m[t][0] || n1 > m[t][1])) {
+          for (int i = 4; i <= 16; i <<= 1) {
+            n0 = fmaxf(n0, shfl_xor(n0, i));
+            n1 = fmaxf(n1, shfl_xor(n1, i));
+          }
+          n0 = fmaxf(n0, m[t][0]);
+          n1 = fmaxf(n1, m[t][1]);
           const float a0 = fast_exp2(m[t][0] - n0), a1 = fast_exp2(m[t][1] - n1);  // 2^-inf = 0 at the start
           m[t][0] = n0;
           m[t][1] = n1;
