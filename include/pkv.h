@@ -79,7 +79,8 @@ typedef enum { PKV_OUT_BF16 = 0, PKV_OUT_FP32 = 1 } pkv_out_dtype;
                                             copy: pair skipped */
 #define PKV_DEVFLAG_WAIT_TIMEOUT 0x8u    /* decode, prefill: a pipeline wait hit its iteration limit */
 #define PKV_DEVFLAG_BAD_INDPTR 0x10u     /* prefill, gather: an entry of the row offsets is negative,
-                                            decreasing or past the rows (that sequence is skipped) */
+                                            decreasing or past the rows (that sequence is skipped);
+                                            differential cascade: a member range or a member is wrong */
 
 /*
  * The caller-owned paged pool.  Nothing is copied; the struct is read during the call.
