@@ -92,9 +92,6 @@ struct DiffChunkCfg {
   static constexpr int kFixWarp0 = 12, kFixWarps = 4;
   static constexpr int kThreads = (kFixWarp0 + kFixWarps) * 32;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;  // per thread
-  static constexpr int kSoftRegs = 184;
-  static constexpr int kAuxRegs = (kLaunchRegs * kThreads - kSoftRegs * 256) / (kThreads - 256) / 8 * 8;
-  static_assert(kSoftRegs * 256 + kAuxRegs * (kThreads - 256) <= kLaunchRegs * kThreads, "register split");
   static constexpr float kLazy = 8.f;
   static constexpr float kBias = FP8 ? kPrefillWeightBias : 0.f;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -163,6 +160,11 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
   constexpr int W = kDiffW;
   constexpr bool RECORDS = FORM != kDiffChunk, PREFIX = FORM == kDiffPrefix || FORM == kDiffPrefixFine;
   constexpr bool FINE = FORM == kDiffPrefixFine;  // weights in two terms
+  // registers of a softmax thread (176: spills, the long chunk 2190 us against 2090; weights in two terms want 192:
+  // prefix passes 2 to 4 % faster than with 184), and what that leaves of the launch's for another
+  constexpr int kSoftRegs = FINE ? 192 : 184;
+  constexpr int kAuxRegs = (C::kLaunchRegs * C::kThreads - kSoftRegs * 256) / (C::kThreads - 256) / 8 * 8;
+  static_assert(kSoftRegs * 256 + kAuxRegs * (C::kThreads - 256) <= C::kLaunchRegs * C::kThreads, "register split");
   constexpr bool kQByThreads = FP8 || PREFIX;  // Q written by the softmax threads: converted, or gathered
   constexpr unsigned NS = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
     if (warp == C::kIssuerWarp || warp == C::kIssuer2Warp) {
       // ======================================================================== MMA issuers, one a map
       const int g = warp == C::kIssuerWarp ? 0 : 1;
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ======================================================================== softmax
     const int g = warp >> 2;           // the map
     const int r = threadIdx.x & 127;   // row of the tile, TMEM lane
