@@ -507,8 +507,9 @@ pkv_status pkv_paged_diff_prefill_attention(const pkv_cache_desc* cache, const v
                                             size_t workspace_bytes, pkv_stream_t stream);
 
 /* One token per sequence (pkv_paged_decode_attention, with no CUDA-core form).
- *   The weights enter as a 16-bit hi + lo pair; E4M3 pools: q times a power of two per head, in fp16.  What the pages
- *   hold past a context does not reach the result, NaN and infinities included. */
+ *   The weights enter as a 16-bit hi + lo pair (bf16 pools: to 2^-16 of a weight; E4M3: to 2^-22, or 2^-32 of the row's
+ *   largest weight if that is more); E4M3 pools: q times a power of two per head, in fp16.  What the pages hold past a
+ *   context does not reach the result, NaN and infinities included. */
 size_t pkv_diff_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t max_context_len);
 

@@ -8,7 +8,10 @@
 // query head of the group): a column's query fills its map's half of the 128, the other half is zero, so one
 // product gives the scores of both maps and the second one both outputs from one reading of V.  Groups of up to
 // four heads make 8 columns, an MMA's N; a group of eight makes two tiles of 8, one map each, whose scores need
-// only that map's half of K.  The weights enter as a 16-bit hi + lo pair (about 2^-17).
+// only that map's half of K.  The weights enter as a 16-bit hi + lo pair: bf16, to 2^-16 of a weight; E4M3 pools, fp16
+// times 2^7 (with a score 2^8 past the reference 2^15, and fp16 holds 2^16): to 2^-22, or, below that, 2^-32 of the
+// column's largest weight.  (Without the factor that floor is 2^-25 of the reference, and keys that much behind, all
+// of the output where the largest's value is 0 or the two maps cancel it, are lost.)
 //   E4M3 pools: the codes go from the ring straight into the fragments, expanded to fp16 (exact); q is scaled per
 // column by a power of two into fp16's range; K's scales (one per map) go into the scores' factor, V's into the
 // output.
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
     }
   }
 
-  constexpr float kLazy = 8.f;
+  constexpr float kLazy = 8.f, kBias = FP8 ? 7.f : 0.f;  // weights are taken times 2^kBias: by a lower reference
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -314,18 +317,19 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           sc[t][e] = gid + 8 * (e >> 1) < valid ? sc[t][e] * factor[t][e & 1] : -INFINITY;
-        // ---- online softmax: the reference moves, to the block's maximum over the lanes of equal tig, when a score
-        // passes it by more than 2^8 (any reference gives the same quotient): rarely, and only then the lanes are asked
+        // ---- online softmax: the reference moves, to kBias below the block's maximum over the lanes of equal tig, when a
+        // score passes that by more than 2^8 (any reference gives the same quotient): rarely, and only then the lanes
+        // are asked
         const float b0 = fmaxf(sc[t][0], sc[t][2]), b1 = fmaxf(sc[t][1], sc[t][3]);
-        if (__any_sync(kFull, b0 > m[t][0] + kLazy || b1 > m[t][1] + kLazy)) {
+        if (__any_sync(kFull, b0 > m[t][0] + (kLazy + kBias) || b1 > m[t][1] + (kLazy + kBias))) {
           float n0 = b0, n1 = b1;
 #pragma unroll
           for (int i = 4; i <= 16; i <<= 1) {
             n0 = fmaxf(n0, shfl_xor(n0, i));
             n1 = fmaxf(n1, shfl_xor(n1, i));
           }
-          n0 = fmaxf(n0, m[t][0]);
-          n1 = fmaxf(n1, m[t][1]);
+          n0 = fmaxf(n0 - kBias, m[t][0]);
+          n1 = fmaxf(n1 - kBias, m[t][1]);
           const float a0 = fast_exp2(m[t][0] - n0), a1 = fast_exp2(m[t][1] - n1);  // 2^-inf = 0 at the start
           m[t][0] = n0;
           m[t][1] = n1;

@@ -1,0 +1,127 @@
+"""Differential attention where its numbers are hard to hold, against 64 bits, with bounds made key by key: weights far
+below the largest."""
+import pytest
+import torch
+
+from diff_helpers import compare
+from diff_tight import tight
+from gpu_helpers import split_tokens
+from prompt_helpers import BF16_HALF, FP32_HALF, offsets
+from test_gpu_diff import D, SHAPES, Job, ints
+from test_gpu_wait_timeout import env
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import paged_kv_cache_17_gb300 as m
+
+    return m
+
+
+def halves(dtype):
+    return FP32_HALF if dtype == torch.float32 else BF16_HALF
+
+
+def step(pkv, j, ctx, scale=0.125, split=None, dtype=torch.float32):
+    """One token a sequence, checked; runs of a warp have at most as many additions as blocks, two a block and at least
+    two warps a CTA, and the joins."""
+    out = torch.full((len(ctx), j.q.shape[1] // 2, 2 * D), 7.0, dtype=dtype, device="cuda")
+    with split_tokens(split):
+        pkv.paged_diff_decode_attention(j.q, j.k, j.v, j.tables, ints(ctx), scale, j.lam, out, **j.keys())
+    assert pkv.check_device_status() == 0
+    run = min(max(ctx), split or 512) // 16
+    want, off = tight(j.q, [1] * len(ctx), (j.k, j.v), j.scales, [[(j.tables[i], c)] for i, c in enumerate(ctx)], scale, j.lam,
+                      False, "fp16 pair" if j.e4m3 else "bf16 pair", 2 * (run + 4) + 16 + max(ctx) // 64, out_half=halves(dtype))
+    compare(out, want, off)
+    return out
+
+
+def chunk(pkv, j, lens, ctx, scale=0.125, split=None, causal=True):
+    out = torch.full((sum(lens), j.q.shape[1] // 2, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    with split_tokens(split):
+        pkv.paged_diff_prefill_attention(j.q, ints(offsets(lens)), j.k, j.v, j.tables, ints(ctx), scale, j.lam, out,
+                                         causal=causal, **j.keys())
+    assert pkv.check_device_status() == 0
+    want, off = tight(j.q, lens, (j.k, j.v), j.scales, [[(j.tables[i], c)] for i, c in enumerate(ctx)], scale, j.lam, causal,
+                      "fp16" if j.e4m3 else "bf16", 8 * (max(ctx) // 128 + 2) + 64, j.e4m3, BF16_HALF)
+    compare(out, want, off)
+    return out
+
+
+def shared(pkv, j, prefixes, members, tails, scale=0.125, dtype=torch.float32, run=None):
+    """run: blocks of a run of the prefix pass (a step, 128 keys, is 16 additions to an accumulator where weights have two
+    terms, else 8)."""
+    n, P = len(tails), len(prefixes)
+    front, own = j.tables[:P, : max(1, max(prefixes) // 16)].contiguous(), j.tables[P:].contiguous()
+    of = [-1] * n
+    for p, who in enumerate(members):
+        for i in who:
+            of[i] = p
+    out = torch.full((n, j.q.shape[1] // 2, 2 * D), 7.0, dtype=dtype, device="cuda")
+    with env(**({} if run is None else {"PKV_PREFIX_SPLIT_BLOCKS": str(run)})):
+        pkv.cascade_diff_decode_attention(
+            j.q, j.k, j.v, front, ints(prefixes), ints(offsets([len(w) for w in members])),
+            ints([i for who in members for i in who]), ints(of), own, ints(tails), scale, j.lam, out,
+            max_members=max(map(len, members)), **j.keys())
+    assert pkv.check_device_status() == 0
+    keys = [([(front[of[i]], prefixes[of[i]])] if of[i] >= 0 else []) + [(own[i], t)] for i, t in enumerate(tails)]
+    one = j.e4m3 and dtype == torch.bfloat16
+    steps = min(64, max(prefixes) // 128 + 1)
+    want, off = tight(j.q, [1] * n, (j.k, j.v), j.scales, keys, scale, j.lam, False,
+                      "fp16" if one else "fp16 pair" if j.e4m3 else "bf16 pair", (8 if one else 16) * steps + 128, j.e4m3,
+                      halves(dtype))
+    compare(out, want, off)
+    return out
+
+
+# ------------------------------------------------------------------ weights far below the largest
+
+def sink(j, where, ahead):
+    """The key at each (sequence, position) ahead of all others by `ahead` in both maps, its value 0; the others' scores
+    are small and their values ordinary."""
+    g = torch.Generator().manual_seed(17)
+    j.q = torch.ones_like(j.q)
+    k = torch.zeros(j.k.shape)
+    k[..., 0] = torch.randint(-4, 5, j.k.shape[:-1], generator=g) / 8.0
+    for b, at in where:
+        k[int(j.tables[b, at // 16]), at % 16] = ahead / 8  # (64 elements, scale 1/8)
+        j.v[int(j.tables[b, at // 16]), at % 16] = 0
+    j.k = k.to(j.k.dtype).cuda()
+    if j.e4m3:
+        j.scales = torch.stack((torch.ones_like(j.scales[0]), j.scales[1]))
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("split", [None, 512])
+@pytest.mark.parametrize("ahead", [12, 18])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_step_one_key_far_ahead(pkv, e4m3, ahead, split, hq, hkv):
+    """Ahead by 18 (2^26), the others' weights are below fp16's smallest step, and all of the output."""
+    ctx = [512, 700]
+    j = Job(2, ctx, hq, hkv, e4m3, 3, norm=False, junk=None)
+    sink(j, [(0, 0), (1, 600)], ahead)
+    step(pkv, j, ctx, split=split)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_one_key_far_ahead(pkv, e4m3, dtype):
+    prefixes, members, tails = [512, 256], [[0, 2], [1]], [300, 0, 40, 513]
+    j = Job(4, prefixes + tails, 8, 2, e4m3, 5, norm=False, junk=None)
+    sink(j, [(0, 3), (1, 255), (5, 100)], 18)
+    shared(pkv, j, prefixes, members, tails, dtype=dtype, run=1000)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_one_key_far_ahead(pkv, e4m3):
+    lens, ctx = [40, 3], [512, 300]
+    j = Job(43, ctx, 8, 2, e4m3, 6, norm=False, junk=None)
+    sink(j, [(0, 0), (1, 130)], 18)
+    chunk(pkv, j, lens, ctx)
