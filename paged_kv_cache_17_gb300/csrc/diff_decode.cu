@@ -8,7 +8,9 @@
 // query head of the group): a column's query fills its map's half of the 128, the other half is zero, so one
 // product gives the scores of both maps and the second one both outputs from one reading of V.  Groups of up to
 // four heads make 8 columns, an MMA's N; a group of eight makes two tiles of 8, one map each, whose scores need
-// only that map's half of K.  The weights enter as a 16-bit hi + lo pair: bf16, to 2^-16 of a weight; E4M3 pools, fp16
+// only that map's half of K.  bf16 pools: the halves of K are summed apart, and a column takes its map's sum, because the
+// zeros of the other half would make NaN of an infinite key there (E4M3 has no infinity, and a NaN key of either map
+// is NaN in the output).  The weights enter as a 16-bit hi + lo pair: bf16, to 2^-16 of a weight; E4M3 pools, fp16
 // times 2^7 (with a score 2^8 past the reference 2^15, and fp16 holds 2^16): to 2^-22, or, below that, 2^-32 of the
 // column's largest weight.  (Without the factor that floor is 2^-25 of the reference, and keys that much behind, all
 // of the output where the largest's value is 0 or the two maps cancel it, are lost.)
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
         __syncwarp();
       }
       // ---- scores: rows = tokens gid, gid + 8; columns 2 tig, 2 tig + 1
-      float sc[NT][4] = {};
+      constexpr int kSums = FP8 ? NT : 2;  // of K's halves together, or each
+      float sc[kSums][4] = {};
       uint32_t vr[4][4];  // E4M3: codes 16 gid .. + 15 of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
       if constexpr (FP8) {
         uint4 kr[2][2];  // tokens gid, gid + 8; 16 codes of each half
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           const uint32_t w0 = u4_word(kr[0][kk / 4], kk & 3), w1 = u4_word(kr[1][kk / 4], kk & 3);
-          mma16<FP8>(sc[NT == 2 ? kk / 4 : 0], e4m3_lo(w0), e4m3_lo(w1), e4m3_hi(w0), e4m3_hi(w1), qb[kk][0], qb[kk][1]);
+          mma16<FP8>(sc[kSums == 2 ? kk / 4 : 0], e4m3_lo(w0), e4m3_lo(w1), e4m3_hi(w0), e4m3_hi(w1), qb[kk][0], qb[kk][1]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -308,7 +311,11 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
         for (int kk = 0; kk < KS; ++kk) {
           uint32_t a0, a1, a2, a3;
           ldsm_x4(diff_at(kb, (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a0, a1, a2, a3);
-          mma16<FP8>(sc[NT == 2 ? kk / 4 : 0], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+          mma16<FP8>(sc[kk / 4], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+        }
+        if constexpr (NT == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[0][e] = tig < 2 ? sc[0][e] : sc[1][e];
         }
       }
       uint32_t bh[NT][2], bl[NT][2];

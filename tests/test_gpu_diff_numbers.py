@@ -1,5 +1,7 @@
 """Differential attention where its numbers are hard to hold, against 64 bits, with bounds made key by key: weights far
-below the largest."""
+below the largest, keys that are infinite."""
+import math
+
 import pytest
 import torch
 
@@ -125,3 +127,29 @@ def test_chunk_one_key_far_ahead(pkv, e4m3):
     j = Job(43, ctx, 8, 2, e4m3, 6, norm=False, junk=None)
     sink(j, [(0, 0), (1, 130)], 18)
     chunk(pkv, j, lens, ctx)
+
+
+# ------------------------------------------------------------------ keys that are infinite
+
+def infinite(j, where, t, keys):
+    """Scores of -inf under map t at `keys` of the sequences (rows of the tables): one element of the keys of every pair
+    -inf, of every query positive."""
+    j.q[:, t::2, 5] = j.q[:, t::2, 5].abs() + 0.5
+    for b in where:
+        for at in keys:
+            j.k[int(j.tables[b, at // 16]), at % 16, t::2, 5] = -math.inf
+
+
+INFINITE = [range(0, 1), range(77, 78), range(150, 160)]
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("split", [None, 16, 512])
+@pytest.mark.parametrize("t", [0, 1])
+@pytest.mark.parametrize("keys", INFINITE, ids=str)
+def test_step_infinite_keys(pkv, keys, t, split, hq, hkv):
+    """Keys whose score is -inf under one map have weight 0 there, and theirs under the other."""
+    ctx = [300, 40]
+    j = Job(2, ctx, hq, hkv, False, 4, norm=False)
+    infinite(j, [0], t, keys)
+    assert not step(pkv, j, ctx, split=split).isnan().any()
