@@ -213,10 +213,13 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
   }
 
   constexpr float kLazy = 8.f, kBias = FP8 ? 7.f : 0.f;  // weights are taken times 2^kBias: by a lower reference
+  // The reference before any score, and of scores that are all -inf: the lowest finite value, so that no difference
+  // of references or scores is inf - inf.  (Nothing but such scores: sums of 0, and NaN in the end.)
+  constexpr float kNone = -3.402823466e38f;
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t][0] = m[t][1] = -INFINITY;
+    m[t][0] = m[t][1] = kNone;
     l[t][0] = l[t][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) o[t][mt][0] = o[t][mt][1] = o[t][mt][2] = o[t][mt][3] = 0.f;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
           }
           n0 = fmaxf(n0 - kBias, m[t][0]);
           n1 = fmaxf(n1 - kBias, m[t][1]);
-          const float a0 = fast_exp2(m[t][0] - n0), a1 = fast_exp2(m[t][1] - n1);  // 2^-inf = 0 at the start
+          const float a0 = fast_exp2(m[t][0] - n0), a1 = fast_exp2(m[t][1] - n1);  // 0 at the start
           m[t][0] = n0;
           m[t][1] = n1;
           l[t][0] *= a0;
@@ -439,8 +442,8 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
       float den = 0.f, num[4] = {};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        // (a warp without blocks has maximum -inf and sum 0, and so has one whose scores were all NaN, sum NaN)
-        const float f = ms[w * NC + c] == -INFINITY ? 1.f : fast_exp2(ms[w * NC + c] - top);
+        // (a warp without blocks has reference kNone and sum 0, one whose scores were all NaN kNone and NaN)
+        const float f = fast_exp2(ms[w * NC + c] - top);
         const float4 x = *reinterpret_cast<const float4*>(os + (w * NC + c) * kDiffW + 4 * lane);
         den = fmaf(f, ls[w * NC + c], den);
         num[0] = fmaf(f, x.x, num[0]);
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
 #pragma unroll
         for (int k = 4; k >= 1; k >>= 1) all = fmaxf(all, shfl_xor(all, k));  // (lanes 0-7; the others repeat the last)
         all = __shfl_sync(kFull, all, 0);
-        const float f = own == -INFINITY ? 1.f : fast_exp2(own - all);
+        const float f = fast_exp2(own - all);
         sum *= f;
 #pragma unroll
         for (int k = 4; k >= 1; k >>= 1) sum += shfl_xor(sum, k);
