@@ -480,7 +480,8 @@ pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block
  *     elements apart (0: one row for all tokens); of any sign.
  *   norm_weight: [2 * head_dim] bf16, 16-byte aligned, or NULL.  eps: finite, >= 0.  out_scale: finite.
  *   out: [tokens][num_q_heads / 2][2 * head_dim], contiguous, 16-byte aligned; it must not overlap the inputs
- *     (with q refused).  A row that sees no key is 0.
+ *     (with q refused).  A row that sees no key is 0; one whose scores are all -inf under a map (infinite keys) is NaN,
+ *     as 0 / 0 is, and a score of -inf beside others has weight 0.
  *   head_dim must be 64, num_q_heads and num_kv_heads even.
  * Everything else is as for the plain call of the same form.  Statistics, the difference and the norm are held
  * in fp32 and rounded once, to out's type.

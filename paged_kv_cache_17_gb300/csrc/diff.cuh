@@ -15,6 +15,9 @@ namespace pkv {
 constexpr int kDiffD = 64;            // elements of a head
 constexpr int kDiffW = 2 * kDiffD;    // of a pair's value
 constexpr int kDiffCluster = 8;       // the largest cluster that every launch may ask for
+// The reference of keys that have no score above -inf: the lowest finite value, so that no difference of references
+// or scores is inf - inf.  With the sum 0 beside it, such a row is 0 / 0; a row, or a run, without keys has -inf
+constexpr float kDiffNothing = -3.402823466e38f;
 
 struct DiffParams {
   const uint16_t* q;        // [rows][2 heads][64] bf16, rows q_stride apart

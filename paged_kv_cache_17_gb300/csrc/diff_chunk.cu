@@ -966,7 +966,9 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       };
       if constexpr (RECORDS) {
         if (!dead && !idle) {
-          if (rv) p.part_ml[rec] = make_float2(m_used - C::kBias, l);
+          // (keys, but none of a score above -inf: kDiffNothing, not the -inf of a run without keys)
+          const bool nothing = l == 0.f && my_lim > st.k0 * C::kKeys;
+          if (rv) p.part_ml[rec] = make_float2(nothing ? kDiffNothing : m_used - C::kBias, l);
           __syncwarp();
           add_odd(g, 0, W);
           // turned, through the columns that are read, so that four lanes store 64 bytes of a row together (lanes
@@ -1003,10 +1005,9 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
         }
       } else {
         // this map's factor; then each group has both outputs' 64 columns of one value head
-        float a = 0.f;  // of a row without keys
-        if (rv && (l > 0.f || l != l)) a = sign / l;
-        join[g * 128 + r] = a;
-        const bool empty = l == 0.f;  // (of both maps alike: they see the same keys)
+        // (a row without keys: 0; one of nothing but scores of -inf under this map: 0 / 0)
+        const bool empty = !rv || my_lim <= 0;
+        join[g * 128 + r] = empty ? 0.f : sign / l;
         tc_fence_before();
         __syncwarp();
         dead = named_sync_or(2, 256, dead);

@@ -213,13 +213,10 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
   }
 
   constexpr float kLazy = 8.f, kBias = FP8 ? 7.f : 0.f;  // weights are taken times 2^kBias: by a lower reference
-  // The reference before any score, and of scores that are all -inf: the lowest finite value, so that no difference
-  // of references or scores is inf - inf.  (Nothing but such scores: sums of 0, and NaN in the end.)
-  constexpr float kNone = -3.402823466e38f;
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t][0] = m[t][1] = kNone;
+    m[t][0] = m[t][1] = kDiffNothing;
     l[t][0] = l[t][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) o[t][mt][0] = o[t][mt][1] = o[t][mt][2] = o[t][mt][3] = 0.f;
@@ -442,7 +439,7 @@ __global__ void __launch_bounds__((DiffDecodeCfg<NT, FP8, CLUSTER>::kThreads))
       float den = 0.f, num[4] = {};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        // (a warp without blocks has reference kNone and sum 0, one whose scores were all NaN kNone and NaN)
+        // (a warp without blocks has reference kDiffNothing and sum 0, one whose scores were all NaN kDiffNothing and NaN)
         const float f = fast_exp2(ms[w * NC + c] - top);
         const float4 x = *reinterpret_cast<const float4*>(os + (w * NC + c) * kDiffW + 4 * lane);
         den = fmaf(f, ls[w * NC + c], den);

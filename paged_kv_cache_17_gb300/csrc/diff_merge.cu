@@ -73,8 +73,11 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const DiffParams p) {
     for (int u = 0; u < kBatch; ++u)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (ml[u][m].y == 0.f) continue;  // an empty record has no output part
         const float n = fmaxf(top[m], ml[u][m].x);
+        if (ml[u][m].y == 0.f) {  // no output part: a record of no keys, or of none but scores of -inf (kDiffNothing)
+          top[m] = n;
+          continue;
+        }
         // (a record whose first scores held a NaN has reference -inf and a sum that is NaN)
         const float a = top[m] == -INFINITY ? 0.f : fast_exp2(top[m] - n);
         const float f = ml[u][m].x == -INFINITY ? 1.f : fast_exp2(ml[u][m].x - n);
@@ -86,6 +89,7 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const DiffParams p) {
         num[m][3] = fmaf(f, v[u][m].w, num[m][3] * a);
       }
   }
+  bool no_keys = top[0] == -INFINITY;  // (both maps see the same keys)
   if constexpr (W > 1) {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -99,6 +103,7 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const DiffParams p) {
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < W; ++w) M = fmaxf(M, mls[warp + w][m].x);
+      no_keys = M == -INFINITY;
       den[m] = num[m][0] = num[m][1] = num[m][2] = num[m][3] = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(256) diff_merge_kernel(const DiffParams p) {
   }
   if (!mine) return;
   const float vs = FP8 ? p.scales[2 * (p.pairs + head / p.group) + lane / 16] : 1.f;
-  const bool none = den[0] == 0.f && den[1] == 0.f;
+  const bool none = den[0] == 0.f && den[1] == 0.f && no_keys;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const float by = vs / den[m];

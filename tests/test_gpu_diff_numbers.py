@@ -32,8 +32,8 @@ def halves(dtype):
 
 
 def step(pkv, j, ctx, scale=0.125, split=None, dtype=torch.float32):
-    """One token a sequence, checked; runs of a warp have at most as many additions as blocks, two a block and at least
-    two warps a CTA, and the joins."""
+    """One token a sequence, checked.  Additions to a warp's accumulator: two a block of a run, of which it has half at
+    most; then the joins of warps and runs."""
     out = torch.full((len(ctx), j.q.shape[1] // 2, 2 * D), 7.0, dtype=dtype, device="cuda")
     with split_tokens(split):
         pkv.paged_diff_decode_attention(j.q, j.k, j.v, j.tables, ints(ctx), scale, j.lam, out, **j.keys())
@@ -131,27 +131,60 @@ def test_chunk_one_key_far_ahead(pkv, e4m3):
 
 # ------------------------------------------------------------------ keys that are infinite
 
-def infinite(j, where, t, keys):
-    """Scores of -inf under map t at `keys` of the sequences (rows of the tables): one element of the keys of every pair
-    -inf, of every query positive."""
-    j.q[:, t::2, 5] = j.q[:, t::2, 5].abs() + 0.5
-    for b in where:
+def infinite(j, maps, keys):
+    """Scores of -inf under the maps at `keys` of the first sequence: one element of the keys of every pair -inf, of
+    every query positive."""
+    for t in maps:
+        j.q[:, t::2, 5] = j.q[:, t::2, 5].abs() + 0.5
         for at in keys:
-            j.k[int(j.tables[b, at // 16]), at % 16, t::2, 5] = -math.inf
+            j.k[int(j.tables[0, at // 16]), at % 16, t::2, 5] = -math.inf
 
 
+MAPS = [(0,), (1,), (0, 1)]
 INFINITE = [range(0, 1), range(77, 78), range(0, 200), range(150, 160), range(0, 300)]
 
 
 @pytest.mark.parametrize("hq,hkv", SHAPES)
 @pytest.mark.parametrize("split", [None, 16, 512])
-@pytest.mark.parametrize("t", [0, 1])
+@pytest.mark.parametrize("maps", MAPS)
 @pytest.mark.parametrize("keys", INFINITE, ids=str)
-def test_step_infinite_keys(pkv, keys, t, split, hq, hkv):
+def test_step_infinite_keys(pkv, keys, maps, split, hq, hkv):
     """Keys whose score is -inf under one map have weight 0 there, the first ones of a warp too, and theirs under the other;
     a row of nothing but such scores has no value."""
     ctx = [300, 40]
     j = Job(2, ctx, hq, hkv, False, 4, norm=False)
-    infinite(j, [0], t, keys)
+    infinite(j, maps, keys)
     out = step(pkv, j, ctx, split=split)
     assert bool(out[0].isnan().all()) == (len(keys) == 300) and not out[1].isnan().any()
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("split", [None, 128])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("maps", MAPS)
+@pytest.mark.parametrize("keys", INFINITE, ids=str)
+def test_chunk_infinite_keys(pkv, keys, maps, norm, split, hq, hkv):
+    """(A row sees some of the keys: only the ones that see no other have no value.)"""
+    lens, ctx = [290, 3], [300, 40]
+    j = Job(293, ctx, hq, hkv, False, 4, norm=False)
+    infinite(j, maps, keys)
+    out = chunk(pkv, j, lens, ctx, split=split)
+    if norm:  # NaN where there is none without it, in the whole row
+        j.w = torch.ones(2 * D, dtype=torch.bfloat16, device="cuda")
+        with split_tokens(split):
+            got = pkv.paged_diff_prefill_attention(j.q, ints(offsets(lens)), j.k, j.v, j.tables, ints(ctx), 0.125, j.lam,
+                                                   **j.keys())
+        assert torch.equal(got.isnan(), out.isnan())
+
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("maps", MAPS)
+@pytest.mark.parametrize("keys", [range(0, 1), range(0, 200), range(0, 256)], ids=str)
+def test_shared_infinite_keys(pkv, keys, maps, hq, hkv):
+    """In a prefix; a member without other keys sees nothing else, one with some does."""
+    prefixes, members, tails = [256, 16], [[0, 2], [1]], [300, 9, 0, 64, 0]
+    j = Job(5, prefixes + tails, hq, hkv, False, 7, norm=False)
+    infinite(j, maps, keys)
+    out = shared(pkv, j, prefixes, members, tails)
+    assert bool(out[2].isnan().all()) == (len(keys) == 256) and not out[[0, 1, 3, 4]].isnan().any()
+    assert not out[4].any()
