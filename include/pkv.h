@@ -292,6 +292,8 @@ typedef struct {
   const int32_t* seq_prefix;     /* [batch]: p for a member of prefix p, else -1; every
                                     sequence belongs to at most one prefix and must appear
                                     in that prefix's member list */
+  int32_t num_member_seqs;       /* entries of member_seqs, or 0: not told.  The differential call
+                                    flags a range past them and does not read it */
 } pkv_prefix_desc;
 
 size_t pkv_cascade_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -522,9 +524,9 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
 
 /* One token per sequence, prefixes shared (pkv_cascade_decode_attention).
  *   The prefix part's weights enter as a 16-bit hi + lo pair too, but for an E4M3 pool with a bf16 output: rounded to
- *   fp16.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong or longer than
- *   max_members, or a member outside the batch, sets PKV_DEVFLAG_BAD_INDPTR: the results of the sequences that it
- *   would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the blocks per run of
+ *   fp16.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong, past the batch or
+ *   num_member_seqs, or longer than max_members, or a member outside the batch, sets PKV_DEVFLAG_BAD_INDPTR: the results
+ *   of the sequences that it would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the blocks per run of
  *   the prefix part (rounded up to a multiple of 8, at most 512). */
 size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t max_context_len, int32_t num_prefixes, int32_t max_members,

@@ -70,7 +70,7 @@ class PrefixDesc(ctypes.Structure):
                 ("prefix_lens", ctypes.c_void_p), ("num_prefixes", ctypes.c_int32),
                 ("member_indptr", ctypes.c_void_p), ("member_seqs", ctypes.c_void_p),
                 ("max_members", ctypes.c_int32), ("max_prefix_len", ctypes.c_int32),
-                ("seq_prefix", ctypes.c_void_p)]
+                ("seq_prefix", ctypes.c_void_p), ("num_member_seqs", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:

@@ -47,7 +47,7 @@ struct DiffParams {
   float score_scale;        // softmax_scale * log2(e)
   // chunks and prefix passes (diff_chunk.cu)
   const int32_t* member_seqs;  // prefix pass: rows of the members, q_indptr their ranges; max_members of one prefix
-  int max_members;
+  int max_members, num_members;  // num_members: entries of member_seqs at most
   int split_tiles;          // 128-key steps of a slot
   int negate;               // softmax_scale is negative
   float score_size;         // |softmax_scale| * log2(e), positive

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, log_g = 31 - __clz(G);  // a power of two
   const int cta_tok = C::kRows >> log_g;         // tokens of a work
+  const int ranges_end = PREFIX ? p.num_members : p.rows;  // where the ranges of q_indptr end at most
 
   if (warp == 0) {
     __syncwarp();
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
             const int last = p.q_indptr[b + 1];
             len = p.context_lens[b];
             n = last - first;
-            if (first < 0 || last < first || last > p.rows || (PREFIX && n > p.max_members)) {
+            if (first < 0 || last < first || last > ranges_end || (PREFIX && n > p.max_members)) {
               set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
               n = 0;
             }
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
       // start may be cancelled, the first one's too
       for (int b = lane; b < p.batch; b += 32) {
         const int first = p.q_indptr[b], last = p.q_indptr[b + 1];
-        if (first < 0 || last < first || last > p.rows || (PREFIX && last - first > p.max_members))
+        if (first < 0 || last < first || last > ranges_end || (PREFIX && last - first > p.max_members))
           set_flag(p.status, PKV_DEVFLAG_BAD_INDPTR);
       }
     } else if (warp >= C::kFixWarp0) {

@@ -1733,6 +1733,7 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
   if (!aligned(px->prefix_tables, 4) || !aligned(px->prefix_lens, 4) || !aligned(px->member_indptr, 4) ||
       !aligned(px->member_seqs, 4) || !aligned(px->seq_prefix, 4))
     return fail(PKV_ERR_INVALID_ARG, "prefix arrays must be 4-byte aligned");
+  if (px->num_member_seqs < 0) return fail(PKV_ERR_INVALID_ARG, "num_member_seqs must be non-negative");
   if (px->max_prefix_len % 16 != 0) return fail(PKV_ERR_INVALID_ARG, "max_prefix_len must be a multiple of 16");
   if (px->max_prefix_len > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "max_prefix_len above 2^30");
   if (static_cast<int64_t>(px->max_prefix_blocks) * 16 < px->max_prefix_len)
@@ -1759,6 +1760,7 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
   pass.q_indptr = px->member_indptr;
   pass.member_seqs = px->member_seqs;
   pass.max_members = px->max_members;
+  pass.num_members = px->num_member_seqs > 0 ? std::min(px->num_member_seqs, batch) : batch;
   pass.block_tables = px->prefix_tables;
   pass.max_blocks = px->max_prefix_blocks;
   pass.context_lens = px->prefix_lens;

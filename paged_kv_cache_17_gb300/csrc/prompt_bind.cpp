@@ -430,6 +430,7 @@ PyObject* diff_cascade(PyObject* const* a) {
   const at::Tensor& seqs = needed(a[6], "member_seqs", dev);
   x.member_seqs = vector<const int32_t>(&seqs, "member_seqs", at::kInt, seqs.dim() == 1 ? seqs.size(0) : 0);
   x.seq_prefix = vector<const int32_t>(&needed(a[7], "seq_prefix", dev), "seq_prefix", at::kInt, s.batch);
+  x.num_member_seqs = static_cast<int32_t>(std::min<int64_t>(seqs.numel(), INT32_MAX));
   x.max_members = seqs.numel() > 0 ? int32(a[16], "max_members") : 0;
   const int64_t most = static_cast<int64_t>(x.max_prefix_blocks) * cache.block_size;
   x.max_prefix_len =
