@@ -1487,11 +1487,15 @@ DiffChunkPlan plan_diff_chunk(int batch, int total_q, int hq, int hkv, bool fp8,
   return c;
 }
 
-// Shared prefixes: a prefix's members are the rows of its tiles.  At most 64 steps a run (8192 keys), so that truncated
-// sums stay within 2^-14.  256 sequences over 2048 tokens: one run of 16 steps 83 us in all (cold), two 95, four 121;
-// sixteen prompts of 2000, eight sequences each, E4M3: 55, 59, 72; two of 784, three each: seven runs of one step 17, four
-// 18, two 22.
-constexpr double kDiffPrefixStepUs = 1.5;  // (2.3 with two-term weights; the runs that it leads to are the best either way)
+// Shared prefixes: a prefix's members are the rows of its tiles.  At most 64 steps a run (8192 keys): each step adds to an
+// accumulator 8 times, 16 where weights have two terms, so truncated sums stay within 2^-14 or 2^-13 (values of one sign,
+// even weights, two terms: 4.5e-5 at 64 steps, 1.9e-5 at 32, 3.3e-6 at 8).  256 sequences over 2048 tokens: one run of 16
+// steps 83 us in all (cold), two 95, four 121; sixteen prompts of 2000, eight sequences each, E4M3: 55, 59, 72; two of
+// 784, three each: seven runs of one step 17, four 18, two 22.
+// The model's step is that of one term; with two a step takes 2.3 us, and runs are then not always the best.  bf16 pools,
+// 64 + 16 heads, runs of 32 / 64 steps / planned: 256 over 8192 tokens 84 / 139 / 94 us, 16 x 32 over 8192 168 / 157 / 168,
+// 32 x 32 319 / 308 / 308, 4 x 64 over 32,768 291 / 268 / 272.
+constexpr double kDiffPrefixStepUs = 1.5;
 constexpr int kDiffPrefixMaxRun = 64;
 
 struct DiffPrefixPlan {

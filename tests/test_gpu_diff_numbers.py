@@ -1,5 +1,5 @@
 """Differential attention where its numbers are hard to hold, against 64 bits, with bounds made key by key: weights far
-below the largest, keys that are infinite."""
+below the largest, weights in two 16-bit terms, keys that are infinite, long runs of a shared prefix."""
 import math
 
 import pytest
@@ -9,7 +9,7 @@ from diff_helpers import compare
 from diff_tight import tight
 from gpu_helpers import split_tokens
 from prompt_helpers import BF16_HALF, FP32_HALF, offsets
-from test_gpu_diff import D, SHAPES, Job, ints
+from test_gpu_diff import D, SHAPES, Job, grow, ints
 from test_gpu_wait_timeout import env
 
 pytestmark = pytest.mark.gpu
@@ -188,3 +188,53 @@ def test_shared_infinite_keys(pkv, keys, maps, hq, hkv):
     out = shared(pkv, j, prefixes, members, tails)
     assert bool(out[2].isnan().all()) == (len(keys) == 256) and not out[[0, 1, 3, 4]].isnan().any()
     assert not out[4].any()
+
+
+# ------------------------------------------------------------------ two terms
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+def test_weights_in_two_terms(pkv, hq, hkv, e4m3):
+    """Few keys and small scores: an fp32 output shows each weight's bits."""
+    ctx = [2, 3, 5, 4, 17]
+    step(pkv, Job(5, ctx, hq, hkv, e4m3, 8, norm=False), ctx, scale=0.01)
+    j = Job(3, [16, 32, 3, 0, 2], hq, hkv, e4m3, 9, norm=False)
+    shared(pkv, j, [16, 32], [[0, 1], [2]], [3, 0, 2], scale=0.01)
+
+
+# ------------------------------------------------------------------ long runs of a prefix
+
+@pytest.mark.parametrize("run", [None, 8, 40, 128, 1000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (8, 2), (16, 2)])
+def test_shared_long_runs(pkv, hq, hkv, e4m3, dtype, run):
+    """Runs of 1, 5, 16 and, at 8192 tokens, as many steps as a run may have."""
+    prefixes, members, tails = [2000, 8192, 336], [[4, 0], [2, 5, 3], [6]], [5, 300, 0, 17, 64, 1, 700]
+    j = Job(7, prefixes + tails, hq, hkv, e4m3, 11, norm=False, per_token=True)
+    shared(pkv, j, prefixes, members, tails, dtype=dtype, run=run)
+
+
+@pytest.mark.parametrize("run", [None, 1000])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_values_of_one_sign(pkv, e4m3, run):
+    """Where truncated sums are all off to the same side."""
+    prefixes, members, tails = [8192], [[0, 1]], [0, 40]
+    j = Job(2, prefixes + tails, 8, 2, e4m3, 12, norm=False)
+    if e4m3:
+        j.v = (j.v.view(torch.uint8) & 0x7F).view(torch.float8_e4m3fn)
+    else:
+        j.v = j.v.abs()
+    j.lam = -j.lam.abs()
+    shared(pkv, j, prefixes, members, tails, scale=0.01, run=run)
+
+
+@pytest.mark.parametrize("run", [None, 40, 1000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_growing_scores(pkv, e4m3, dtype, run):
+    """The reference moves again and again, and the outputs are rescaled."""
+    prefixes, tails = [2000], [30, 0, 1]
+    j = Job(3, prefixes + tails, 8, 2, e4m3, 13, norm=False)
+    grow(j, prefixes + tails)
+    shared(pkv, j, prefixes, [[0, 2]], tails, scale=0.05, dtype=dtype, run=run)
