@@ -485,6 +485,9 @@ pkv_status pkv_paged_kv_gather(const pkv_cache_desc* cache, const int32_t* block
  *     (with q refused).  A row that sees no key is 0; one whose scores are all -inf under a map (infinite keys) is NaN,
  *     as 0 / 0 is, and a score of -inf beside others has weight 0.
  *   head_dim must be 64, num_q_heads and num_kv_heads even.
+ *   A value of V that is not finite, at a position that a row sees, makes its element of that row's output (with the norm
+ *   the whole row) NaN or infinite: an infinity may come out as either, since weights in two terms and weights that
+ *   are 0 in fp32 make NaN of it.  Nothing else is touched by it.
  * Everything else is as for the plain call of the same form.  Statistics, the difference and the norm are held
  * in fp32 and rounded once, to out's type.
  */

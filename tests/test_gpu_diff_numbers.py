@@ -1,5 +1,5 @@
 """Differential attention where its numbers are hard to hold, against 64 bits, with bounds made key by key: weights far
-below the largest, weights in two 16-bit terms, keys that are infinite, long runs of a shared prefix."""
+below the largest, weights in two 16-bit terms, keys and values that are not finite, long runs of a shared prefix."""
 import math
 
 import pytest
@@ -238,3 +238,57 @@ def test_shared_growing_scores(pkv, e4m3, dtype, run):
     j = Job(3, prefixes + tails, 8, 2, e4m3, 13, norm=False)
     grow(j, prefixes + tails)
     shared(pkv, j, prefixes, [[0, 2]], tails, scale=0.05, dtype=dtype, run=run)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("hq,hkv", SHAPES)
+@pytest.mark.parametrize("kind,e4m3", [("nan", False), ("inf", False), ("nan", True)])  # (E4M3 has no infinity)
+def test_one_token_values_not_finite(pkv, kind, e4m3, hq, hkv):
+    """A value inside a context that is not finite makes its own element, of its own kv pair's heads, of the sequences
+    that see it, infinite or NaN (with the norm their whole rows), and nothing else."""
+
+    def spoil(j, row, at, head, e):
+        blk = int(j.tables[row, at // 16])
+        if e4m3:
+            j.v.view(torch.uint8)[blk, at % 16, head, e] = 0x7F
+        else:
+            j.v[blk, at % 16, head, e] = math.nan if kind == "nan" else math.inf
+
+    head = hkv - 1  # the last pair's second half
+    heads = slice(hq // 2 - hq // hkv, hq // 2)
+    touched = torch.zeros((4, hq // 2, 2 * D), dtype=torch.bool, device="cuda")
+    touched[1, heads, D + 9] = True
+    ctx = [40, 300, 17, 0]
+    for norm in (False, True):
+        j = Job(4, ctx, hq, hkv, e4m3, 14, norm=norm)
+
+        def run():
+            return pkv.paged_diff_decode_attention(j.q, j.k, j.v, j.tables, ints(ctx), 0.125, j.lam, **j.keys())
+
+        clean = run()
+        spoil(j, 1, 123, head, 9)
+        got = run()
+        where = touched.any(-1, keepdim=True).expand_as(touched) if norm else touched
+        assert torch.equal(~torch.isfinite(got), where)
+        assert torch.equal(got[~where], clean[~where])
+    # in a prefix: of all its members
+    prefixes, tails = [336, 32], [9, 0, 700, 64]
+    touched.zero_()
+    touched[[0, 2], heads, D + 9] = True
+    for norm in (False, True):
+        j = Job(4, prefixes + tails, hq, hkv, e4m3, 15, norm=norm)
+        front, own = j.tables[:2, :21].contiguous(), j.tables[2:].contiguous()
+
+        def run():
+            return pkv.cascade_diff_decode_attention(j.q, j.k, j.v, front, ints(prefixes), ints([0, 2, 3]), ints([2, 0, 3]),
+                                                     ints([0, -1, 0, 1]), own, ints(tails), 0.125, j.lam, max_members=2,
+                                                     **j.keys())
+
+        clean = run()
+        spoil(j, 0, 123, head, 9)
+        got = run()
+        where = touched.any(-1, keepdim=True).expand_as(touched) if norm else touched
+        assert torch.equal(~torch.isfinite(got), where)
+        assert torch.equal(got[~where], clean[~where])
+    assert pkv.check_device_status() == 0
