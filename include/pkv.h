@@ -173,7 +173,8 @@ int32_t pkv_decode_partition_tokens(int32_t batch, int32_t num_kv_heads, int32_t
  *   Arithmetic: the per-block products run on the tensor cores with fp32 accumulation; K
  *   and V enter as stored (bf16, or E4M3 expanded exactly to fp16); q enters as bf16, or
  *   for E4M3 pools times a per-head power of two rounded to fp16 (relative error at most
- *   2^-11); the softmax weights enter as a 16-bit hi + lo pair.  While the environment
+ *   2^-11); the softmax weights enter as a 16-bit hi + lo pair (bf16 pools: to 2^-16 of a
+ *   weight; E4M3: to 2^-22, or 2^-40 of the largest if that is more).  While the environment
  *   variable PKV_DECODE_CUDA_CORES is "1" (read at each call), every product runs in fp32
  *   on the CUDA cores instead.  PKV_SPLIT_TOKENS (a positive multiple of 16, read at each
  *   call and by pkv_decode_workspace_size) fixes the partition length (tuning; the

@@ -30,6 +30,9 @@
 // before the expansion; the output rows come back with the same map.  The products run in
 // fp16 -- q scaled per head by a power of two into fp16's range (the factor is folded into
 // that head's score scale), the K scale into the score scale, the V scale into the output.
+// The weights are 2^15 for the largest score (fp16 holds up to 2^16): two fp16 terms are then good
+// to 2^-22 of a weight, or 2^-40 of the largest where that is more; without the factor the floor is
+// 2^-25, and keys that much behind the largest would be lost from the output.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__((NWC + 1) * 32)
     __syncwarp();
   }
 
-  // per thread: heads 2tig, 2tig+1 of the group (running max, this thread's share of the
+  // per thread: heads 2tig, 2tig+1 of the group (running reference, this thread's share of the
   // running sum) and O^T fragments: o[mt] = dims 16mt + gid (+8) x heads 2tig, 2tig+1
   float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
   float o[MT][4];
@@ -373,7 +376,9 @@ __global__ void __launch_bounds__((NWC + 1) * 32)
         bm0 = fmaxf(bm0, shfl_xor(bm0, m));
         bm1 = fmaxf(bm1, shfl_xor(bm1, m));
       }
-      const float mn0 = fmaxf(mrun[0], bm0), mn1 = fmaxf(mrun[1], bm1);
+      // (the reference: the maximum, or kBias below it; any gives the same quotient)
+      constexpr float kBias = FP8 ? 15.f : 0.f;
+      const float mn0 = fmaxf(mrun[0], bm0 - kBias), mn1 = fmaxf(mrun[1], bm1 - kBias);
       const bool moved = __any_sync(kFull, (mn0 > mrun[0]) || (mn1 > mrun[1]));
       if (moved) {
         const float al0 = fast_exp2(mrun[0] - mn0), al1 = fast_exp2(mrun[1] - mn1);  // 2^-inf = 0 at start
