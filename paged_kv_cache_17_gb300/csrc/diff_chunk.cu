@@ -39,9 +39,9 @@
 // chain of a map, scores -> weights -> products, is 1250 cycles of softmax (220 to load the scores, 650 for the
 // first 32 weights beside the maximum, 380 to the first half's arrival) and about 1000 from there to the next
 // scores, and the other map covers as much of it as the turns allow.  Exponentials left out: 6 % less; softmax left
-// out: 1.65 ms of 2.09, the measured cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.1 ms = 1.47
-// PFLOP/s, 78 % of the measured burst rate and 86 % of the sustained one (the power limit holds the clock at 1.9
-// GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96 PFLOP/s: 6.4 steps a work, and 6000 cycles of start,
+// out: 1.65 ms of 2.09, the measured cuBLAS rate.  4096 tokens over 32,768, 64 + 16 heads, bf16: 2.11 to 2.14 ms =
+// 1.45 PFLOP/s, 76 % of the measured burst rate and 84 % of the sustained one (the power limit holds the clock at
+// 1.9 GHz).  Nine prompts of 257 to 2048 tokens: 202 us = 0.96 PFLOP/s: 6.4 steps a work, and 6000 cycles of start,
 // join, norm and store.  24 x 3 to 8 tokens over 1800 to 12,000, split: 136 us, 67 % of the copy rate: a step's
 // chain takes as long for 32 rows as for 128.  E4M3, 4 x 700 to 1100 over 3000 to 9000, 128 + 16 heads: 0.90 ms =
 // 1.2 PFLOP/s.  A prefix of 2048 tokens for 256 sequences: 42 us alone, 16 steps (29 us with one weight term).
@@ -1072,9 +1072,8 @@ __global__ void __launch_bounds__((DiffChunkCfg<FP8>::kThreads), 1)
             const int rr = (r & ~31) + 8 * k + (lane >> 2);
             const int i = rr >> log_g;
             const uint32_t* x = v[k >> 1] + (k & 1);
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                  (static_cast<int64_t>(w.tok0 + i) * p.heads + w.h * G + (rr & (G - 1))) * W) +
-                         8 * g + (lane & 3);
+            const int64_t to = static_cast<int64_t>(w.tok0 + i) * p.heads + w.h * G + (rr & (G - 1));
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to * W) + 8 * g + (lane & 3);
             if (i < w.ntok) {
               dst[0] = make_uint4(x[0], x[2], x[4], x[6]);
               dst[4] = make_uint4(x[8], x[10], x[12], x[14]);

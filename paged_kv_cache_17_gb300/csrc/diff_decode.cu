@@ -25,12 +25,13 @@
 // read each other's states through distributed shared memory and end the rows themselves, without a second kernel.
 //
 // What bounds it.  Reading K and V once, for bf16 pools: 64 requests of 512 to 4096 tokens, 64 + 16 heads: 97 us = 6.2
-// TB/s of all bytes, 91 % of the measured copy; 8 of 32 to 128 thousand, 128 + 16 heads: 374 us = 6.55 TB/s, 97 % (three
-// consumer warps and a 48 KiB ring for two tiles; two and 32 KiB: 395).  E4M3, 33 of 1000 to 9001, 16 heads of their own: 68
-// us = 5.0 TB/s (71 with a maximum over the lanes for every block; 128 heads: 90, 100): some 360 instructions a block from
-// two warps a CTA, half of the issue slots, and a wave of uneven CTAs (an SM is busy 80 % of the time); two blocks at a
-// time in a warp, or the next block's scores under this one's softmax, need more than the 96 registers that let six CTAs
-// share an SM (79, 91), four warps a CTA the same; 80 registers for eight CTAs spill (81).  One request of 777 tokens: 7.2 us in a graph, launch and five dependent round trips.
+// TB/s of all bytes, 91 % of the measured copy; 8 of 32 to 128 thousand, 128 + 16 heads: 374 us = 6.55 TB/s, 97 %
+// (three consumer warps and a 48 KiB ring for two tiles; two and 32 KiB: 395).  E4M3, 33 of 1000 to 9001, 16 heads of
+// their own: 68 us = 5.0 TB/s (71 with a maximum over the lanes for every block; 128 heads: 90, 100): some 360
+// instructions a block from two warps a CTA, half of the issue slots, and a wave of uneven CTAs (an SM is busy 80 % of
+// the time); two blocks at a time in a warp, or the next block's scores under this one's softmax, need more than the
+// 96 registers that let six CTAs share an SM (79, 91), four warps a CTA the same; 80 registers for eight CTAs spill
+// (81).  One request of 777 tokens: 7.2 us in a graph, launch and five dependent round trips.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -1388,7 +1388,8 @@ DiffSplit choose_diff_split(int batch, int pairs, int max_context_len, bool reco
     const bool cluster =
         !records && eighth <= want + 8 && static_cast<long long>(batch) * pairs * std::min(blocks, 8LL) <= 3LL * sm_count;
     s.split.split_blocks =
-        static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks, cluster ? std::max(want, eighth) : (want + 3) / 4 * 4}));
+        static_cast<int>(std::min<long long>({blocks, kMinSplitBlocks,
+                                              cluster ? std::max(want, eighth) : (want + 3) / 4 * 4}));
     s.split.max_splits = static_cast<int>((blocks + s.split.split_blocks - 1) / s.split.split_blocks);
     s.cluster = cluster && s.split.max_splits > 1 && s.split.max_splits <= pkv::kDiffCluster;
   }
@@ -1778,10 +1779,11 @@ pkv_status pkv_cascade_diff_decode_attention(const pkv_cache_desc* cache, const 
       (fp8 && !encode_kv_map(&pass_v, cache->v_cache, cache->num_blocks, hkv / 2, pkv::kDiffW, true)))
     return fail(PKV_ERR_INVALID_ARG, "cannot describe the KV pool as a TMA tensor map");
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  // One term of a weight, fp16, is far below a bf16 output's rounding; one bf16 term is as large as it (256 sequences over
-  // one prompt: 67 us against 69, error 0.0025 against 0.0017)
+  // One term of a weight, fp16, is far below a bf16 output's rounding; one bf16 term is as large as it (256 sequences
+  // over one prompt: 67 us against 69, error 0.0025 against 0.0017)
   const bool fine = !fp8 || p.out_fp32;
-  cudaError_t e = pkv::launch_diff_chunk(fp8, fine ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, tk, fp8 ? pass_v : tv, pass, x.tile_slots, x.runs.splits, cs);
+  cudaError_t e = pkv::launch_diff_chunk(fp8, fine ? pkv::kDiffPrefixFine : pkv::kDiffPrefix, none, tk,
+                                         fp8 ? pass_v : tv, pass, x.tile_slots, x.runs.splits, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential prefix-pass launch");
   e = pkv::launch_diff_decode(fp8, tk, tv, p, cs);
   if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
