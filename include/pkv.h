@@ -530,8 +530,8 @@ pkv_status pkv_paged_diff_decode_attention(const pkv_cache_desc* cache, const vo
  *   The prefix part's weights enter as a 16-bit hi + lo pair too, but for an E4M3 pool with a bf16 output: rounded to
  *   fp16.  member_seqs has member_indptr[num_prefixes] entries.  A member range that is wrong, past the batch or
  *   num_member_seqs, or longer than max_members, or a member outside the batch, sets PKV_DEVFLAG_BAD_INDPTR: the results
- *   of the sequences that it would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the blocks per run of
- *   the prefix part (rounded up to a multiple of 8, at most 512). */
+ *   of the sequences that it would have served are unspecified, the others' are right.  PKV_PREFIX_SPLIT_BLOCKS fixes the
+ *   blocks per run of the prefix part (rounded up to a multiple of 8, at most 512). */
 size_t pkv_cascade_diff_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t max_context_len, int32_t num_prefixes, int32_t max_members,
                                        int32_t max_prefix_len);
